@@ -46,11 +46,11 @@ def listed():
         # four layers, fp16, clipped
         _step("step32 4 layers", "fp32", LAYERS4, "fp16", "fp16", clip=1.0),
         # the same range with states in 8 bits
-        _step("step8 few small", "e4m3", "4096*2,64,1", "bf16", "bf16"),
+        _step("step8 few small", "fp8", "4096*2,64,1", "bf16", "bf16"),
         # parameters kept in fp32 alone, with gradients summed in fp32
-        _step("step8 many odd", "e4m3", "4096*65,1000003,65537*3,333,7", "fp32", "fp32", clip=1.0, dither=True),
-        _step("step8 layer", "e4m3", LAYER, "bf16", "bf16", dither=True),
-        _step("step8 4 layers", "e4m3", LAYERS4, "bf16", "bf16", clip=1.0, dither=True),
+        _step("step8 many odd", "fp8", "4096*65,1000003,65537*3,333,7", "fp32", "fp32", clip=1.0, dither=True),
+        _step("step8 layer", "fp8", LAYER, "bf16", "bf16", dither=True),
+        _step("step8 4 layers", "fp8", LAYERS4, "bf16", "bf16", clip=1.0, dither=True),
         # one token over a few experts
         _balance("balance 1 token", 1, 8, 2, "bf16"),
         # a micro-batch of 4096 tokens, part of it padding, loss-scaled fp16
@@ -77,9 +77,9 @@ def draw(rng):
         sizes = [max(1, int(total * w / sum(weights))) for w in weights]
         copy = rng.choice(["fp16", "bf16", "fp32"])
         grad = rng.choice([copy, "fp32"])
-        states = rng.choice(["fp32", "e4m3"])
+        states = rng.choice(["fp32", "fp8"])
         c = _step("", states, ",".join(map(str, sizes)), grad, copy, rng.choice([0.0, 1.0]),
-                  states == "e4m3" and rng.random() < 0.5)
+                  states == "fp8" and rng.random() < 0.5)
     del c["name"]
     return c
 
@@ -145,11 +145,11 @@ def _prepare_step(case, seed):
     if case["states"] == "fp32":
         s["m"], s["v"] = m, v
     else:                                               # held in 8 bits with a scale for each 256
-        for key, x in (("m", m), ("v", v.sqrt_())):
+        for key, x, most, kind in (("m", m, 448, torch.float8_e4m3fn), ("v", v, 57344, torch.float8_e5m2)):
             x = x.view(-1, ALIGN)
-            sc = x.abs().amax(1) / 448
+            sc = x.abs().amax(1) / most
             s[key + "_scale"] = sc
-            s[key] = (x / torch.where(sc > 0, sc, 1)[:, None]).clamp_(-448, 448).to(torch.float8_e4m3fn).view(-1)
+            s[key] = (x / torch.where(sc > 0, sc, 1)[:, None]).clamp_(-most, most).to(kind).view(-1)
     few = [n >= 65536 for n in sizes]                   # norms and biases do not decay
     s["decay"] = [DECAY if big else 0.0 for big in few]
     s["applied"] = torch.tensor(float(t), dtype=torch.float64, device=dev)
@@ -171,7 +171,7 @@ def _own_step(s):
     if op.master is not None:
         op.master.copy_(s["master"])
         s["master"] = op.master
-    for key in ("m", "v") + (("m_scale", "v_scale") if c["states"] == "e4m3" else ()):
+    for key in ("m", "v") + (("m_scale", "v_scale") if c["states"] == "fp8" else ()):
         getattr(op, key).copy_(s[key])
         s[key] = getattr(op, key)
     op.set_gradients(views(s["grad"]))
@@ -227,9 +227,9 @@ def _places(s):
 
 
 def _dither(s, t, tensor, block):
-    """The 20-bit dither of m's and of sqrt(v)'s codes, by block and element (half a step each without dither)."""
+    """The dither of m's codes (20 bits) and of v's (21), by block and element (half a step each without dither)."""
     if not s["case"]["dither"]:
-        return 1 << 19, 1 << 19
+        return 1 << 19, 1 << 20
     dev = s["grad"].device
     key = torch.full((), SEED >> 32, dtype=torch.int64, device=dev)
     key = _mix(_mix(key) ^ (SEED & M32))
@@ -237,21 +237,23 @@ def _dither(s, t, tensor, block):
     key = _mix((key + tensor * GOLD) & M32)
     key = _mix((key + block * GOLD) & M32)[:, None]
     lane = torch.arange(ALIGN, device=dev) * GOLD
-    return (((key + lane) & M32) >> 12).int(), (((_mix(key ^ ROOT3) + lane) & M32) >> 12).int()
+    return (((key + lane) & M32) >> 12).int(), (((_mix(key ^ ROOT3) + lane) & M32) >> 11).int()
 
 
-def _encode(x, u, keep):
-    """x by blocks of 256 as e4m3 codes and scales; keep: a positive value never becomes zero."""
+def _encode(x, u, most, low, bits, kind, keep):
+    """x by blocks of 256 as 8-bit floats of ``kind`` (largest value ``most``, smallest normal one ``low``, a step every
+    2^bits of an fp32 bit pattern) and scales; keep: a positive value never becomes zero."""
     top = x.abs().amax(1)
     ok = top >= 2.0 ** -110
-    a = (x.abs() * torch.where(ok, 448 / top, 0)[:, None]).clamp_(max=448)
-    low = a < 2.0 ** -6
-    code = ((torch.where(low, a + 2.0 ** -6, a).view(torch.int32) + u) >> 20) - torch.where(low, 968, 960)
-    code = code.clamp_(max=126)
+    a = (x.abs() * torch.where(ok, most / top, 0)[:, None]).clamp_(max=most)
+    small = a < low                                     # in the binade above, whose steps are as wide
+    zero = (127 + round(math.log2(low))) << 23 - bits
+    code = (torch.where(small, a + low, a).view(torch.int32) + u) >> bits
+    code = code - torch.where(small, zero, zero - (1 << 23 - bits))
     if keep:
         code = torch.where(x > 0, code.clamp(min=1), code)
     code = code + torch.where(x < 0, 128, 0)
-    return code.to(torch.uint8).view(torch.float8_e4m3fn).view(-1), torch.where(ok, top * (1 / 448), 0)
+    return code.to(torch.uint8).view(kind).view(-1), torch.where(ok, top * (1 / most), 0)
 
 
 def _plain_step(s):
@@ -265,10 +267,10 @@ def _plain_step(s):
     t = s["applied"] + 1
     size = (LR / (1 - BETA1 ** t)).float()
     root = (1 / (1 - BETA2 ** t).sqrt()).float()
-    eight = c["states"] == "e4m3"
+    eight = c["states"] == "fp8"
     if eight:
         m = (s["m"].float().view(-1, ALIGN) * s["m_scale"][:, None]).view(-1)
-        v = (s["v"].float().view(-1, ALIGN) * s["v_scale"][:, None]).square().view(-1)
+        v = (s["v"].float().view(-1, ALIGN) * s["v_scale"][:, None]).view(-1)
     else:
         m, v = s["m"], s["v"]
     g = g * inv
@@ -278,13 +280,12 @@ def _plain_step(s):
     shrink = torch.tensor([LR * d for d in s["decay"]], device=g.device)[tensor]
     p = s["master"]
     p = (p.view(-1, ALIGN) - shrink[:, None] * p.view(-1, ALIGN)).view(-1)
-    r = v.sqrt()
-    p = p - size * (m / (r * root + EPS))
+    p = p - size * (m / (v.sqrt() * root + EPS))
     if eight:
-        um, ur = _dither(s, t, tensor, block)
-        mc, ms = _encode(m.view(-1, ALIGN), um, False)
-        rc, rs = _encode(r.view(-1, ALIGN), ur, True)
-        new = {"m": mc.view(torch.uint8), "m_scale": ms, "v": rc.view(torch.uint8), "v_scale": rs}
+        um, uv = _dither(s, t, tensor, block)
+        mc, ms = _encode(m.view(-1, ALIGN), um, 448, 2.0 ** -6, 20, torch.float8_e4m3fn, False)
+        vc, vs = _encode(v.view(-1, ALIGN), uv, 57344, 2.0 ** -14, 21, torch.float8_e5m2, True)
+        new = {"m": mc.view(torch.uint8), "m_scale": ms, "v": vc.view(torch.uint8), "v_scale": vs}
     else:
         new = {"m": m, "v": v}
     for key, x in {**new, "master": p}.items():         # a step whose gradient is not finite changes nothing
@@ -337,7 +338,7 @@ def run(s):
     else:
         _plain_step(s)
     keys = ["params", "m", "v"] + (["master"] if s["params"] is not s["master"] else [])
-    return {k: s[k] for k in keys + (["m_scale", "v_scale"] if c["states"] == "e4m3" else [])}
+    return {k: s[k] for k in keys + (["m_scale", "v_scale"] if c["states"] == "fp8" else [])}
 
 
 # ---- the definition, in 64 bits --------------------------------------------------------------------------------------
@@ -351,15 +352,15 @@ def _hash32(x):
     return x ^ x >> 16
 
 
-def _exact_codes(x, u, keep):
+def _exact_codes(x, u, most, exponent, mantissa, keep):
     """Codes' values and scales of x (float64, blocks of 256), from the definition: floor(a / ulp + u) steps of ulp."""
     top = x.abs().max(dim=1, keepdim=True).values
-    a = torch.nan_to_num(x.abs() / top * 448, nan=0.0)
-    ulp = torch.exp2(torch.floor(torch.log2(a.clamp(min=2.0 ** -6))) - 3)
-    q = (torch.floor(a / ulp + u) * ulp).clamp(max=448)
+    a = torch.nan_to_num(x.abs() / top * most, nan=0.0)
+    ulp = torch.exp2(torch.floor(torch.log2(a.clamp(min=2.0 ** exponent))) - mantissa)
+    q = (torch.floor(a / ulp + u) * ulp).clamp(max=most)
     if keep:
-        q = torch.maximum(q, (x > 0) * 2.0 ** -9)
-    return (q * torch.sign(x)).reshape(-1), (top / 448).reshape(-1)
+        q = torch.maximum(q, (x > 0) * 2.0 ** (exponent - mantissa))
+    return (q * torch.sign(x)).reshape(-1), (top / most).reshape(-1)
 
 
 def _exact_step(case, seed):
@@ -369,7 +370,7 @@ def _exact_step(case, seed):
     norm2 = sum(float(x.double().pow(2).sum()) for x in g.split(1 << 26))
     norm = math.sqrt(norm2) / s["scale"]
     factor = (min(1.0, c["clip"] / (norm + 1e-6)) if c["clip"] else 1.0) / s["scale"]
-    eight = c["states"] == "e4m3"
+    eight = c["states"] == "fp8"
     out = {"params": torch.zeros(g.numel(), dtype=torch.float64, device=g.device)}
     for key in ("m", "v"):
         out[key] = torch.zeros_like(out["params"])
@@ -385,24 +386,23 @@ def _exact_step(case, seed):
             m, v = s["m"][at].double(), s["v"][at].double()
             if eight:
                 m = (m.view(-1, ALIGN) * s["m_scale"][blk].double()[:, None]).view(-1)
-                v = (v.view(-1, ALIGN) * s["v_scale"][blk].double()[:, None]).view(-1) ** 2
+                v = (v.view(-1, ALIGN) * s["v_scale"][blk].double()[:, None]).view(-1)
             m = BETA1 * m + (1 - BETA1) * x
             v = BETA2 * v + (1 - BETA2) * x * x
             p = s["master"][at].double() * (1 - LR * wd)
-            r = torch.sqrt(v)
-            out["params"][at] = p - LR / (1 - BETA1 ** t) * m / (r / math.sqrt(1 - BETA2 ** t) + EPS)
+            out["params"][at] = p - LR / (1 - BETA1 ** t) * m / (torch.sqrt(v) / math.sqrt(1 - BETA2 ** t) + EPS)
             if not eight:
                 out["m"][at], out["v"][at] = m, v
                 continue
-            um = ur = 0.5
+            um = uv = 0.5
             if c["dither"]:
                 key = _hash32(_hash32(_hash32(_hash32(SEED >> 32) ^ SEED % 2 ** 32) + t * GOLD & M32) + j * GOLD & M32)
                 key = _mix((key + torch.arange(lo // ALIGN, lo // ALIGN + blk.stop - blk.start, device=g.device) * GOLD)
                            % 2 ** 32)[:, None]
                 um = torch.floor((key + lane) % 2 ** 32 / 4096.0) / 2.0 ** 20
-                ur = torch.floor((_mix(key ^ ROOT3) + lane) % 2 ** 32 / 4096.0) / 2.0 ** 20
-            out["m"][at], out["m_scale"][blk] = _exact_codes(m.view(-1, ALIGN), um, False)
-            out["v"][at], out["v_scale"][blk] = _exact_codes(r.view(-1, ALIGN), ur, True)
+                uv = torch.floor((_mix(key ^ ROOT3) + lane) % 2 ** 32 / 2048.0) / 2.0 ** 21
+            out["m"][at], out["m_scale"][blk] = _exact_codes(m.view(-1, ALIGN), um, 448, -6, 3, False)
+            out["v"][at], out["v_scale"][blk] = _exact_codes(v.view(-1, ALIGN), uv, 57344, -14, 2, True)
     if c["copy"] != "fp32":
         out["master"] = out["params"]
     return out
