@@ -86,7 +86,9 @@ typedef enum ds_status DS_ENUM_BASE {
     DS_ERR_HIP = 7
 } ds_status;
 
-typedef enum ds_dtype DS_ENUM_BASE { DS_FP16 = 1, DS_FP32 = 2, DS_BF16 = 3 } ds_dtype;
+/* DS_FP8: 8-bit floats with a scale per 256 elements, for the states of a
+ * ds_tensor_list only (every other call refuses it). */
+typedef enum ds_dtype DS_ENUM_BASE { DS_FP16 = 1, DS_FP32 = 2, DS_BF16 = 3, DS_FP8 = 4 } ds_dtype;
 
 /*
  * Per-step device state, 128 bytes, kept in caller-owned DEVICE memory so that
@@ -488,6 +490,188 @@ ds_status ds_layout_greedy(const int64_t* numels, int32_t count, int64_t cap, in
  */
 ds_status ds_partition_range(int64_t total, int32_t world, int32_t rank, int64_t align,
                              int64_t* start, int64_t* count);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The optimizer step over a list of tensors
+ * ---------------------------------------------------------------------------
+ * For parameters that are not one flat partition: expert groups, norms and
+ * biases with a decay of their own, fp32 parameters beside 16-bit ones.  One
+ * call covers every tensor of the list with the arithmetic of ds_adam_step,
+ * gated by the same ds_scaler; the two Adam states are held in 32 bits
+ * (DS_FP32) or in 8 (DS_FP8).
+ *
+ * 8-bit states.  Element i of a tensor belongs to block i / 256 of that tensor
+ * (the last block may be short).  m is stored as e4m3 codes (sign, 4 exponent
+ * bits with bias 7, 3 mantissa bits; no infinity, 0x7F is NaN, the largest
+ * value 448), v as e5m2 codes (5 exponent bits with bias 15, 2 mantissa bits;
+ * the largest finite value 57344, 0x7F is NaN), with one fp32 scale per block
+ * and state; a code of value c stands for c * scale.  A step decodes m and v,
+ * updates in fp32 as ds_adam_step does (the parameter moves by the new m and v
+ * before they are rounded), and encodes x = m, v, with max = 448, 57344:
+ *   top   = max |x| over the block, at most 2^126
+ *   scale = top / max,  a = min(|x| * (max * (1 / top)), max)
+ *           (top < 2^-110: scale 0 and codes 0)
+ *   code  = floor(a / ulp + u) steps of ulp: 2^(max(floor(log2 a), -6) - 3)
+ *           for m, 2^(max(floor(log2 a), -14) - 2) for v
+ * with u = 1/2 (DS_ROUND_NEAREST) or a dither in [0, 1) (DS_ROUND_DITHER).
+ * A positive v never becomes code 0, which would leave a zero denominator
+ * under a moment that is not zero.  A NaN is kept as a NaN code.  Why a
+ * dither: v moves by (1 - beta2) of itself or less per step, far below half a
+ * step of its code, so rounding to nearest would hold it where it is; with
+ * the dither the expected value of the stored state is the fp32 one (a
+ * positive v below the smallest code aside).
+ * The dither is fixed by (seed, t, tensor index, block, element), so a
+ * repeated step gives the same bits.  With all arithmetic modulo 2^32,
+ * G = 0x9E3779B9 and mix(x): x ^= x >> 16, x *= 0x6A09E667, x ^= x >> 15,
+ * x *= 0xBB67AE85, x ^= x >> 16:
+ *   k = mix(mix(seed >> 32) ^ seed);  k = mix(k + t * G);
+ *   k = mix(k + tensor * G);          k = mix(k + block * G)
+ *   u of m = ((k + (i % 256) * G) >> 12) / 2^20
+ *   u of v = ((mix(k ^ 0xBB67AE85) + (i % 256) * G) >> 11) / 2^21
+ */
+typedef enum ds_rounding DS_ENUM_BASE { DS_ROUND_NEAREST = 0, DS_ROUND_DITHER = 1 } ds_rounding;
+
+/* Elements that share one scale of an 8-bit state. */
+#define DS_STATE_BLOCK 256
+
+/* One tensor of a list (host memory; the arrays are device memory). */
+typedef struct ds_tensor {
+    float* master;       /* fp32[n], in and out */
+    uint16_t* p16;       /* 16-bit[n] out, of type pdt; NULL with pdt DS_FP32 */
+    void* m;             /* fp32[n], or e4m3 codes [n] */
+    void* v;             /* fp32[n], or e5m2 codes [n] */
+    float* m_scale;      /* fp32[ceil(n / 256)] for 8-bit states, else NULL */
+    float* v_scale;      /* likewise */
+    const void* grad;    /* [n] of type gdt */
+    int64_t n;           /* elements; 0 is allowed (the pointers may be NULL then) */
+    float weight_decay;  /* this tensor's */
+    float lr_scale;      /* multiplies the learning rate for this tensor */
+    ds_dtype pdt;        /* DS_FP16, DS_BF16, or DS_FP32: the master is the parameter */
+    ds_dtype gdt;        /* DS_FP16, DS_BF16 or DS_FP32 */
+} ds_tensor;
+
+/* A list as the calls below take it (host memory, filled by
+ * ds_tensor_list_write, passed back unchanged). */
+typedef struct ds_tensor_list {
+    void* table;         /* the device table */
+    int64_t tiles;       /* tiles of 4096 elements over all tensors */
+    int64_t elems;       /* elements over all tensors */
+    int32_t count;       /* tensors */
+    ds_dtype sdt;        /* DS_FP32 or DS_FP8 */
+} ds_tensor_list;
+
+/* Device bytes of the table of a list of `count` tensors (0 for count < 0). */
+size_t ds_tensor_list_bytes(int32_t count);
+
+/*
+ * Describe `count` tensors to the device: validates them, writes the table
+ * (caller-owned device memory of at least ds_tensor_list_bytes(count) bytes,
+ * 16-byte aligned) with kernels that carry the descriptors as arguments, so
+ * it can be captured and `tensors` may be freed on return, and fills *list.
+ * Write it again when an address changes (new gradient tensors); steps already
+ * enqueued on the same stream use the table as it was.  The arrays need the
+ * alignment of their element type only; whole 4096-element tiles whose arrays
+ * are 16-byte (16-bit arrays 8-byte, codes 4-byte) aligned move in vectors.
+ * Errors: count < 0 or above 2^20, some n < 0, or more than 2^40 elements in
+ * all -> DS_ERR_SIZE, likewise a short table; list NULL, or (count > 0) tensors
+ * or table NULL, or a NULL array of a tensor with n > 0 -> DS_ERR_NULL; sdt not
+ * DS_FP32 / DS_FP8, or an unknown pdt or gdt -> DS_ERR_DTYPE; p16 given with
+ * pdt DS_FP32 or a scale array given with 32-bit states, weight_decay or
+ * lr_scale negative or not finite -> DS_ERR_HPARAM; a misaligned pointer ->
+ * DS_ERR_ALIGN; a written array that overlaps any other array or the table ->
+ * DS_ERR_ALIAS (gradients may overlap one another).
+ */
+ds_status ds_tensor_list_write(ds_tensor_list* list, void* table, size_t table_bytes, const ds_tensor* tensors,
+                               int32_t count, ds_dtype sdt, void* stream);
+
+/* Workspace of ds_check_overflow_list with the sum of squares: one fp64 per
+ * tile and per group of 4096 tiles (0 for list NULL). */
+size_t ds_tensor_list_workspace_bytes(const ds_tensor_list* list);
+
+/*
+ * ds_check_overflow over every gradient of the list, and with a workspace
+ * (device, 8-byte aligned, no initial contents) also the sum of squares as
+ * ds_check_overflow_sumsq: per tile in a fixed order, then per 4096 tiles, so
+ * the sum depends on the list alone.  It adds to st->grad_sumsq, so a flat
+ * partition checked in the same step is clipped by the joint norm.  An empty
+ * list launches nothing.  Errors as for ds_check_overflow_sumsq; a list that
+ * ds_tensor_list_write has not filled -> DS_ERR_NULL / DS_ERR_SIZE.
+ */
+ds_status ds_check_overflow_list(ds_scaler* st, const ds_tensor_list* list, void* workspace_or_null,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * The gated Adam step over every tensor of the list in one kernel, with the
+ * arithmetic of ds_adam_step (lr / sched_or_null, eps, max_grad_norm and
+ * accum_steps as there) and lr_j = lr * lr_scale (fp32) and weight_decay of
+ * each tensor.  The betas come in 64 bits: 1 - beta is formed there and then
+ * rounded (1 - 0.999f in fp32 is 4.7e-5 off 0.001, as much as 8-bit codes can
+ * see); betas that fp32 holds give the bits of ds_adam_step.  end_step != 0 also advances the scaler, as
+ * ds_adam_step_fused does; 0 leaves that to a later call of the same step
+ * (another list, or a flat partition's ds_adam_step_fused).  rounding and seed:
+ * of 8-bit states (ignored with 32-bit ones).  An empty list only advances the
+ * scaler, if asked.  Errors as for ds_adam_step_fused; an unknown rounding ->
+ * DS_ERR_HPARAM.
+ */
+ds_status ds_adam_step_list(ds_scaler* st, const ds_tensor_list* list, float lr,
+                            const ds_lr_schedule* sched_or_null, double beta1, double beta2, float eps,
+                            float max_grad_norm, int32_t accum_steps, ds_rounding rounding, uint64_t seed,
+                            int32_t end_step, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Balance loss of a mixture-of-experts router, counts per expert, gradient
+ * ---------------------------------------------------------------------------
+ * logits: [tokens] rows of `experts` values of type dt (DS_FP16, DS_BF16 or
+ * DS_FP32), row t starting row_stride elements after row t - 1.  A row is used
+ * if mask is NULL or mask[t] != 0, and some logit is above -infinity; T' is
+ * the number of used rows (*used).  Over used rows, with p = softmax(row):
+ *   counts[e] = rows in which e is among the k largest logits (of equal logits
+ *               the lowest index first; a logit of -infinity is never chosen)
+ *   f_e = counts[e] / (k T'),  mean_prob[e] = sum_t p_te / T'
+ *   loss = coef * experts * sum_e f_e mean_prob[e]
+ * and, f being constant,
+ *   d loss / d logit_tj = coef * experts / T' * p_tj (f_j - sum_e f_e p_te)
+ * T' = 0: mean_prob, loss and the gradient are 0.  Rows that are not used have
+ * gradient 0, whatever they hold.  A used row with a NaN or +infinity makes
+ * mean_prob, the loss and its own gradient NaN and counts nothing.  fp32
+ * arithmetic per row, sums over rows in fp32 per block and fp64 across blocks
+ * in a fixed order (the same bits every call).
+ */
+#define DS_MAX_EXPERTS 512
+#define DS_MAX_EXPERT_CHOICES 16
+
+/* Device scratch of ds_balance_loss (0 for sizes out of range). */
+size_t ds_balance_workspace_bytes(int64_t tokens, int32_t experts);
+
+/*
+ * counts: int32[experts], mean_prob: fp32[experts], loss: fp32[1], used:
+ * int32[1], all device, all written.  workspace: device, 8-byte aligned, no
+ * initial contents.  tokens may be 0 (logits may be NULL then).
+ * Errors: tokens outside [0, 2^30], experts outside 1..512, k outside
+ * 1..min(experts, 16), row_stride < experts, a short workspace -> DS_ERR_SIZE;
+ * coef not finite or negative -> DS_ERR_HPARAM; else as in the conventions
+ * (logits need the alignment of their type).
+ */
+ds_status ds_balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t experts, int64_t row_stride,
+                          const uint8_t* mask_or_null, int32_t k, float coef, int32_t* counts, float* mean_prob,
+                          float* loss, int32_t* used, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient, from the same logits and mask and the counts and *used that
+ * ds_balance_loss left on the device: dlogits (type dt, row stride
+ * grad_stride) = S * d loss / d logits, with S = st->scale read on the device
+ * (st_or_null NULL: 1), so that it joins a loss-scaled backward pass.
+ * accumulate != 0 adds to what dlogits holds (the sum in fp32, rounded once;
+ * rows that are not used stay as they are); 0 overwrites.  dlogits, from its
+ * first to its last element, must not overlap any other array.  Errors as for
+ * ds_balance_loss.
+ */
+ds_status ds_balance_loss_grad(const ds_scaler* st_or_null, const void* logits, ds_dtype dt, int64_t tokens,
+                               int32_t experts, int64_t row_stride, const uint8_t* mask_or_null, int32_t k,
+                               float coef, const int32_t* counts, const int32_t* used, void* dlogits,
+                               int64_t grad_stride, int32_t accumulate, void* stream);
 
 /* Static string naming a status code. */
 const char* ds_status_string(ds_status s);

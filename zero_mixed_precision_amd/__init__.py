@@ -11,6 +11,8 @@ from ._lib import DS_BF16, DS_FP16, DS_FP32, DsError, DsScaler
 from .config import ZeroMPConfig
 from .layout import FlatLayout
 from .step import ShardStep
+from .multi_tensor import MultiTensorStep
+from .balance import ExpertBalance
 
 __all__ = ["_lib", "DS_BF16", "DS_FP16", "DS_FP32", "DsError", "DsScaler", "ZeroMPConfig", "FlatLayout",
-           "ShardStep"]
+           "ShardStep", "MultiTensorStep", "ExpertBalance"]

@@ -15,7 +15,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdszero.so")
 
 DS_OK, DS_ERR_NULL, DS_ERR_SIZE, DS_ERR_ALIGN, DS_ERR_DTYPE, DS_ERR_HPARAM, DS_ERR_ALIAS, DS_ERR_HIP = range(8)
-DS_FP16, DS_FP32, DS_BF16 = 1, 2, 3
+DS_FP16, DS_FP32, DS_BF16, DS_FP8 = 1, 2, 3, 4
+DS_ROUND_NEAREST, DS_ROUND_DITHER = 0, 1
+DS_STATE_BLOCK, DS_MAX_EXPERTS, DS_MAX_EXPERT_CHOICES = 256, 512, 16
 
 EXPORTED = (
     "ds_scaler_size", "ds_state_init", "ds_state_read", "ds_state_write", "ds_accumulate",
@@ -24,6 +26,8 @@ EXPORTED = (
     "ds_check_overflow_sumsq", "ds_accumulate_sumsq", "ds_adam_step_sched", "ds_lr_scalars",
     "ds_adam_step_fused", "ds_accumulate_multi", "ds_check_overflow_sumsq_noalloc", "ds_adam_step_double_buffered",
     "ds_accumulate_adam_double_buffered", "ds_update_loss_scale_double_buffered",
+    "ds_tensor_list_bytes", "ds_tensor_list_write", "ds_tensor_list_workspace_bytes", "ds_check_overflow_list",
+    "ds_adam_step_list", "ds_balance_workspace_bytes", "ds_balance_loss", "ds_balance_loss_grad",
 )
 DS_NOALLOC_MAX_ELEMS = 17175674880
 DS_LR_WARMUP, DS_LR_WARMUP_DECAY = 1, 2
@@ -74,6 +78,35 @@ class DsLrSchedule(ctypes.Structure):
     def make(cls, kind, warmup_min_lr, warmup_max_lr, warmup_num_steps, total_num_steps=0):
         return cls(int(kind), 0, int(warmup_num_steps), int(total_num_steps), float(warmup_min_lr),
                    float(warmup_max_lr))
+
+
+class DsTensor(ctypes.Structure):
+    """Mirror of ``ds_tensor`` (80 bytes, host memory)."""
+    _fields_ = [
+        ("master", ctypes.c_void_p),
+        ("p16", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("weight_decay", ctypes.c_float),
+        ("lr_scale", ctypes.c_float),
+        ("pdt", ctypes.c_int32),
+        ("gdt", ctypes.c_int32),
+    ]
+
+
+class DsTensorList(ctypes.Structure):
+    """Mirror of ``ds_tensor_list`` (32 bytes, host memory)."""
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("tiles", ctypes.c_int64),
+        ("elems", ctypes.c_int64),
+        ("count", ctypes.c_int32),
+        ("sdt", ctypes.c_int32),
+    ]
 
 
 class DsError(RuntimeError):
@@ -141,6 +174,18 @@ def _load():
         "ds_lr_scalars": ([vp, ctypes.POINTER(DsLrSchedule), f32, f32, vp, vp], ctypes.c_int),
         "ds_adam_step_fused": ([vp, vp, vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, i64, f32,
                                 ctypes.POINTER(DsLrSchedule), f32, f32, f32, f32, f32, i32, vp], ctypes.c_int),
+        "ds_tensor_list_bytes": ([i32], ctypes.c_size_t),
+        "ds_tensor_list_write": ([ctypes.POINTER(DsTensorList), vp, ctypes.c_size_t, ctypes.POINTER(DsTensor), i32,
+                                  ctypes.c_int, vp], ctypes.c_int),
+        "ds_tensor_list_workspace_bytes": ([ctypes.POINTER(DsTensorList)], ctypes.c_size_t),
+        "ds_check_overflow_list": ([vp, ctypes.POINTER(DsTensorList), vp, ctypes.c_size_t, vp], ctypes.c_int),
+        "ds_adam_step_list": ([vp, ctypes.POINTER(DsTensorList), f32, ctypes.POINTER(DsLrSchedule), ctypes.c_double,
+                               ctypes.c_double, f32, f32, i32, ctypes.c_int, ctypes.c_uint64, i32, vp], ctypes.c_int),
+        "ds_balance_workspace_bytes": ([i64, i32], ctypes.c_size_t),
+        "ds_balance_loss": ([vp, ctypes.c_int, i64, i32, i64, vp, i32, f32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+                            ctypes.c_int),
+        "ds_balance_loss_grad": ([vp, vp, ctypes.c_int, i64, i32, i64, vp, i32, f32, vp, vp, vp, i64, i32, vp],
+                                 ctypes.c_int),
         "ds_layout_greedy": ([vp, i32, i64, i64, vp, vp, vp, vp, ctypes.POINTER(i32),
                               ctypes.POINTER(i64)], ctypes.c_int),
         "ds_partition_range": ([i64, i32, i32, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)],
@@ -373,6 +418,82 @@ def ds_adam_bias_scalars(st, lr, beta1, beta2, out2, stream=None) -> None:
 def ds_lr_scalars(st, sched: DsLrSchedule, beta1, beta2, out3, stream=None) -> None:
     _ok(lib.ds_lr_scalars(_scaler(st), ctypes.byref(sched), beta1, beta2, _p(out3, 12, "out3"), _s(stream)),
         "ds_lr_scalars")
+
+
+def ds_tensor_list_bytes(count) -> int:
+    return lib.ds_tensor_list_bytes(int(count))
+
+
+def ds_tensor_list_write(table, tensors, sdt, stream=None) -> DsTensorList:
+    """Describe ``tensors`` (a sequence of DsTensor) in the device table; returns the list that
+    ds_check_overflow_list and ds_adam_step_list take.  ``table``: a GPU tensor of at least
+    ds_tensor_list_bytes(len(tensors)) bytes."""
+    out, count = DsTensorList(), len(tensors)
+    arr = tensors if isinstance(tensors, ctypes.Array) else (DsTensor * max(count, 1))(*tensors)
+    nbytes = 0 if table is None else table.numel() * table.element_size()
+    _ok(lib.ds_tensor_list_write(ctypes.byref(out), _p(table, what="table"), nbytes, arr, count, int(sdt), _s(stream)),
+        "ds_tensor_list_write")
+    return out
+
+
+def ds_tensor_list_workspace_bytes(tensors: DsTensorList) -> int:
+    return lib.ds_tensor_list_workspace_bytes(ctypes.byref(tensors))
+
+
+def ds_check_overflow_list(st, tensors: DsTensorList, workspace=None, workspace_bytes=None, stream=None) -> None:
+    """ds_check_overflow over a list; with a workspace also the gradients' sum of squares."""
+    ws_bytes = 0 if workspace is None else _nbytes(workspace, workspace_bytes)
+    ws = None if workspace is None else _p(workspace, ds_tensor_list_workspace_bytes(tensors), "workspace")
+    _ok(lib.ds_check_overflow_list(_scaler(st), ctypes.byref(tensors), ws, ws_bytes, _s(stream)),
+        "ds_check_overflow_list")
+
+
+def ds_adam_step_list(st, tensors: DsTensorList, lr, sched, beta1, beta2, eps, max_grad_norm, accum_steps,
+                      rounding=DS_ROUND_NEAREST, seed=0, end_step=True, stream=None) -> None:
+    sched_p = ctypes.byref(sched) if sched is not None else None
+    _ok(lib.ds_adam_step_list(_scaler(st), ctypes.byref(tensors), lr, sched_p, beta1, beta2, eps, max_grad_norm,
+                              int(accum_steps), int(rounding), int(seed), int(bool(end_step)), _s(stream)),
+        "ds_adam_step_list")
+
+
+def ds_balance_workspace_bytes(tokens, experts) -> int:
+    return lib.ds_balance_workspace_bytes(int(tokens), int(experts))
+
+
+def _rows(x, dtype, tokens, experts, stride, what):
+    """Address of a strided [tokens, experts] matrix: an int, or a GPU tensor with unit stride inside its rows."""
+    if x is None or isinstance(x, int):
+        return x
+    if not getattr(x, "is_cuda", False):
+        raise ValueError(f"{what}: expected a tensor in GPU memory, got one on {x.device}")
+    if tokens > 0:
+        shape = tuple(x.shape)
+        if len(shape) != 2 or shape[0] < tokens or shape[1] < experts or x.element_size() != _esize(dtype):
+            raise ValueError(f"{what}: expected [{tokens}, {experts}] values of {_esize(dtype)} bytes, got {shape} of "
+                             f"{x.element_size()}")
+        if (experts > 1 and x.stride(1) != 1) or (tokens > 1 and x.stride(0) != stride):
+            raise ValueError(f"{what}: expected strides ({stride}, 1), got {tuple(x.stride())}")
+    return x.data_ptr()
+
+
+def ds_balance_loss(logits, dtype, tokens, experts, row_stride, mask, k, coef, counts, mean_prob, loss, used, workspace,
+                    workspace_bytes=None, stream=None) -> None:
+    T, E = int(tokens), int(experts)
+    _ok(lib.ds_balance_loss(_rows(logits, dtype, T, E, int(row_stride), "logits"), int(dtype), T, E, int(row_stride),
+                            _p(mask, T, "mask"), int(k), coef, _p(counts, 4 * E, "counts"),
+                            _p(mean_prob, 4 * E, "mean_prob"), _p(loss, 4, "loss"), _p(used, 4, "used"),
+                            _p(workspace, ds_balance_workspace_bytes(T, E), "workspace"),
+                            _nbytes(workspace, workspace_bytes), _s(stream)), "ds_balance_loss")
+
+
+def ds_balance_loss_grad(st_or_null, logits, dtype, tokens, experts, row_stride, mask, k, coef, counts, used, dlogits,
+                         grad_stride, accumulate=False, stream=None) -> None:
+    T, E = int(tokens), int(experts)
+    _ok(lib.ds_balance_loss_grad(_scaler(st_or_null), _rows(logits, dtype, T, E, int(row_stride), "logits"),
+                                 int(dtype), T, E, int(row_stride), _p(mask, T, "mask"), int(k), coef,
+                                 _p(counts, 4 * E, "counts"), _p(used, 4, "used"),
+                                 _rows(dlogits, dtype, T, E, int(grad_stride), "dlogits"), int(grad_stride),
+                                 int(bool(accumulate)), _s(stream)), "ds_balance_loss_grad")
 
 
 def ds_layout_greedy(numels, cap, align):

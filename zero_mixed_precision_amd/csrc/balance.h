@@ -1,0 +1,654 @@
+// balance.h -- a mixture-of-experts router's balance loss, counts per expert,
+// and the gradient.  Included by dszero.hip inside its namespace.
+//
+// A token's row is held by G lanes of a wave, 64 / G tokens per wave at a
+// time.  Lane g holds the experts 4 (c G + g) + j, j = 0..3, for its chunks
+// c = 0 .. V/4 - 1, in registers: loads are vectors of four, the softmax's
+// maximum and sum and the k largest are reductions over G lanes, and since a
+// lane meets the same experts in every row, the counts and the probability
+// sums stay in its registers until the block has done all its rows.
+
+constexpr int kBalBlock = 256;
+constexpr int kBalMaxBlocks = 512;         // rows of partial sums the finishing kernel adds
+constexpr int kBalFinishCols = 32;         // experts per block of the finishing kernel
+constexpr int64_t kBalMaxTokens = int64_t(1) << 30;
+static_assert(DS_MAX_EXPERTS == 512 && DS_MAX_EXPERT_CHOICES == 16, "the instances below");
+
+struct BalShape {
+    int64_t tokens, stride;                // rows, elements from row to row
+    int32_t experts, k, vec;               // vec: rows allow vectors of four
+};
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+template <int G>
+__device__ __forceinline__ float row_max(float x)
+{
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1)
+        x = fmaxf(x, __shfl_xor(x, off));
+    return x;
+}
+
+template <int G>
+__device__ __forceinline__ float row_sum(float x)
+{
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1)
+        x = x + __shfl_xor(x, off);
+    return x;
+}
+
+template <int G>
+__device__ __forceinline__ int row_sum_int(int x)
+{
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1)
+        x = x + __shfl_xor(x, off);
+    return x;
+}
+
+// The lane's V logits of one row (absent experts: -infinity).
+template <int GF, int G, int V>
+__device__ __forceinline__ void bal_load(const void* row, const BalShape& s, int g, float (&z)[V])
+{
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+        const int e0 = 4 * (c * G + g);
+        if (s.vec && e0 + 4 <= s.experts) {
+            f32x4 x;
+            if constexpr (GF == kF32)
+                x = *reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + e0);
+            else
+                x = widen4<GF>(*reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(row) + e0));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                z[4 * c + j] = x[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                z[4 * c + j] = e0 + j < s.experts ? load_grad1<GF>(row, e0 + j) : kNegInf;
+        }
+    }
+}
+
+// z becomes exp(z - max); returns 1 / sum.  `top` is the row's maximum (NaN
+// left out); a NaN or +infinity in the row makes the sum, so 1 / sum, NaN.
+template <int G, int V>
+__device__ __forceinline__ float bal_softmax(float (&z)[V], float top)
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        z[v] = __expf(z[v] - top);
+        sum = sum + z[v];
+    }
+    return 1.0f / row_sum<G>(sum);
+}
+
+template <int G, int V>
+__device__ __forceinline__ float bal_top(const float (&z)[V])
+{
+    float top = z[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v)
+        top = fmaxf(top, z[v]);
+    return row_max<G>(top);
+}
+
+// Whether the row counts as used: some logit is not -infinity (a NaN is not).
+template <int G, int V>
+__device__ __forceinline__ bool bal_used(const float (&z)[V], float top)
+{
+    int any = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        any |= z[v] != kNegInf ? 1 : 0;
+    return top > kNegInf || row_sum_int<G>(any) != 0;
+}
+
+// KK largest of the row in falling order, the same in each of its G lanes:
+// first of the lane's own values (insertion, one median per place), then by
+// merging the lists of lanes 1, 2, 4 .. apart.
+template <int G, int V, int KK>
+__device__ __forceinline__ void bal_largest(const float (&z)[V], float (&best)[KK])
+{
+#pragma unroll
+    for (int i = 0; i < KK; ++i)
+        best[i] = kNegInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int i = KK - 1; i > 0; --i)
+            best[i] = __builtin_amdgcn_fmed3f(best[i - 1], best[i], z[v]);
+        best[0] = fmaxf(best[0], z[v]);
+    }
+#pragma unroll
+    for (int off = 1; off < G; off <<= 1) {
+        float other[KK];
+#pragma unroll
+        for (int i = 0; i < KK; ++i)
+            other[i] = __shfl_xor(best[i], off);
+#pragma unroll
+        for (int i = 0; i < KK; ++i)   // the KK largest of both, rising then falling
+            best[i] = fmaxf(best[i], other[KK - 1 - i]);
+#pragma unroll
+        for (int d = KK / 2; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < KK; ++i)
+                if ((i & d) == 0) {
+                    const float hi = fmaxf(best[i], best[i + d]), lo = fminf(best[i], best[i + d]);
+                    best[i] = hi;
+                    best[i + d] = lo;
+                }
+    }
+}
+
+// Forward: counts and probability sums of this block's rows into row
+// blockIdx.x of the partial arrays, used rows into used[blockIdx.x].
+template <int GF, int G, int V, int KK>
+__global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restrict__ logits, BalShape s,
+                                                            const uint8_t* __restrict__ mask,
+                                                            int32_t* __restrict__ part_count,
+                                                            float* __restrict__ part_prob,
+                                                            int32_t* __restrict__ part_used,
+                                                            uint32_t* __restrict__ ticket)
+{
+    constexpr int kRows = 64 / G;          // rows of a wave
+    constexpr int kWaves = kBalBlock / 64;
+    __shared__ int32_t lds_count[kWaves][G * V];
+    __shared__ float lds_prob[kWaves][G * V];
+    __shared__ int32_t lds_used[kWaves];
+    const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64, g = lane % G;
+    int cnt[V];
+    float prob[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        cnt[v] = 0;
+        prob[v] = 0.0f;
+    }
+    int used = 0;
+    constexpr int es = GF == kF32 ? 4 : 2;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kRows;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kRows; t0 < s.tokens; t0 += step) {
+        const int64_t t = t0 + lane / G;
+        bool on = t < s.tokens;
+        if (on && mask != nullptr)
+            on = mask[t] != 0;
+        float z[V];
+        if (on) {
+            bal_load<GF, G, V>(static_cast<const unsigned char*>(logits) + t * s.stride * es, s, g, z);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                z[v] = kNegInf;
+        }
+        const float top = bal_top<G, V>(z);
+        on = on && bal_used<G, V>(z, top);
+        float best[KK];
+        bal_largest<G, V, KK>(z, best);
+        float cut = best[0];               // the k-th largest
+#pragma unroll
+        for (int i = 1; i < KK; ++i)
+            cut = i == s.k - 1 ? best[i] : cut;
+        // rows above the cut are chosen; of those equal to it as many as are
+        // left of k, the lowest indices first
+        int above = 0;
+#pragma unroll
+        for (int i = 0; i < KK; ++i)
+            above += i < s.k && best[i] > cut ? 1 : 0;
+        const int want = cut > kNegInf ? s.k - above : 0;
+        int equal = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            equal += z[v] == cut ? 1 : 0;
+        equal = row_sum_int<G>(equal);
+        uint32_t chosen = 0u;              // bit v: the lane's value v is chosen
+        if (__ballot(on && equal != want) == 0ull) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                chosen |= z[v] >= cut && z[v] > kNegInf ? 1u << v : 0u;
+        } else {
+            int left = want;
+#pragma unroll
+            for (int c = 0; c < V / 4; ++c) {
+                int mine = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mine += z[4 * c + j] == cut ? 1 : 0;
+                int before = mine;         // inclusive prefix over the row's lanes
+#pragma unroll
+                for (int off = 1; off < G; off <<= 1) {
+                    const int x = __shfl_up(before, off, G);
+                    before += g >= off ? x : 0;
+                }
+                const int all = __shfl(before, G - 1, G);
+                int rank = before - mine;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool tie = z[4 * c + j] == cut;
+                    if ((tie && rank < left) || (z[4 * c + j] > cut))
+                        chosen |= 1u << (4 * c + j);
+                    rank += tie ? 1 : 0;
+                }
+                left = left > all ? left - all : 0;
+            }
+        }
+        const float inv = bal_softmax<G, V>(z, top);
+        if (on) {
+            used += 1;
+            const bool fine = inv == inv;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                prob[v] = prob[v] + z[v] * inv;
+                cnt[v] += fine && ((chosen >> v) & 1u) ? 1 : 0;
+            }
+        }
+    }
+    // rows of the wave, then waves of the block, in a fixed order
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int off = G; off < 64; off <<= 1) {
+            cnt[v] += __shfl_xor(cnt[v], off);
+            prob[v] = prob[v] + __shfl_xor(prob[v], off);
+        }
+        if (lane < G) {
+            const int e = 4 * ((v / 4) * G + g) + v % 4;
+            lds_count[wave][e] = cnt[v];
+            lds_prob[wave][e] = prob[v];
+        }
+    }
+#pragma unroll
+    for (int off = G; off < 64; off <<= 1)
+        used += __shfl_xor(used, off);
+    if (lane == 0)
+        lds_used[wave] = used;
+    __syncthreads();
+    for (int e = threadIdx.x; e < s.experts; e += kBalBlock) {
+        int n = 0;
+        float p = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            n += lds_count[w][e];
+            p = p + lds_prob[w][e];
+        }
+        part_count[static_cast<int64_t>(blockIdx.x) * s.experts + e] = n;
+        part_prob[static_cast<int64_t>(blockIdx.x) * s.experts + e] = p;
+    }
+    if (threadIdx.x == 0) {
+        int n = 0;
+        for (int w = 0; w < kWaves; ++w)
+            n += lds_used[w];
+        part_used[blockIdx.x] = n;
+        if (blockIdx.x == 0)
+            *ticket = 0u;                  // of the finishing kernel, which runs after this one
+    }
+}
+
+// Sums the partial rows: 32 experts per block, 8 groups of rows each, fp64.
+// The block that finishes last adds the blocks' parts of the loss in order.
+__global__ __launch_bounds__(kBalBlock) void balance_finish_kernel(
+    int32_t parts, int32_t experts, int32_t k, float coef, const int32_t* __restrict__ part_count,
+    const float* __restrict__ part_prob, const int32_t* __restrict__ part_used, uint32_t* ticket, double* part_loss,
+    int32_t* __restrict__ counts, float* __restrict__ mean_prob, float* __restrict__ loss, int32_t* __restrict__ used)
+{
+    constexpr int kGroups = kBalBlock / kBalFinishCols;
+    __shared__ double lds_prob[kGroups][kBalFinishCols];
+    __shared__ int32_t lds_count[kGroups][kBalFinishCols];
+    __shared__ int32_t lds_used[kBalBlock / 64];
+    __shared__ double lds_loss[kBalFinishCols];
+    __shared__ uint32_t last;
+    const int col = threadIdx.x % kBalFinishCols, group = threadIdx.x / kBalFinishCols;
+    const int e = blockIdx.x * kBalFinishCols + col;
+    int rows = 0;
+    for (int i = threadIdx.x; i < parts; i += kBalBlock)
+        rows += part_used[i];
+    rows = row_sum_int<64>(rows);
+    if ((threadIdx.x & 63) == 0)
+        lds_used[threadIdx.x / 64] = rows;
+    int n = 0;
+    double p = 0.0;
+    if (e < experts) {
+        for (int i = group; i < parts; i += kGroups) {
+            n += part_count[static_cast<int64_t>(i) * experts + e];
+            p = p + static_cast<double>(part_prob[static_cast<int64_t>(i) * experts + e]);
+        }
+    }
+    lds_count[group][col] = n;
+    lds_prob[group][col] = p;
+    __syncthreads();
+    rows = 0;
+    for (int w = 0; w < kBalBlock / 64; ++w)
+        rows += lds_used[w];
+    if (group == 0) {
+        double mean = 0.0, part = 0.0;
+        if (e < experts) {
+            n = 0;
+            p = 0.0;
+            for (int i = 0; i < kGroups; ++i) {
+                n += lds_count[i][col];
+                p = p + lds_prob[i][col];
+            }
+            const double some = rows > 0 ? static_cast<double>(rows) : 1.0;
+            mean = p / some;
+            part = mean * (static_cast<double>(n) / (some * static_cast<double>(k)));
+            counts[e] = n;
+            mean_prob[e] = static_cast<float>(mean);
+        }
+        lds_loss[col] = part;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double sum = 0.0;
+        for (int i = 0; i < kBalFinishCols; ++i)
+            sum = sum + lds_loss[i];
+        if (gridDim.x > 1) {
+            part_loss[blockIdx.x] = sum;
+            __threadfence();
+            last = atomicAdd(ticket, 1u) == gridDim.x - 1u ? 1u : 0u;
+            if (last) {
+                __threadfence();
+                sum = 0.0;
+                for (unsigned i = 0; i < gridDim.x; ++i)
+                    sum = sum + __builtin_nontemporal_load(part_loss + i);
+            }
+        } else {
+            last = 1u;
+        }
+        if (last) {
+            *loss = static_cast<float>(static_cast<double>(coef) * static_cast<double>(experts) * sum);
+            *used = rows;
+        }
+    }
+}
+
+template <int GF, bool ACC>
+__device__ __forceinline__ void bal_store1(void* row, int e, float d)
+{
+    if constexpr (GF == kF32) {
+        float* p = static_cast<float*>(row) + e;
+        *p = ACC ? *p + d : d;
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(row) + e;
+        *p = static_cast<uint16_t>(enc1<GF>(ACC ? dec1<GF>(*p) + d : d));
+    }
+}
+
+// Gradient: d_j = S coef E / T' p_j (f_j - sum_e f_e p_e).  Since the p of a
+// row add up to 1, f may be taken off by a constant: f_e - 1/E-th of their
+// sum, formed from the counts exactly, so that the difference loses nothing
+// where the counts are nearly even.
+template <int GF, int G, int V, bool ACC>
+__global__ __launch_bounds__(kBalBlock) void balance_grad_kernel(const ds_scaler* __restrict__ st,
+                                                                 const void* __restrict__ logits, BalShape s,
+                                                                 const uint8_t* __restrict__ mask, float coef,
+                                                                 const int32_t* __restrict__ counts,
+                                                                 const int32_t* __restrict__ used,
+                                                                 void* __restrict__ dlogits, int64_t dstride,
+                                                                 int32_t dvec)
+{
+    constexpr int kRows = 64 / G, kWaves = kBalBlock / 64;
+    constexpr int es = GF == kF32 ? 4 : 2;
+    const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64, g = lane % G;
+    const int rows = *used;
+    const double scale = st != nullptr ? static_cast<double>(st->scale) : 1.0;
+    const double some = rows > 0 ? static_cast<double>(rows) : 1.0;
+    const float factor =
+        rows > 0 ? static_cast<float>(scale * static_cast<double>(coef) * static_cast<double>(s.experts) / some) : 0.0f;
+    float f[V];
+    int64_t total = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 4 * ((v / 4) * G + g) + v % 4;
+        total += e < s.experts ? counts[e] : 0;
+    }
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1)
+        total += __shfl_xor(total, off);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 4 * ((v / 4) * G + g) + v % 4;
+        const int64_t c = e < s.experts ? counts[e] : 0;
+        const double off = static_cast<double>(c * s.experts - total);
+        f[v] = static_cast<float>(off / (static_cast<double>(s.experts) * some * static_cast<double>(s.k)));
+    }
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kRows;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kRows; t0 < s.tokens; t0 += step) {
+        const int64_t t = t0 + lane / G;
+        const bool in = t < s.tokens;
+        bool on = in;
+        if (on && mask != nullptr)
+            on = mask[t] != 0;
+        float z[V];
+        if (on) {
+            bal_load<GF, G, V>(static_cast<const unsigned char*>(logits) + t * s.stride * es, s, g, z);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                z[v] = kNegInf;
+        }
+        const float top = bal_top<G, V>(z);
+        on = on && bal_used<G, V>(z, top);
+        const float inv = bal_softmax<G, V>(z, top);
+        float dot = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            z[v] = z[v] * inv;
+            dot = dot + z[v] * f[v];
+        }
+        dot = row_sum<G>(dot);
+        if (!in || (ACC && !on))
+            continue;
+        unsigned char* row = static_cast<unsigned char*>(dlogits) + t * dstride * es;
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) {
+            const int e0 = 4 * (c * G + g);
+            f32x4 d;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                d[j] = on ? factor * (z[4 * c + j] * (f[4 * c + j] - dot)) : 0.0f;
+            if (dvec && e0 + 4 <= s.experts) {
+                if constexpr (GF == kF32) {
+                    f32x4* p = reinterpret_cast<f32x4*>(row) + e0 / 4;
+                    *p = ACC ? *p + d : d;
+                } else {
+                    u32x2* p = reinterpret_cast<u32x2*>(row) + e0 / 4;
+                    *p = narrow4<GF>(ACC ? widen4<GF>(*p) + d : d);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (e0 + j < s.experts)
+                        bal_store1<GF, ACC>(row, e0 + j, d[j]);
+            }
+        }
+    }
+}
+
+// ---- host side ----
+
+// Blocks of the forward pass: one per 4 waves' rows, at most kBalMaxBlocks.
+int bal_lanes(int32_t experts) { return experts <= 256 ? 8 : 16; }
+
+int64_t bal_blocks(int64_t tokens, int32_t experts)
+{
+    const int64_t rows = static_cast<int64_t>(kBalBlock) / bal_lanes(experts);
+    const int64_t b = (tokens + rows - 1) / rows;
+    return b < 1 ? 1 : (b > kBalMaxBlocks ? kBalMaxBlocks : b);
+}
+
+// Workspace: parts of the loss (fp64), the ticket, counts, probability sums
+// and used rows per block.
+struct BalWork {
+    double* loss;
+    uint32_t* ticket;
+    int32_t *used, *count;
+    float* prob;
+};
+
+constexpr int kBalLossParts = DS_MAX_EXPERTS / kBalFinishCols;
+
+uint64_t bal_ws_bytes(int64_t blocks, int32_t experts)
+{
+    return 8 * kBalLossParts + 8 + 4 * static_cast<uint64_t>(blocks) * (1 + 2 * static_cast<uint64_t>(experts));
+}
+
+BalWork bal_work(void* ws, int64_t blocks, int32_t experts)
+{
+    BalWork w;
+    w.loss = static_cast<double*>(ws);
+    w.ticket = reinterpret_cast<uint32_t*>(w.loss + kBalLossParts);
+    w.used = reinterpret_cast<int32_t*>(w.ticket + 2);
+    w.count = w.used + blocks;
+    w.prob = reinterpret_cast<float*>(w.count + blocks * experts);
+    return w;
+}
+
+bool bal_sizes_ok(int64_t tokens, int32_t experts)
+{
+    return tokens >= 0 && tokens <= kBalMaxTokens && experts >= 1 && experts <= DS_MAX_EXPERTS;
+}
+
+// Bytes from the first to the last element of the rows.
+uint64_t bal_span(int64_t tokens, int32_t experts, int64_t stride, uint64_t es)
+{
+    return tokens == 0 ? 0 : es * (static_cast<uint64_t>(tokens - 1) * static_cast<uint64_t>(stride) + experts);
+}
+
+bool bal_vec(const void* p, int64_t stride, int32_t experts, uint64_t es)
+{
+    return aligned(p, 4 * es) && stride % 4 == 0 && experts % 4 == 0;
+}
+
+ds_status bal_check(const void* logits, ds_dtype dt, int64_t tokens, int32_t experts, int64_t stride, int32_t k,
+                    float coef)
+{
+    if (!bal_sizes_ok(tokens, experts) || k < 1 || k > experts || k > DS_MAX_EXPERT_CHOICES || stride < experts ||
+        stride > kMaxElems || (tokens > 0 && stride > kMaxElems / tokens))
+        return DS_ERR_SIZE;
+    if (!known(dt))
+        return DS_ERR_DTYPE;
+    if (!finite_ge0(coef))
+        return DS_ERR_HPARAM;
+    if (tokens > 0 && logits == nullptr)
+        return DS_ERR_NULL;
+    if (!aligned(logits, esize(dt)))
+        return DS_ERR_ALIGN;
+    return DS_OK;
+}
+
+// Whether any two of the ranges overlap, `reads` first ones aside.
+bool bal_alias(const void* const* p, const uint64_t* bytes, int n, int reads)
+{
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (j >= reads && overlap(p[i], bytes[i], p[j], bytes[j]))
+                return true;
+    return false;
+}
+
+template <int GF, int G, int V>
+void launch_balance3(int64_t blocks, hipStream_t st, const void* z, const BalShape& s, const uint8_t* mask,
+                     const BalWork& w)
+{
+    const unsigned b = static_cast<unsigned>(blocks);
+    if (s.k <= 2)      balance_kernel<GF, G, V, 2><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
+    else if (s.k <= 4) balance_kernel<GF, G, V, 4><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
+    else if (s.k <= 8) balance_kernel<GF, G, V, 8><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
+    else               balance_kernel<GF, G, V, 16><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
+}
+
+template <int GF>
+void launch_balance2(int64_t blocks, hipStream_t st, const void* z, const BalShape& s, const uint8_t* mask,
+                     const BalWork& w)
+{
+    if (s.experts <= 32)       launch_balance3<GF, 8, 4>(blocks, st, z, s, mask, w);
+    else if (s.experts <= 64)  launch_balance3<GF, 8, 8>(blocks, st, z, s, mask, w);
+    else if (s.experts <= 128) launch_balance3<GF, 8, 16>(blocks, st, z, s, mask, w);
+    else if (s.experts <= 256) launch_balance3<GF, 8, 32>(blocks, st, z, s, mask, w);
+    else                       launch_balance3<GF, 16, 32>(blocks, st, z, s, mask, w);
+}
+
+ds_status balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t experts, int64_t stride,
+                       const uint8_t* mask, int32_t k, float coef, int32_t* counts, float* mean_prob, float* loss,
+                       int32_t* used, void* ws, size_t ws_bytes, hipStream_t s)
+{
+    if (const ds_status rc = bal_check(logits, dt, tokens, experts, stride, k, coef); rc != DS_OK)
+        return rc;
+    if (counts == nullptr || mean_prob == nullptr || loss == nullptr || used == nullptr || ws == nullptr)
+        return DS_ERR_NULL;
+    if (!aligned(counts, 4) || !aligned(mean_prob, 4) || !aligned(loss, 4) || !aligned(used, 4) || !aligned(ws, 8))
+        return DS_ERR_ALIGN;
+    const int64_t blocks = bal_blocks(tokens, experts);
+    const uint64_t need = bal_ws_bytes(blocks, experts), ue = static_cast<uint64_t>(experts);
+    if (ws_bytes < need)
+        return DS_ERR_SIZE;
+    const uint64_t es = esize(dt);
+    const void* p[7] = {logits, mask, counts, mean_prob, loss, used, ws};
+    const uint64_t bytes[7] = {bal_span(tokens, experts, stride, es), static_cast<uint64_t>(tokens), 4 * ue, 4 * ue, 4,
+                               4, need};
+    if (bal_alias(p, bytes, 7, 2))
+        return DS_ERR_ALIAS;
+    const BalShape shape{tokens, stride, experts, k, bal_vec(logits, stride, experts, es) ? 1 : 0};
+    const BalWork w = bal_work(ws, blocks, experts);
+    if (dt == DS_FP16)      launch_balance2<kF16>(blocks, s, logits, shape, mask, w);
+    else if (dt == DS_BF16) launch_balance2<kBF16>(blocks, s, logits, shape, mask, w);
+    else                    launch_balance2<kF32>(blocks, s, logits, shape, mask, w);
+    if (launched() != DS_OK)
+        return DS_ERR_HIP;
+    const unsigned fb = static_cast<unsigned>((experts + kBalFinishCols - 1) / kBalFinishCols);
+    balance_finish_kernel<<<fb, kBalBlock, 0, s>>>(static_cast<int32_t>(blocks), experts, k, coef, w.count, w.prob,
+                                                   w.used, w.ticket, w.loss, counts, mean_prob, loss, used);
+    return launched();
+}
+
+template <int GF, bool ACC>
+void launch_balance_grad(unsigned b, hipStream_t s, const ds_scaler* st, const void* z, const BalShape& sh,
+                         const uint8_t* mask, float coef, const int32_t* counts, const int32_t* used, void* d,
+                         int64_t ds, int32_t dv)
+{
+    if (sh.experts <= 32)       balance_grad_kernel<GF, 8, 4, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
+    else if (sh.experts <= 64)  balance_grad_kernel<GF, 8, 8, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
+    else if (sh.experts <= 128) balance_grad_kernel<GF, 8, 16, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
+    else if (sh.experts <= 256) balance_grad_kernel<GF, 8, 32, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
+    else                        balance_grad_kernel<GF, 16, 32, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
+}
+
+ds_status balance_grad(const ds_scaler* st, const void* logits, ds_dtype dt, int64_t tokens, int32_t experts,
+                       int64_t stride, const uint8_t* mask, int32_t k, float coef, const int32_t* counts,
+                       const int32_t* used, void* dlogits, int64_t dstride, bool accumulate, hipStream_t s)
+{
+    if (const ds_status rc = bal_check(logits, dt, tokens, experts, stride, k, coef); rc != DS_OK)
+        return rc;
+    if (dstride < experts || dstride > kMaxElems || (tokens > 0 && dstride > kMaxElems / tokens))
+        return DS_ERR_SIZE;
+    if (counts == nullptr || used == nullptr || (tokens > 0 && dlogits == nullptr))
+        return DS_ERR_NULL;
+    const uint64_t es = esize(dt);
+    if (!aligned(st, 8) || !aligned(counts, 4) || !aligned(used, 4) || !aligned(dlogits, es))
+        return DS_ERR_ALIGN;
+    const void* p[6] = {logits, mask, counts, used, st, dlogits};
+    const uint64_t bytes[6] = {bal_span(tokens, experts, stride, es), static_cast<uint64_t>(tokens),
+                               4 * static_cast<uint64_t>(experts), 4, sizeof(ds_scaler),
+                               bal_span(tokens, experts, dstride, es)};
+    if (bal_alias(p, bytes, 6, 5))
+        return DS_ERR_ALIAS;
+    if (tokens == 0)
+        return DS_OK;
+    const BalShape sh{tokens, stride, experts, k, bal_vec(logits, stride, experts, es) ? 1 : 0};
+    const int32_t dv = bal_vec(dlogits, dstride, experts, es) ? 1 : 0;
+    const int64_t rows = static_cast<int64_t>(kBalBlock) / bal_lanes(experts);
+    const unsigned b = grid_blocks((tokens + rows - 1) / rows, kBalBlock);
+    const int gf = fmt_of(dt);
+    if (accumulate) {
+        if (gf == kF16)       launch_balance_grad<kF16, true>(b, s, st, logits, sh, mask, coef, counts, used, dlogits, dstride, dv);
+        else if (gf == kBF16) launch_balance_grad<kBF16, true>(b, s, st, logits, sh, mask, coef, counts, used, dlogits, dstride, dv);
+        else                  launch_balance_grad<kF32, true>(b, s, st, logits, sh, mask, coef, counts, used, dlogits, dstride, dv);
+    } else {
+        if (gf == kF16)       launch_balance_grad<kF16, false>(b, s, st, logits, sh, mask, coef, counts, used, dlogits, dstride, dv);
+        else if (gf == kBF16) launch_balance_grad<kBF16, false>(b, s, st, logits, sh, mask, coef, counts, used, dlogits, dstride, dv);
+        else                  launch_balance_grad<kF32, false>(b, s, st, logits, sh, mask, coef, counts, used, dlogits, dstride, dv);
+    }
+    return launched();
+}

@@ -51,6 +51,7 @@
 // hardware's exact widening and round-to-nearest-even narrowing.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -64,6 +65,7 @@
 
 static_assert(sizeof(ds_scaler) == 128, "ds_scaler must stay 128 bytes");
 static_assert(sizeof(ds_lr_schedule) == 32, "ds_lr_schedule is 32 bytes");
+static_assert(sizeof(ds_tensor) == 80 && sizeof(ds_tensor_list) == 32, "host structs of the tensor lists");
 
 namespace {
 
@@ -412,10 +414,10 @@ struct AdamConsts {
 // beta1^t and beta2^t by binary exponentiation over the bits of t, least
 // significant first (fp64 multiplies only), then the two bias-correction
 // factors in fp64, each rounded once to fp32.
-__device__ __forceinline__ void bias_scalars(int64_t t, float lr, float beta1, float beta2,
+__device__ __forceinline__ void bias_scalars(int64_t t, float lr, double beta1, double beta2,
                                              float* step_size, float* rbc2)
 {
-    double r1 = 1.0, r2 = 1.0, x1 = static_cast<double>(beta1), x2 = static_cast<double>(beta2);
+    double r1 = 1.0, r2 = 1.0, x1 = beta1, x2 = beta2;
     for (int64_t e = t; e > 0; e >>= 1) {
         if (e & 1) {
             r1 = r1 * x1;
@@ -1493,6 +1495,9 @@ ds_status adam_step(const ds_scaler* st, float* master, float* m, float* v, uint
     return launched();
 }
 
+#include "tensor_list.h"
+#include "balance.h"
+
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -2050,6 +2055,66 @@ ds_status ds_lr_scalars(const ds_scaler* st, const ds_lr_schedule* sched, float 
                        sched->total_num_steps};
     lr_scalars_kernel<<<1, 1, 0, static_cast<hipStream_t>(stream)>>>(st, hp, out3);
     return launched();
+}
+
+size_t ds_tensor_list_bytes(int32_t count) { return list_bytes(count); }
+
+ds_status ds_tensor_list_write(ds_tensor_list* list, void* table, size_t table_bytes, const ds_tensor* tensors,
+                               int32_t count, ds_dtype sdt, void* stream)
+{
+    return list_write(list, table, table_bytes, tensors, count, sdt, static_cast<hipStream_t>(stream));
+}
+
+size_t ds_tensor_list_workspace_bytes(const ds_tensor_list* list)
+{
+    return list_ok(list) == DS_OK ? list_ws_bytes(list->tiles) : 0;
+}
+
+ds_status ds_check_overflow_list(ds_scaler* st, const ds_tensor_list* list, void* workspace_or_null,
+                                 size_t workspace_bytes, void* stream)
+{
+    return list_check(st, list, workspace_or_null, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+ds_status ds_adam_step_list(ds_scaler* st, const ds_tensor_list* list, float lr,
+                            const ds_lr_schedule* sched_or_null, double beta1, double beta2, float eps,
+                            float max_grad_norm, int32_t accum_steps, ds_rounding rounding, uint64_t seed,
+                            int32_t end_step, void* stream)
+{
+    AdamHyper hp{lr, static_cast<float>(beta1), static_cast<float>(beta2), eps, 0.0f, max_grad_norm, accum_steps,
+                 0, 0.0f, 0, 0};
+    if (sched_or_null != nullptr) {
+        if (!schedule_ok(*sched_or_null))
+            return DS_ERR_HPARAM;
+        hp.lr = sched_or_null->warmup_max_lr;
+        hp.lr_kind = sched_or_null->kind;
+        hp.lr_min = sched_or_null->warmup_min_lr;
+        hp.lr_warmup = sched_or_null->warmup_num_steps;
+        hp.lr_total = sched_or_null->total_num_steps;
+    }
+    return list_adam(st, list, hp, beta1, beta2, rounding, seed, end_step != 0, static_cast<hipStream_t>(stream));
+}
+
+size_t ds_balance_workspace_bytes(int64_t tokens, int32_t experts)
+{
+    return bal_sizes_ok(tokens, experts) ? bal_ws_bytes(bal_blocks(tokens, experts), experts) : 0;
+}
+
+ds_status ds_balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t experts, int64_t row_stride,
+                          const uint8_t* mask_or_null, int32_t k, float coef, int32_t* counts, float* mean_prob,
+                          float* loss, int32_t* used, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return balance_loss(logits, dt, tokens, experts, row_stride, mask_or_null, k, coef, counts, mean_prob, loss, used,
+                        workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+ds_status ds_balance_loss_grad(const ds_scaler* st_or_null, const void* logits, ds_dtype dt, int64_t tokens,
+                               int32_t experts, int64_t row_stride, const uint8_t* mask_or_null, int32_t k,
+                               float coef, const int32_t* counts, const int32_t* used, void* dlogits,
+                               int64_t grad_stride, int32_t accumulate, void* stream)
+{
+    return balance_grad(st_or_null, logits, dt, tokens, experts, row_stride, mask_or_null, k, coef, counts, used,
+                        dlogits, grad_stride, accumulate != 0, static_cast<hipStream_t>(stream));
 }
 
 ds_status ds_layout_greedy(const int64_t* numels, int32_t count, int64_t cap, int64_t align,
