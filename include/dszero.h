@@ -586,14 +586,14 @@ ds_status ds_tensor_list_write(ds_tensor_list* list, void* table, size_t table_b
                                int32_t count, ds_dtype sdt, void* stream);
 
 /* Workspace of ds_check_overflow_list with the sum of squares: one fp64 per
- * tile and per group of 4096 tiles (0 for list NULL). */
+ * four tiles and per 4096 of those (0 for list NULL). */
 size_t ds_tensor_list_workspace_bytes(const ds_tensor_list* list);
 
 /*
  * ds_check_overflow over every gradient of the list, and with a workspace
  * (device, 8-byte aligned, no initial contents) also the sum of squares as
- * ds_check_overflow_sumsq: per tile in a fixed order, then per 4096 tiles, so
- * the sum depends on the list alone.  It adds to st->grad_sumsq, so a flat
+ * ds_check_overflow_sumsq: per four tiles in a fixed order, then per 4096 of
+ * those sums, so the result depends on the list alone.  It adds to st->grad_sumsq, so a flat
  * partition checked in the same step is clipped by the joint norm.  An empty
  * list launches nothing.  Errors as for ds_check_overflow_sumsq; a list that
  * ds_tensor_list_write has not filled -> DS_ERR_NULL / DS_ERR_SIZE.

@@ -37,47 +37,57 @@ class ExpertBalance:
             # enough for any number of tokens (2.1 MB for 512 experts)
             need = _lib.ds_balance_workspace_bytes(1 << 30, self.E)
             self._ws = torch.empty((need + 7) // 8, dtype=torch.float64, device=device)
+        self._at = (self.counts.data_ptr(), self.mean_prob.data_ptr(), self.value.data_ptr(), self.used.data_ptr(),
+                    self._ws.data_ptr(), self._ws.numel() * 8)
 
     def _rows(self, x, what):
-        if x.dim() != 2 or x.shape[1] != self.E:
-            raise ValueError(f"{what}: expected [tokens, {self.E}], got {tuple(x.shape)}")
+        """(address, row stride) of a [tokens, experts] matrix."""
+        shape = x.shape
+        if len(shape) != 2 or shape[1] != self.E:
+            raise ValueError(f"{what}: expected [tokens, {self.E}], got {tuple(shape)}")
         if x.device != self.counts.device:
             raise ValueError(f"{what}: expected a tensor on {self.counts.device}, got one on {x.device}")
-        if self.E > 1 and x.shape[0] > 0 and x.stride(1) != 1:
+        T = shape[0]
+        stride, inner = x.stride()
+        if inner != 1 and self.E > 1 and T > 0:
             raise ValueError(f"{what}: the experts of a row must be adjacent")
-        stride = x.stride(0) if x.shape[0] > 1 else self.E
-        if stride < self.E:
+        if T <= 1:
+            stride = self.E
+        elif stride < self.E:
             raise ValueError(f"{what}: rows overlap")
-        return stride
+        return (x.data_ptr() if T else None), stride
 
     def _mask(self, mask, tokens):
-        torch = self.torch
         if mask is None:
             return None
+        torch = self.torch
         if mask.dtype not in (torch.bool, torch.uint8) or mask.dim() != 1 or mask.shape[0] != tokens:
             raise ValueError(f"mask: expected {tokens} bool or uint8 values")
-        return mask if tokens else None
+        if mask.device != self.counts.device or not mask.is_contiguous():
+            raise ValueError(f"mask: expected a contiguous tensor on {self.counts.device}")
+        return mask.data_ptr() if tokens else None
 
     def loss(self, logits, mask=None):
         """Counts and loss of ``logits`` (fp16, bf16 or fp32 [tokens, experts], rows any distance apart); ``mask``:
         bool or uint8 per token, 0 leaves it out.  Returns ``value``."""
-        torch = self.torch
-        stride, T = self._rows(logits, "logits"), logits.shape[0]
-        dt = _dtype_of(logits, torch, "logits")
-        mask = self._mask(mask, T)
-        _lib.ds_balance_loss(logits if T else None, dt, T, self.E, stride, mask, self.k, self.coef, self.counts,
-                             self.mean_prob, self.value, self.used, self._ws, stream=self.stream)
+        dt = _dtype_of(logits, self.torch, "logits")
+        z, stride = self._rows(logits, "logits")
+        T = logits.shape[0]
+        counts, mean, value, used, ws, ws_bytes = self._at
+        _lib._ok(_lib.lib.ds_balance_loss(z, dt, T, self.E, stride, self._mask(mask, T), self.k, self.coef, counts, mean,
+                                          value, used, ws, ws_bytes, _lib._s(self.stream)), "ds_balance_loss")
         return self.value
 
     def gradient(self, logits, out, mask=None, scaler=None, accumulate=False):
         """The gradient by ``logits`` of the loss() just taken of them, into ``out`` (their type and shape), times the
         scale of ``scaler`` (a ds_scaler state on the device; None: 1).  accumulate: add to ``out``."""
-        torch = self.torch
-        stride, gstride, T = self._rows(logits, "logits"), self._rows(out, "out"), logits.shape[0]
         if out.dtype != logits.dtype or out.shape != logits.shape:
             raise ValueError("out: expected the logits' type and shape")
-        dt = _dtype_of(logits, torch, "logits")
-        mask = self._mask(mask, T)
-        _lib.ds_balance_loss_grad(scaler, logits if T else None, dt, T, self.E, stride, mask, self.k, self.coef,
-                                  self.counts, self.used, out if T else None, gstride, accumulate, stream=self.stream)
+        dt = _dtype_of(logits, self.torch, "logits")
+        z, stride = self._rows(logits, "logits")
+        d, gstride = self._rows(out, "out")
+        T = logits.shape[0]
+        _lib._ok(_lib.lib.ds_balance_loss_grad(_lib._scaler(scaler), z, dt, T, self.E, stride, self._mask(mask, T),
+                                               self.k, self.coef, self._at[0], self._at[3], d, gstride, accumulate,
+                                               _lib._s(self.stream)), "ds_balance_loss_grad")
         return out

@@ -9,8 +9,9 @@
 // sums stay in its registers until the block has done all its rows.
 
 constexpr int kBalBlock = 256;
-constexpr int kBalMaxBlocks = 512;         // rows of partial sums the finishing kernel adds
-constexpr int kBalFinishCols = 32;         // experts per block of the finishing kernel
+constexpr int kBalMaxBlocks = 1024;        // rows of partial sums: four blocks per CU
+constexpr int kBalFinishBlock = 1024, kBalFinishCols = 16;   // finishing kernel: lanes, experts per block
+constexpr int64_t kBalGradBlocks = 2048;   // gradient: eight blocks per CU
 constexpr int64_t kBalMaxTokens = int64_t(1) << 30;
 static_assert(DS_MAX_EXPERTS == 512 && DS_MAX_EXPERT_CHOICES == 16, "the instances below");
 
@@ -19,34 +20,16 @@ struct BalShape {
     int32_t experts, k, vec;               // vec: rows allow vectors of four
 };
 
+// Workspace: parts of the loss (fp64), the ticket, counts, probability sums
+// and used rows per block.
+struct BalWork {
+    double* loss;
+    uint32_t* ticket;
+    int32_t *used, *count;
+    float* prob;
+};
+
 constexpr float kNegInf = -__builtin_huge_valf();
-
-template <int G>
-__device__ __forceinline__ float row_max(float x)
-{
-#pragma unroll
-    for (int off = G / 2; off > 0; off >>= 1)
-        x = fmaxf(x, __shfl_xor(x, off));
-    return x;
-}
-
-template <int G>
-__device__ __forceinline__ float row_sum(float x)
-{
-#pragma unroll
-    for (int off = G / 2; off > 0; off >>= 1)
-        x = x + __shfl_xor(x, off);
-    return x;
-}
-
-template <int G>
-__device__ __forceinline__ int row_sum_int(int x)
-{
-#pragma unroll
-    for (int off = G / 2; off > 0; off >>= 1)
-        x = x + __shfl_xor(x, off);
-    return x;
-}
 
 // The lane's V logits of one row (absent experts: -infinity).
 template <int GF, int G, int V>
@@ -100,11 +83,33 @@ __device__ __forceinline__ float bal_top(const float (&z)[V])
 template <int G, int V>
 __device__ __forceinline__ bool bal_used(const float (&z)[V], float top)
 {
-    int any = 0;
+    uint32_t any = 0u;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        any |= z[v] != kNegInf ? 1 : 0;
+        any |= z[v] != kNegInf ? 1u : 0u;
     return top > kNegInf || row_sum_int<G>(any) != 0;
+}
+
+// The KK largest of two lanes' falling lists, falling.
+template <int OFF, int KK>
+__device__ __forceinline__ void bal_merge(float (&best)[KK])
+{
+    float other[KK];
+#pragma unroll
+    for (int i = 0; i < KK; ++i)
+        other[i] = row_other<OFF>(best[i]);
+#pragma unroll
+    for (int i = 0; i < KK; ++i)       // the KK largest of both, rising then falling
+        best[i] = fmaxf(best[i], other[KK - 1 - i]);
+#pragma unroll
+    for (int d = KK / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < KK; ++i)
+            if ((i & d) == 0) {
+                const float hi = fmaxf(best[i], best[i + d]), lo = fminf(best[i], best[i + d]);
+                best[i] = hi;
+                best[i + d] = lo;
+            }
 }
 
 // KK largest of the row in falling order, the same in each of its G lanes:
@@ -123,42 +128,52 @@ __device__ __forceinline__ void bal_largest(const float (&z)[V], float (&best)[K
             best[i] = __builtin_amdgcn_fmed3f(best[i - 1], best[i], z[v]);
         best[0] = fmaxf(best[0], z[v]);
     }
-#pragma unroll
-    for (int off = 1; off < G; off <<= 1) {
-        float other[KK];
-#pragma unroll
-        for (int i = 0; i < KK; ++i)
-            other[i] = __shfl_xor(best[i], off);
-#pragma unroll
-        for (int i = 0; i < KK; ++i)   // the KK largest of both, rising then falling
-            best[i] = fmaxf(best[i], other[KK - 1 - i]);
-#pragma unroll
-        for (int d = KK / 2; d > 0; d >>= 1)
-#pragma unroll
-            for (int i = 0; i < KK; ++i)
-                if ((i & d) == 0) {
-                    const float hi = fmaxf(best[i], best[i + d]), lo = fminf(best[i], best[i + d]);
-                    best[i] = hi;
-                    best[i + d] = lo;
-                }
-    }
+    bal_merge<1, KK>(best);
+    bal_merge<2, KK>(best);
+    bal_merge<4, KK>(best);
+    if constexpr (G == 16)
+        bal_merge<8, KK>(best);
+}
+
+// What the forward pass leaves, and what it is scaled by.
+struct BalOut {
+    int32_t* counts;
+    float* mean_prob;
+    float* loss;
+    int32_t* used;
+    float coef;
+};
+
+// Expert e of E: its count n and probability sum p become outputs; returns its
+// part of the loss, f_e mean_prob_e.
+__device__ __forceinline__ double bal_expert(const BalOut& o, int32_t k, int rows, int e, int n, double p)
+{
+    const double some = rows > 0 ? static_cast<double>(rows) : 1.0;
+    const double mean = p / some;
+    o.counts[e] = n;
+    o.mean_prob[e] = static_cast<float>(mean);
+    return mean * (static_cast<double>(n) / (some * static_cast<double>(k)));
+}
+
+__device__ __forceinline__ void bal_end(const BalOut& o, int32_t experts, int rows, double sum)
+{
+    *o.loss = static_cast<float>(static_cast<double>(o.coef) * static_cast<double>(experts) * sum);
+    *o.used = rows;
 }
 
 // Forward: counts and probability sums of this block's rows into row
-// blockIdx.x of the partial arrays, used rows into used[blockIdx.x].
+// blockIdx.x of the partial arrays, used rows into used[blockIdx.x].  A grid
+// of one block ends the call itself.
 template <int GF, int G, int V, int KK>
 __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restrict__ logits, BalShape s,
-                                                            const uint8_t* __restrict__ mask,
-                                                            int32_t* __restrict__ part_count,
-                                                            float* __restrict__ part_prob,
-                                                            int32_t* __restrict__ part_used,
-                                                            uint32_t* __restrict__ ticket)
+                                                            const uint8_t* __restrict__ mask, BalWork w, BalOut o)
 {
     constexpr int kRows = 64 / G;          // rows of a wave
     constexpr int kWaves = kBalBlock / 64;
     __shared__ int32_t lds_count[kWaves][G * V];
     __shared__ float lds_prob[kWaves][G * V];
     __shared__ int32_t lds_used[kWaves];
+    __shared__ double lds_loss[2 * kWaves];
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64, g = lane % G;
     int cnt[V];
     float prob[V];
@@ -265,102 +280,113 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
     if (lane == 0)
         lds_used[wave] = used;
     __syncthreads();
+    int rows = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+        rows += lds_used[i];
+    double part = 0.0;
     for (int e = threadIdx.x; e < s.experts; e += kBalBlock) {
         int n = 0;
         float p = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            n += lds_count[w][e];
-            p = p + lds_prob[w][e];
+        for (int i = 0; i < kWaves; ++i) {
+            n += lds_count[i][e];
+            p = p + lds_prob[i][e];
         }
-        part_count[static_cast<int64_t>(blockIdx.x) * s.experts + e] = n;
-        part_prob[static_cast<int64_t>(blockIdx.x) * s.experts + e] = p;
+        if (gridDim.x > 1) {
+            w.count[static_cast<int64_t>(blockIdx.x) * s.experts + e] = n;
+            w.prob[static_cast<int64_t>(blockIdx.x) * s.experts + e] = p;
+        } else {
+            part = part + bal_expert(o, s.k, rows, e, n, static_cast<double>(p));
+        }
     }
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int w = 0; w < kWaves; ++w)
-            n += lds_used[w];
-        part_used[blockIdx.x] = n;
+    if (gridDim.x == 1) {
+        part = block_sum_fixed<kBalBlock>(part, lds_loss, 0);
+        if (threadIdx.x == 0)
+            bal_end(o, s.experts, rows, part);
+    } else if (threadIdx.x == 0) {
+        w.used[blockIdx.x] = rows;
         if (blockIdx.x == 0)
-            *ticket = 0u;                  // of the finishing kernel, which runs after this one
+            *w.ticket = 0u;                // of the finishing kernel, which runs after this one
     }
 }
 
-// Sums the partial rows: 32 experts per block, 8 groups of rows each, fp64.
-// The block that finishes last adds the blocks' parts of the loss in order.
-__global__ __launch_bounds__(kBalBlock) void balance_finish_kernel(
-    int32_t parts, int32_t experts, int32_t k, float coef, const int32_t* __restrict__ part_count,
-    const float* __restrict__ part_prob, const int32_t* __restrict__ part_used, uint32_t* ticket, double* part_loss,
-    int32_t* __restrict__ counts, float* __restrict__ mean_prob, float* __restrict__ loss, int32_t* __restrict__ used)
+// Sums the partial rows: 16 experts per block, 64 groups of rows, fp64.  The
+// block that finishes last adds the blocks' parts of the loss in order.
+__global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t parts, int32_t experts, int32_t k,
+                                                                         BalWork w, BalOut o)
 {
-    constexpr int kGroups = kBalBlock / kBalFinishCols;
-    __shared__ double lds_prob[kGroups][kBalFinishCols];
-    __shared__ int32_t lds_count[kGroups][kBalFinishCols];
-    __shared__ int32_t lds_used[kBalBlock / 64];
-    __shared__ double lds_loss[kBalFinishCols];
-    __shared__ uint32_t last;
+    constexpr int kGroups = kBalFinishBlock / kBalFinishCols, kWaves = kBalFinishBlock / 64, kDeep = 8;
+    __shared__ double lds_prob[kWaves][kBalFinishCols];
+    __shared__ int32_t lds_count[kWaves][kBalFinishCols];
+    __shared__ int32_t lds_used[kWaves];
     const int col = threadIdx.x % kBalFinishCols, group = threadIdx.x / kBalFinishCols;
+    const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
     const int e = blockIdx.x * kBalFinishCols + col;
     int rows = 0;
-    for (int i = threadIdx.x; i < parts; i += kBalBlock)
-        rows += part_used[i];
-    rows = row_sum_int<64>(rows);
-    if ((threadIdx.x & 63) == 0)
-        lds_used[threadIdx.x / 64] = rows;
+    for (int i = threadIdx.x; i < parts; i += kBalFinishBlock)
+        rows += w.used[i];
     int n = 0;
     double p = 0.0;
-    if (e < experts) {
-        for (int i = group; i < parts; i += kGroups) {
-            n += part_count[static_cast<int64_t>(i) * experts + e];
-            p = p + static_cast<double>(part_prob[static_cast<int64_t>(i) * experts + e]);
+    for (int i0 = group; i0 < parts; i0 += kGroups * kDeep) {
+        int32_t c[kDeep];
+        float q[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            const int i = i0 + u * kGroups;
+            const bool in = i < parts && e < experts;
+            c[u] = in ? w.count[static_cast<int64_t>(i) * experts + e] : 0;
+            q[u] = in ? w.prob[static_cast<int64_t>(i) * experts + e] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            n += c[u];
+            p = p + static_cast<double>(q[u]);
         }
     }
-    lds_count[group][col] = n;
-    lds_prob[group][col] = p;
+#pragma unroll
+    for (int off = kBalFinishCols; off < 64; off <<= 1) {
+        n += __shfl_xor(n, off);
+        p = p + __shfl_xor(p, off);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        rows += __shfl_xor(rows, off);
+    if (lane < kBalFinishCols) {
+        lds_count[wave][col] = n;
+        lds_prob[wave][col] = p;
+    }
+    if (lane == 0)
+        lds_used[wave] = rows;
     __syncthreads();
+    if (wave != 0)
+        return;
     rows = 0;
-    for (int w = 0; w < kBalBlock / 64; ++w)
-        rows += lds_used[w];
-    if (group == 0) {
-        double mean = 0.0, part = 0.0;
-        if (e < experts) {
-            n = 0;
-            p = 0.0;
-            for (int i = 0; i < kGroups; ++i) {
-                n += lds_count[i][col];
-                p = p + lds_prob[i][col];
-            }
-            const double some = rows > 0 ? static_cast<double>(rows) : 1.0;
-            mean = p / some;
-            part = mean * (static_cast<double>(n) / (some * static_cast<double>(k)));
-            counts[e] = n;
-            mean_prob[e] = static_cast<float>(mean);
-        }
-        lds_loss[col] = part;
+    n = 0;
+    p = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        rows += lds_used[i];
+        n += lds_count[i][col];
+        p = p + lds_prob[i][col];
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double sum = 0.0;
-        for (int i = 0; i < kBalFinishCols; ++i)
-            sum = sum + lds_loss[i];
-        if (gridDim.x > 1) {
-            part_loss[blockIdx.x] = sum;
-            __threadfence();
-            last = atomicAdd(ticket, 1u) == gridDim.x - 1u ? 1u : 0u;
-            if (last) {
-                __threadfence();
-                sum = 0.0;
-                for (unsigned i = 0; i < gridDim.x; ++i)
-                    sum = sum + __builtin_nontemporal_load(part_loss + i);
-            }
-        } else {
-            last = 1u;
-        }
-        if (last) {
-            *loss = static_cast<float>(static_cast<double>(coef) * static_cast<double>(experts) * sum);
-            *used = rows;
-        }
+    double part = lane < kBalFinishCols && e < experts ? bal_expert(o, k, rows, e, n, p) : 0.0;
+#pragma unroll
+    for (int off = 1; off < kBalFinishCols; off <<= 1)
+        part = part + __shfl_xor(part, off);
+    if (lane != 0)
+        return;
+    if (gridDim.x > 1) {
+        w.loss[blockIdx.x] = part;
+        __threadfence();
+        if (atomicAdd(w.ticket, 1u) != gridDim.x - 1u)
+            return;
+        __threadfence();
+        part = 0.0;
+        for (unsigned i = 0; i < gridDim.x; ++i)
+            part = part + __builtin_nontemporal_load(w.loss + i);
     }
+    bal_end(o, experts, rows, part);
 }
 
 template <int GF, bool ACC>
@@ -406,12 +432,12 @@ __global__ __launch_bounds__(kBalBlock) void balance_grad_kernel(const ds_scaler
 #pragma unroll
     for (int off = G / 2; off > 0; off >>= 1)
         total += __shfl_xor(total, off);
+    const double unit = 1.0 / (static_cast<double>(s.experts) * some * static_cast<double>(s.k));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = 4 * ((v / 4) * G + g) + v % 4;
         const int64_t c = e < s.experts ? counts[e] : 0;
-        const double off = static_cast<double>(c * s.experts - total);
-        f[v] = static_cast<float>(off / (static_cast<double>(s.experts) * some * static_cast<double>(s.k)));
+        f[v] = static_cast<float>(static_cast<double>(c * s.experts - total) * unit);
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kRows;
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kRows; t0 < s.tokens; t0 += step) {
@@ -478,15 +504,6 @@ int64_t bal_blocks(int64_t tokens, int32_t experts)
     return b < 1 ? 1 : (b > kBalMaxBlocks ? kBalMaxBlocks : b);
 }
 
-// Workspace: parts of the loss (fp64), the ticket, counts, probability sums
-// and used rows per block.
-struct BalWork {
-    double* loss;
-    uint32_t* ticket;
-    int32_t *used, *count;
-    float* prob;
-};
-
 constexpr int kBalLossParts = DS_MAX_EXPERTS / kBalFinishCols;
 
 uint64_t bal_ws_bytes(int64_t blocks, int32_t experts)
@@ -550,24 +567,24 @@ bool bal_alias(const void* const* p, const uint64_t* bytes, int n, int reads)
 
 template <int GF, int G, int V>
 void launch_balance3(int64_t blocks, hipStream_t st, const void* z, const BalShape& s, const uint8_t* mask,
-                     const BalWork& w)
+                     const BalWork& w, const BalOut& o)
 {
     const unsigned b = static_cast<unsigned>(blocks);
-    if (s.k <= 2)      balance_kernel<GF, G, V, 2><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
-    else if (s.k <= 4) balance_kernel<GF, G, V, 4><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
-    else if (s.k <= 8) balance_kernel<GF, G, V, 8><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
-    else               balance_kernel<GF, G, V, 16><<<b, kBalBlock, 0, st>>>(z, s, mask, w.count, w.prob, w.used, w.ticket);
+    if (s.k <= 2)      balance_kernel<GF, G, V, 2><<<b, kBalBlock, 0, st>>>(z, s, mask, w, o);
+    else if (s.k <= 4) balance_kernel<GF, G, V, 4><<<b, kBalBlock, 0, st>>>(z, s, mask, w, o);
+    else if (s.k <= 8) balance_kernel<GF, G, V, 8><<<b, kBalBlock, 0, st>>>(z, s, mask, w, o);
+    else               balance_kernel<GF, G, V, 16><<<b, kBalBlock, 0, st>>>(z, s, mask, w, o);
 }
 
 template <int GF>
 void launch_balance2(int64_t blocks, hipStream_t st, const void* z, const BalShape& s, const uint8_t* mask,
-                     const BalWork& w)
+                     const BalWork& w, const BalOut& o)
 {
-    if (s.experts <= 32)       launch_balance3<GF, 8, 4>(blocks, st, z, s, mask, w);
-    else if (s.experts <= 64)  launch_balance3<GF, 8, 8>(blocks, st, z, s, mask, w);
-    else if (s.experts <= 128) launch_balance3<GF, 8, 16>(blocks, st, z, s, mask, w);
-    else if (s.experts <= 256) launch_balance3<GF, 8, 32>(blocks, st, z, s, mask, w);
-    else                       launch_balance3<GF, 16, 32>(blocks, st, z, s, mask, w);
+    if (s.experts <= 32)       launch_balance3<GF, 8, 4>(blocks, st, z, s, mask, w, o);
+    else if (s.experts <= 64)  launch_balance3<GF, 8, 8>(blocks, st, z, s, mask, w, o);
+    else if (s.experts <= 128) launch_balance3<GF, 8, 16>(blocks, st, z, s, mask, w, o);
+    else if (s.experts <= 256) launch_balance3<GF, 8, 32>(blocks, st, z, s, mask, w, o);
+    else                       launch_balance3<GF, 16, 32>(blocks, st, z, s, mask, w, o);
 }
 
 ds_status balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t experts, int64_t stride,
@@ -592,14 +609,16 @@ ds_status balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t 
         return DS_ERR_ALIAS;
     const BalShape shape{tokens, stride, experts, k, bal_vec(logits, stride, experts, es) ? 1 : 0};
     const BalWork w = bal_work(ws, blocks, experts);
-    if (dt == DS_FP16)      launch_balance2<kF16>(blocks, s, logits, shape, mask, w);
-    else if (dt == DS_BF16) launch_balance2<kBF16>(blocks, s, logits, shape, mask, w);
-    else                    launch_balance2<kF32>(blocks, s, logits, shape, mask, w);
+    const BalOut o{counts, mean_prob, loss, used, coef};
+    if (dt == DS_FP16)      launch_balance2<kF16>(blocks, s, logits, shape, mask, w, o);
+    else if (dt == DS_BF16) launch_balance2<kBF16>(blocks, s, logits, shape, mask, w, o);
+    else                    launch_balance2<kF32>(blocks, s, logits, shape, mask, w, o);
     if (launched() != DS_OK)
         return DS_ERR_HIP;
+    if (blocks == 1)
+        return DS_OK;
     const unsigned fb = static_cast<unsigned>((experts + kBalFinishCols - 1) / kBalFinishCols);
-    balance_finish_kernel<<<fb, kBalBlock, 0, s>>>(static_cast<int32_t>(blocks), experts, k, coef, w.count, w.prob,
-                                                   w.used, w.ticket, w.loss, counts, mean_prob, loss, used);
+    balance_finish_kernel<<<fb, kBalFinishBlock, 0, s>>>(static_cast<int32_t>(blocks), experts, k, w, o);
     return launched();
 }
 
@@ -639,7 +658,8 @@ ds_status balance_grad(const ds_scaler* st, const void* logits, ds_dtype dt, int
     const BalShape sh{tokens, stride, experts, k, bal_vec(logits, stride, experts, es) ? 1 : 0};
     const int32_t dv = bal_vec(dlogits, dstride, experts, es) ? 1 : 0;
     const int64_t rows = static_cast<int64_t>(kBalBlock) / bal_lanes(experts);
-    const unsigned b = grid_blocks((tokens + rows - 1) / rows, kBalBlock);
+    const int64_t turns = (tokens + rows - 1) / rows;
+    const unsigned b = grid_blocks(turns < kBalGradBlocks ? turns : kBalGradBlocks, kBalBlock);
     const int gf = fmt_of(dt);
     if (accumulate) {
         if (gf == kF16)       launch_balance_grad<kF16, true>(b, s, st, logits, sh, mask, coef, counts, used, dlogits, dstride, dv);

@@ -411,11 +411,9 @@ struct AdamConsts {
     float eps;
 };
 
-// beta1^t and beta2^t by binary exponentiation over the bits of t, least
-// significant first (fp64 multiplies only), then the two bias-correction
-// factors in fp64, each rounded once to fp32.
-__device__ __forceinline__ void bias_scalars(int64_t t, float lr, double beta1, double beta2,
-                                             float* step_size, float* rbc2)
+// 1 - beta1^t and 1 - beta2^t, the powers by binary exponentiation over the
+// bits of t, least significant first (fp64 multiplies only).
+__device__ __forceinline__ void bias_powers(int64_t t, double beta1, double beta2, double* om1, double* om2)
 {
     double r1 = 1.0, r2 = 1.0, x1 = beta1, x2 = beta2;
     for (int64_t e = t; e > 0; e >>= 1) {
@@ -426,8 +424,18 @@ __device__ __forceinline__ void bias_scalars(int64_t t, float lr, double beta1, 
         x1 = x1 * x1;
         x2 = x2 * x2;
     }
-    *step_size = static_cast<float>(static_cast<double>(lr) / (1.0 - r1));
-    *rbc2 = static_cast<float>(1.0 / sqrt(1.0 - r2));
+    *om1 = 1.0 - r1;
+    *om2 = 1.0 - r2;
+}
+
+// The two bias-correction factors in fp64, each rounded once to fp32.
+__device__ __forceinline__ void bias_scalars(int64_t t, float lr, float beta1, float beta2,
+                                             float* step_size, float* rbc2)
+{
+    double om1, om2;
+    bias_powers(t, beta1, beta2, &om1, &om2);
+    *step_size = static_cast<float>(static_cast<double>(lr) / om1);
+    *rbc2 = static_cast<float>(1.0 / sqrt(om2));
 }
 
 // Learning rate of schedule iteration `it` (Adam steps applied before this
@@ -1495,6 +1503,7 @@ ds_status adam_step(const ds_scaler* st, float* master, float* m, float* v, uint
     return launched();
 }
 
+#include "lanes.h"
 #include "tensor_list.h"
 #include "balance.h"
 

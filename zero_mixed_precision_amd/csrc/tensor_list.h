@@ -11,6 +11,10 @@ constexpr int kListBlock = 256;                    // lanes: 4 quads each per ti
 constexpr int kListQuads = 4;
 static_assert(kListTile == 4 * kListBlock * kListQuads, "one tile per block");
 static_assert(DS_STATE_BLOCK == 4 * 64, "one quad per lane of a wave is one block of an 8-bit state");
+constexpr int kCheckTiles = 4;                     // tiles that share one partial sum of squares
+// A ticket per block, all from one address, costs about 13 ns each: past this
+// many blocks the scaler is advanced by a kernel of its own (2 us).
+constexpr unsigned kFuseBlocks = 1024;
 constexpr int32_t kMaxTensors = 1 << 20;
 
 // One tensor in the device table.
@@ -66,25 +70,52 @@ __device__ __forceinline__ int list_find(const int32_t* __restrict__ tile0, int 
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Loads and stores through pointers that come from the table: they are known
+// to be global memory, not the generic pointers that the compiler must take
+// them for (whose accesses also occupy the shared memory's counters).
+#define DS_GLOBAL __attribute__((address_space(1)))
+
+template <bool NT = false, typename T>
+__device__ __forceinline__ T gload(const T* p)
+{
+    const DS_GLOBAL T* q = (const DS_GLOBAL T*)p;
+    if constexpr (NT)
+        return __builtin_nontemporal_load(q);
+    else
+        return *q;
+}
+
+template <bool NT = false, typename T>
+__device__ __forceinline__ void gstore(T* p, T x)
+{
+    DS_GLOBAL T* q = (DS_GLOBAL T*)p;
+    if constexpr (NT)
+        __builtin_nontemporal_store(x, q);
+    else
+        *q = x;
+}
+
 __device__ __forceinline__ float list_grad1(int gf, const void* grad, int64_t i)
 {
     if (gf == kF32)
-        return load_grad1<kF32>(grad, i);
-    return gf == kBF16 ? load_grad1<kBF16>(grad, i) : load_grad1<kF16>(grad, i);
+        return gload(static_cast<const float*>(grad) + i);
+    const uint32_t w = gload(static_cast<const uint16_t*>(grad) + i);
+    return gf == kBF16 ? dec1<kBF16>(w) : dec1<kF16>(w);
 }
 
 // ---- overflow check and sum of squares ----
 
-template <int GF, bool SUMSQ>
-__device__ __forceinline__ void list_check_tile(const void* grad, uint32_t& bad, double& s)
+// TILES whole, aligned tiles at `grad`: every load before the arithmetic.
+template <int GF, bool SUMSQ, int TILES>
+__device__ __forceinline__ void list_check_tiles(const void* grad, uint32_t& bad, double& s)
 {
     constexpr int kPer = GF == kF32 ? 4 : 8;
-    constexpr int kVecs = static_cast<int>(kListTile) / (kListBlock * kPer);
+    constexpr int kVecs = TILES * static_cast<int>(kListTile) / (kListBlock * kPer);
     const u32x4* G = static_cast<const u32x4*>(grad) + threadIdx.x;
     u32x4 w[kVecs];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
-        w[j] = G[j * kListBlock];
+        w[j] = gload(G + j * kListBlock);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
         if constexpr (SUMSQ)
@@ -97,7 +128,29 @@ __device__ __forceinline__ void list_check_tile(const void* grad, uint32_t& bad,
     }
 }
 
-// One tile per block and loop turn; with SUMSQ its sum goes to part[tile].
+// Tile `left` elements from its tensor's end (whole and aligned, or not).
+template <bool SUMSQ>
+__device__ __forceinline__ void list_check_tile(const unsigned char* g, int gf, int64_t left, uint32_t& bad, double& s)
+{
+    if (left >= kListTile && (reinterpret_cast<uintptr_t>(g) & 15) == 0) {
+        if (gf == kF32)
+            list_check_tiles<kF32, SUMSQ, 1>(g, bad, s);
+        else if (gf == kBF16)
+            list_check_tiles<kBF16, SUMSQ, 1>(g, bad, s);
+        else
+            list_check_tiles<kF16, SUMSQ, 1>(g, bad, s);
+    } else {
+        for (int64_t i = threadIdx.x; i < left && i < kListTile; i += kListBlock) {
+            const float x = list_grad1(gf, g, i);
+            bad |= nonfinite_f32(__float_as_uint(x));
+            if constexpr (SUMSQ)
+                s = s + sq(x);
+        }
+    }
+}
+
+// A group of four tiles per block and loop turn; with SUMSQ its sum goes to
+// part[group].  Four whole tiles of one 16-bit tensor go at once.
 template <bool SUMSQ>
 __global__ __launch_bounds__(kListBlock) void list_check_kernel(ds_scaler* __restrict__ st,
                                                                 const unsigned char* __restrict__ table,
@@ -107,34 +160,33 @@ __global__ __launch_bounds__(kListBlock) void list_check_kernel(ds_scaler* __res
     __shared__ double lds[2 * (kListBlock / 64)];
     const int32_t* tile0 = reinterpret_cast<const int32_t*>(table);
     const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
+    const int groups = (tiles + kCheckTiles - 1) / kCheckTiles;
     uint32_t bad = 0u;
     int parity = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const ListEntry e = entries[list_find(tile0, count, tile)];
-        const int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile;
-        const unsigned char* g = static_cast<const unsigned char*>(e.grad) + base * (e.gf == kF32 ? 4 : 2);
-        const int64_t left = e.n - base;
+    for (int group = blockIdx.x; group < groups; group += gridDim.x) {
+        int tile = group * kCheckTiles;
+        const int end = tile + kCheckTiles < tiles ? tile + kCheckTiles : tiles;
         double s = 0.0;
-        if (left >= kListTile && (reinterpret_cast<uintptr_t>(g) & 15) == 0) {
-            if (e.gf == kF32)
-                list_check_tile<kF32, SUMSQ>(g, bad, s);
-            else if (e.gf == kBF16)
-                list_check_tile<kBF16, SUMSQ>(g, bad, s);
-            else
-                list_check_tile<kF16, SUMSQ>(g, bad, s);
-        } else {
-            for (int64_t i = threadIdx.x; i < left && i < kListTile; i += kListBlock) {
-                const float x = list_grad1(e.gf, g, i);
-                bad |= nonfinite_f32(__float_as_uint(x));
-                if constexpr (SUMSQ)
-                    s = s + sq(x);
+        while (tile < end) {
+            const ListEntry e = entries[list_find(tile0, count, tile)];
+            int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile;
+            const unsigned char* g = static_cast<const unsigned char*>(e.grad) + base * (e.gf == kF32 ? 4 : 2);
+            if (e.gf != kF32 && tile + kCheckTiles == end && e.n - base >= kCheckTiles * kListTile &&
+                (reinterpret_cast<uintptr_t>(g) & 15) == 0) {
+                if (e.gf == kBF16)
+                    list_check_tiles<kBF16, SUMSQ, kCheckTiles>(g, bad, s);
+                else
+                    list_check_tiles<kF16, SUMSQ, kCheckTiles>(g, bad, s);
+                break;
             }
+            for (; tile < end && base < e.n; ++tile, base += kListTile, g += kListTile * (e.gf == kF32 ? 4 : 2))
+                list_check_tile<SUMSQ>(g, e.gf, e.n - base, bad, s);
         }
         if constexpr (SUMSQ) {
             const double ts = block_sum_fixed<kListBlock>(s, lds, parity);
             parity ^= 1;
             if (threadIdx.x == 0)
-                part[tile] = ts;
+                part[group] = ts;
         }
     }
     raise_flag(st, bad);
@@ -161,20 +213,20 @@ constexpr float kTopMax = 0x1p126f;       // above: 1 / top would be subnormal, 
 // formats' exponents become fp32's lowest ones, subnormals with subnormals, so
 // that a step is 2^20 (2^21) units of the pattern everywhere: adding u of
 // those units and dropping as many bits is floor(a / ulp + u).  A NaN keeps
-// its code.
-__device__ __forceinline__ uint32_t code_m(float x, float inv, uint32_t u)
+// its code; blocks without one (`nan` false) skip the test.
+__device__ __forceinline__ uint32_t code_m(float x, float inv, uint32_t u, bool nan)
 {
     const float a = fabsf(x) * inv;
     const uint32_t c = (__float_as_uint(fminf(a, kMaxM) * 0x1p-120f) + u) >> 20;
-    return (a == a ? c : 0x7Fu) | ((__float_as_uint(x) >> 24) & 0x80u);
+    return nan && a != a ? 0x7Fu : c;    // the sign joins in list_encode
 }
 
-__device__ __forceinline__ uint32_t code_v(float x, float inv, uint32_t u)
+__device__ __forceinline__ uint32_t code_v(float x, float inv, uint32_t u, bool nan)
 {
     const float a = x * inv;
     uint32_t c = (__float_as_uint(fminf(a, kMaxV) * 0x1p-112f) + u) >> 21;
     c = x > 0.0f && c == 0u ? 1u : c;
-    return a == a ? c : 0x7Fu;
+    return nan && a != a ? 0x7Fu : c;
 }
 
 __device__ __forceinline__ f32x4 decode_m(uint32_t w)
@@ -195,10 +247,11 @@ __device__ __forceinline__ f32x4 decode_v(uint32_t w)
 // the maxNum of the lanes' own maxima).
 __device__ __forceinline__ float wave_top(float x)
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1)
-        x = fmaxf(x, __shfl_xor(x, off));
-    return x;
+    x = row_max<16>(x);
+    const int b = __float_as_int(x);     // rows of 16 lanes; non-negative floats order as integers
+    const int r01 = max(__builtin_amdgcn_readlane(b, 0), __builtin_amdgcn_readlane(b, 16));
+    const int r23 = max(__builtin_amdgcn_readlane(b, 32), __builtin_amdgcn_readlane(b, 48));
+    return __int_as_float(max(r01, r23));
 }
 
 // ---- Adam ----
@@ -213,14 +266,28 @@ struct ListHyper {
 struct ListStep {
     AdamConsts c;           // step_size and lrwd of the tensor at hand
     float lr;
+    double om1;             // 1 - beta1^t
     uint32_t key;           // dither key of the step
 };
 
-__device__ __forceinline__ void list_tensor_consts(const ds_scaler* st, const ListHyper& hp, const ListEntry& e,
-                                                   ListStep& q)
+__device__ __forceinline__ ListStep list_step(const ds_scaler* st, const ListHyper& hp)
+{
+    ListStep q;
+    q.c = make_consts(st, hp.h);
+    q.c.omb1 = static_cast<float>(1.0 - hp.beta1);
+    q.c.omb2 = static_cast<float>(1.0 - hp.beta2);
+    q.lr = step_lr(st, hp.h);
+    double om2;
+    bias_powers(st->step + 1, hp.beta1, hp.beta2, &q.om1, &om2);
+    q.c.rbc2 = static_cast<float>(1.0 / sqrt(om2));
+    q.key = dither_mix(hp.seed + static_cast<uint32_t>(st->step + 1) * kGold);
+    return q;
+}
+
+__device__ __forceinline__ void list_tensor_consts(const ListEntry& e, ListStep& q)
 {
     const float lr = q.lr * e.lr_scale;
-    bias_scalars(st->step + 1, lr, hp.beta1, hp.beta2, &q.c.step_size, &q.c.rbc2);
+    q.c.step_size = static_cast<float>(static_cast<double>(lr) / q.om1);
     q.c.lrwd = lr * e.weight_decay;
 }
 
@@ -248,177 +315,274 @@ __device__ __forceinline__ void list_encode(const f32x4& m, const f32x4& v, uint
     s_v = tv >= kTopMin ? tv * (1.0f / kMaxV) : 0.0f;
     const uint32_t lane = 4u * __lane_id() * kGold;
     const uint32_t a = key + lane, b = dither_mix(key ^ kMixB) + lane;
-    cm = cv = 0u;
+    // a NaN anywhere shows in the sum (as may infinities of both signs)
+    const float sum = ((m.x + m.y) + (m.z + m.w)) + ((v.x + v.y) + (v.z + v.w));
+    const bool nan = __ballot(sum != sum) != 0ull;
+    uint32_t c[4], d[4];
 #pragma unroll
     for (uint32_t k = 0; k < 4; ++k) {
-        const uint32_t um = DITHER ? (a + k * kGold) >> 12 : 1u << 19;
-        const uint32_t uv = DITHER ? (b + k * kGold) >> 11 : 1u << 20;
-        cm |= code_m(m[k], im, um) << (8 * k);
-        cv |= code_v(v[k], iv, uv) << (8 * k);
+        c[k] = code_m(m[k], im, DITHER ? (a + k * kGold) >> 12 : 1u << 19, false);
+        d[k] = code_v(v[k], iv, DITHER ? (b + k * kGold) >> 11 : 1u << 20, false);
     }
+    if (nan) {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+            c[k] = code_m(m[k], im, DITHER ? (a + k * kGold) >> 12 : 1u << 19, true);
+            d[k] = code_v(v[k], iv, DITHER ? (b + k * kGold) >> 11 : 1u << 20, true);
+        }
+    }
+    cm = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+    cv = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
+    // signs: the top bits of the values' top bytes
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(m.y), __float_as_uint(m.x), 0x0C0C0703u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(m.w), __float_as_uint(m.z), 0x07030C0Cu);
+    cm |= (lo | hi) & 0x80808080u;
 }
 
-// A whole, aligned tile: vectors of four, every load before the arithmetic.
-template <bool E8, bool DITHER, bool NT>
-__device__ __forceinline__ void list_tile(const ListEntry& e, int64_t base, const AdamConsts& c, uint32_t key)
+// One element with 8-bit states: adam1 with the hardware's square root and
+// reciprocal (each within 1 unit) and fused multiply-adds in the parameter's
+// part.  Its states' arithmetic is adam1's, rounding by rounding.  The IEEE
+// forms take about 20 of some 70 instructions per element here, where they,
+// not the memory, would set the pace.
+__device__ __forceinline__ void adam1_fp8(float graw, float& p, float& m, float& v, const AdamConsts& c)
+{
+    const float g = graw * c.inv;
+    const float m1 = c.b1 * m, m2 = c.omb1 * g;
+    m = m1 + m2;
+    const float gg = g * g, v1 = c.b2 * v, v2 = c.omb2 * gg;
+    v = v1 + v2;
+    // at least the smallest normal number: the reciprocal of a smaller one is infinite
+    const float den = fmaxf(__builtin_fmaf(__builtin_amdgcn_sqrtf(v), c.rbc2, c.eps), 0x1p-126f);
+    p = __builtin_fmaf(-c.lrwd, p, p);
+    p = __builtin_fmaf(-c.step_size, m * __builtin_amdgcn_rcpf(den), p);
+}
+
+// One tile's data in registers: four quads per lane.
+template <bool E8>
+struct ListRegs {
+    f32x4 g[kListQuads], p[kListQuads], m[kListQuads], v[kListQuads];
+};
+
+template <>
+struct ListRegs<true> {
+    f32x4 g[kListQuads], p[kListQuads];
+    uint32_t m[kListQuads], v[kListQuads];
+    float m_scale[kListQuads], v_scale[kListQuads];
+};
+
+// Scale block of the wave's quad u in the tile at element `base`.
+__device__ __forceinline__ int64_t list_block(int64_t base, int u)
+{
+    return base / DS_STATE_BLOCK + u * (kListBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+}
+
+// Loads of a tile.  FULL: whole and aligned, vectors of four throughout.
+// Else quad by quad: a vector where the tensor is aligned and the quad whole,
+// single elements otherwise, zeros past the end (so that a short block's top
+// is right).
+template <bool E8, bool NT, bool FULL>
+__device__ __forceinline__ void list_load(const ListEntry& e, int64_t base, ListRegs<E8>& r)
 {
     constexpr int U = kListQuads;
     const int64_t q0 = base / 4 + threadIdx.x;
-    f32x4* P = reinterpret_cast<f32x4*>(e.master) + q0;
-    f32x4 g[U], p[U], m[U], v[U];
-    uint32_t mc[U], vc[U];
-    float ms[U], vs[U];
-    const int64_t blk0 = base / DS_STATE_BLOCK + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        p[u] = load<NT>(P + u * kListBlock);
+        const int64_t q = q0 + u * kListBlock;
         if constexpr (E8) {
-            mc[u] = load<NT>(static_cast<const uint32_t*>(e.m) + q0 + u * kListBlock);
-            vc[u] = load<NT>(static_cast<const uint32_t*>(e.v) + q0 + u * kListBlock);
-            ms[u] = e.m_scale[blk0 + u * (kListBlock / 64)];
-            vs[u] = e.v_scale[blk0 + u * (kListBlock / 64)];
+            const int64_t blk = list_block(base, u);
+            const bool in = FULL || blk * DS_STATE_BLOCK < e.n;
+            r.m_scale[u] = in ? gload(e.m_scale + blk) : 0.0f;
+            r.v_scale[u] = in ? gload(e.v_scale + blk) : 0.0f;
+        }
+        if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
+            r.p[u] = gload<NT>(reinterpret_cast<const f32x4*>(e.master) + q);
+            if constexpr (E8) {
+                r.m[u] = gload<NT>(static_cast<const uint32_t*>(e.m) + q);
+                r.v[u] = gload<NT>(static_cast<const uint32_t*>(e.v) + q);
+            } else {
+                r.m[u] = gload<NT>(static_cast<const f32x4*>(e.m) + q);
+                r.v[u] = gload<NT>(static_cast<const f32x4*>(e.v) + q);
+            }
         } else {
-            m[u] = load<NT>(static_cast<const f32x4*>(e.m) + q0 + u * kListBlock);
-            v[u] = load<NT>(static_cast<const f32x4*>(e.v) + q0 + u * kListBlock);
+            r.p[u] = f32x4{0, 0, 0, 0};
+            r.m[u] = r.v[u] = {};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = 4 * q + k;
+                if (i < e.n) {
+                    r.p[u][k] = gload(e.master + i);
+                    if constexpr (E8) {
+                        r.m[u] |= static_cast<uint32_t>(gload(static_cast<const uint8_t*>(e.m) + i)) << (8 * k);
+                        r.v[u] |= static_cast<uint32_t>(gload(static_cast<const uint8_t*>(e.v) + i)) << (8 * k);
+                    } else {
+                        r.m[u][k] = gload(static_cast<const float*>(e.m) + i);
+                        r.v[u][k] = gload(static_cast<const float*>(e.v) + i);
+                    }
+                }
+            }
         }
     }
+    // the gradients last: what converts them waits for all of the loads
     if (e.gf == kF32) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            g[u] = load_grad4<kF32, NT>(e.grad, q0 + u * kListBlock);
+        for (int u = 0; u < U; ++u) {
+            const int64_t q = q0 + u * kListBlock;
+            if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
+                r.g[u] = gload<NT>(static_cast<const f32x4*>(e.grad) + q);
+            } else {
+                r.g[u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (4 * q + k < e.n)
+                        r.g[u][k] = gload(static_cast<const float*>(e.grad) + 4 * q + k);
+            }
+        }
     } else {
-        u32x2 w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            w[u] = load<NT>(static_cast<const u32x2*>(e.grad) + q0 + u * kListBlock);
-        if (e.gf == kBF16) {
+        for (int u = 0; u < U; ++u) {
+            const int64_t q = q0 + u * kListBlock;
+            u32x2 w = {0u, 0u};
+            if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
+                w = gload<NT>(static_cast<const u32x2*>(e.grad) + q);
+            } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                g[u] = widen4<kBF16>(w[u]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                g[u] = widen4<kF16>(w[u]);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if constexpr (E8) {
-            m[u] = decode_m(mc[u]) * ms[u];
-            v[u] = decode_v(vc[u]) * vs[u];
-        }
-        list_update(g[u], p[u], m[u], v[u], c.lrwd != 0.0f, c);
-        store<NT>(P + u * kListBlock, p[u]);
-        if constexpr (E8) {
-            const int64_t blk = blk0 + u * (kListBlock / 64);
-            float sm, sv;
-            uint32_t cm, cv;
-            const uint32_t bk = DITHER ? dither_mix(key + static_cast<uint32_t>(blk) * kGold) : 0u;
-            list_encode<DITHER>(m[u], v[u], bk, sm, sv, cm, cv);
-            store<NT>(static_cast<uint32_t*>(e.m) + q0 + u * kListBlock, cm);
-            store<NT>(static_cast<uint32_t*>(e.v) + q0 + u * kListBlock, cv);
-            if (__lane_id() == 0u) {
-                e.m_scale[blk] = sm;
-                e.v_scale[blk] = sv;
+                for (int k = 0; k < 4; ++k)
+                    if (4 * q + k < e.n)
+                        w[k / 2] |= static_cast<uint32_t>(gload(static_cast<const uint16_t*>(e.grad) + 4 * q + k))
+                                    << (16 * (k % 2));
             }
-        } else {
-            store<NT>(static_cast<f32x4*>(e.m) + q0 + u * kListBlock, m[u]);
-            store<NT>(static_cast<f32x4*>(e.v) + q0 + u * kListBlock, v[u]);
+            r.g[u].x = __uint_as_float(w.x);   // widened by list_widen, once every load is on its way
+            r.g[u].y = __uint_as_float(w.y);
         }
-        if (e.pf == kBF16)
-            store<NT>(reinterpret_cast<u32x2*>(e.p16) + q0 + u * kListBlock, narrow4<kBF16>(p[u]));
-        else if (e.pf == kF16)
-            store<NT>(reinterpret_cast<u32x2*>(e.p16) + q0 + u * kListBlock, narrow4<kF16>(p[u]));
     }
 }
 
-// A short or unaligned tile: element by element, the same arithmetic.
-template <bool E8, bool DITHER>
-__device__ __forceinline__ void list_tile_edge(const ListEntry& e, int64_t base, const AdamConsts& c, uint32_t key)
+template <bool E8>
+__device__ __forceinline__ void list_widen(int gf, ListRegs<E8>& r)
 {
+    if (gf == kF32)
+        return;
+#pragma unroll
     for (int u = 0; u < kListQuads; ++u) {
-        const int64_t i0 = base + 4 * (static_cast<int64_t>(u) * kListBlock + threadIdx.x);
-        const int64_t blk = base / DS_STATE_BLOCK + u * (kListBlock / 64) +
-                            __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-        if (blk * DS_STATE_BLOCK >= e.n)   // uniform over the wave
-            break;
-        f32x4 g = {0, 0, 0, 0}, p = {0, 0, 0, 0}, m = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-        float ms = 0.0f, vs = 0.0f;
+        const u32x2 w = {__float_as_uint(r.g[u].x), __float_as_uint(r.g[u].y)};
+        r.g[u] = gf == kBF16 ? widen4<kBF16>(w) : widen4<kF16>(w);
+    }
+}
+
+// Update and stores of a tile loaded by list_load.
+template <bool E8, bool DITHER, bool NT, bool FULL>
+__device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, ListRegs<E8>& r, const AdamConsts& c,
+                                            uint32_t key)
+{
+    const int64_t q0 = base / 4 + threadIdx.x;
+    list_widen<E8>(e.gf, r);
+#pragma unroll
+    for (int u = 0; u < kListQuads; ++u) {
+        const int64_t q = q0 + u * kListBlock, blk = list_block(base, u);
+        if (!FULL && blk * DS_STATE_BLOCK >= e.n)   // uniform over the wave
+            return;
+        f32x4 m, v;
         if constexpr (E8) {
-            ms = e.m_scale[blk];
-            vs = e.v_scale[blk];
+            m = decode_m(r.m[u]) * r.m_scale[u];
+            v = decode_v(r.v[u]) * r.v_scale[u];
+        } else {
+            m = r.m[u];
+            v = r.v[u];
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t i = i0 + k;
-            if (i < e.n) {
-                g[k] = list_grad1(e.gf, e.grad, i);
-                p[k] = e.master[i];
-                if constexpr (E8) {
-                    m[k] = decode_m(static_cast<const uint8_t*>(e.m)[i]).x * ms;
-                    v[k] = decode_v(static_cast<const uint8_t*>(e.v)[i]).x * vs;
-                } else {
-                    m[k] = static_cast<const float*>(e.m)[i];
-                    v[k] = static_cast<const float*>(e.v)[i];
-                }
-            }
-        }
-        list_update(g, p, m, v, c.lrwd != 0.0f, c);
-        float sm = 0.0f, sv = 0.0f;
+        f32x4 p = r.p[u];
         uint32_t cm = 0u, cv = 0u;
-        if constexpr (E8) {   // elements past the end are zero: they raise no top
-            const uint32_t bk = DITHER ? dither_mix(key + static_cast<uint32_t>(blk) * kGold) : 0u;
-            list_encode<DITHER>(m, v, bk, sm, sv, cm, cv);
+        if constexpr (E8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float pk = p[k], mk = m[k], vk = v[k];
+                adam1_fp8(r.g[u][k], pk, mk, vk, c);
+                p[k] = pk, m[k] = mk, v[k] = vk;
+            }
+        } else {
+            list_update(r.g[u], p, m, v, c.lrwd != 0.0f, c);
+        }
+        if constexpr (E8) {
+            float sm, sv;
+            list_encode<DITHER>(m, v, DITHER ? dither_mix(key + static_cast<uint32_t>(blk) * kGold) : 0u, sm, sv, cm,
+                                cv);
             if (__lane_id() == 0u) {
-                e.m_scale[blk] = sm;
-                e.v_scale[blk] = sv;
+                gstore(e.m_scale + blk, sm);
+                gstore(e.v_scale + blk, sv);
             }
         }
+        if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
+            gstore<NT>(reinterpret_cast<f32x4*>(e.master) + q, p);
+            if constexpr (E8) {
+                gstore<NT>(static_cast<uint32_t*>(e.m) + q, cm);
+                gstore<NT>(static_cast<uint32_t*>(e.v) + q, cv);
+            } else {
+                gstore<NT>(static_cast<f32x4*>(e.m) + q, m);
+                gstore<NT>(static_cast<f32x4*>(e.v) + q, v);
+            }
+            if (e.pf == kBF16)
+                gstore<NT>(reinterpret_cast<u32x2*>(e.p16) + q, narrow4<kBF16>(p));
+            else if (e.pf == kF16)
+                gstore<NT>(reinterpret_cast<u32x2*>(e.p16) + q, narrow4<kF16>(p));
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t i = i0 + k;
-            if (i < e.n) {
-                e.master[i] = p[k];
-                if constexpr (E8) {
-                    static_cast<uint8_t*>(e.m)[i] = static_cast<uint8_t>(cm >> (8 * k));
-                    static_cast<uint8_t*>(e.v)[i] = static_cast<uint8_t>(cv >> (8 * k));
-                } else {
-                    static_cast<float*>(e.m)[i] = m[k];
-                    static_cast<float*>(e.v)[i] = v[k];
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = 4 * q + k;
+                if (i < e.n) {
+                    gstore(e.master + i, float(p[k]));
+                    if constexpr (E8) {
+                        gstore(static_cast<uint8_t*>(e.m) + i, static_cast<uint8_t>(cm >> (8 * k)));
+                        gstore(static_cast<uint8_t*>(e.v) + i, static_cast<uint8_t>(cv >> (8 * k)));
+                    } else {
+                        gstore(static_cast<float*>(e.m) + i, float(m[k]));
+                        gstore(static_cast<float*>(e.v) + i, float(v[k]));
+                    }
+                    if (e.pf == kBF16)
+                        gstore(e.p16 + i, static_cast<uint16_t>(enc1<kBF16>(p[k])));
+                    else if (e.pf == kF16)
+                        gstore(e.p16 + i, static_cast<uint16_t>(enc1<kF16>(p[k])));
                 }
-                if (e.pf == kBF16)
-                    e.p16[i] = static_cast<uint16_t>(enc1<kBF16>(p[k]));
-                else if (e.pf == kF16)
-                    e.p16[i] = static_cast<uint16_t>(enc1<kF16>(p[k]));
             }
         }
     }
 }
 
+// One tile per block and loop turn.  The step's constants (fp64 powers and
+// divisions) are formed while the first tile's loads are on their way; the
+// scaler's values that they need are read before anything is written, when
+// scalar loads may serve them (a vector load per wave of the line that the
+// tickets are taken from made the kernel 4.6 times slower).
 template <bool E8, bool DITHER, bool NT, bool FUSE>
 __global__ __launch_bounds__(kListBlock) void list_adam_kernel(ds_scaler* __restrict__ st,
                                                                const unsigned char* __restrict__ table,
                                                                int32_t count, int32_t tiles, ListHyper hp)
 {
+    const int32_t* tile0 = reinterpret_cast<const int32_t*>(table);
+    const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
+    int tile = blockIdx.x;
+    ds_scaler now{};
+    now.scale = st->scale;
+    now.step = st->step;
+    now.grad_sumsq = st->grad_sumsq;
     if (st->overflow == 0u) {
-        const int32_t* tile0 = reinterpret_cast<const int32_t*>(table);
-        const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
         ListStep q;
-        q.c = make_consts(st, hp.h);
-        q.c.omb1 = static_cast<float>(1.0 - hp.beta1);
-        q.c.omb2 = static_cast<float>(1.0 - hp.beta2);
-        q.lr = step_lr(st, hp.h);
-        q.key = dither_mix(hp.seed + static_cast<uint32_t>(st->step + 1) * kGold);
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        for (bool first = true; tile < tiles; tile += gridDim.x, first = false) {
             const int j = list_find(tile0, count, tile);
             const ListEntry e = entries[j];
-            list_tensor_consts(st, hp, e, q);
-            const uint32_t key = DITHER ? dither_mix(q.key + static_cast<uint32_t>(j) * kGold) : 0u;
             const int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile;
-            if (e.vec && e.n - base >= kListTile)
-                list_tile<E8, DITHER, NT>(e, base, q.c, key);
+            const bool full = e.vec && e.n - base >= kListTile;
+            ListRegs<E8> r;
+            if (full)
+                list_load<E8, NT, true>(e, base, r);
             else
-                list_tile_edge<E8, DITHER>(e, base, q.c, key);
+                list_load<E8, false, false>(e, base, r);
+            if (first)
+                q = list_step(&now, hp);
+            list_tensor_consts(e, q);
+            const uint32_t key = DITHER ? dither_mix(q.key + static_cast<uint32_t>(j) * kGold) : 0u;
+            if (full)
+                list_finish<E8, DITHER, NT, true>(e, base, r, q.c, key);
+            else
+                list_finish<E8, DITHER, false, false>(e, base, r, q.c, key);
         }
     }
     if constexpr (FUSE) {
@@ -514,7 +678,14 @@ ds_status list_ok(const ds_tensor_list* l)
     return DS_OK;
 }
 
-uint64_t list_ws_bytes(int64_t tiles) { return 8 * static_cast<uint64_t>(tiles + finish_groups(tiles)); }
+// Partial sums of squares of a list: one per group of tiles.
+int64_t list_parts(int64_t tiles) { return (tiles + kCheckTiles - 1) / kCheckTiles; }
+
+uint64_t list_ws_bytes(int64_t tiles)
+{
+    const int64_t parts = list_parts(tiles);
+    return 8 * static_cast<uint64_t>(parts + finish_groups(parts));
+}
 
 ds_status list_write(ds_tensor_list* list, void* table, size_t table_bytes, const ds_tensor* tensors, int32_t count,
                      ds_dtype sdt, hipStream_t s)
@@ -588,7 +759,7 @@ ds_status list_check(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws
     if (overlap(st, sizeof(ds_scaler), l->table, tb) || overlap(ws, list_ws_bytes(l->tiles), l->table, tb) ||
         overlap(ws, list_ws_bytes(l->tiles), st, sizeof(ds_scaler)))
         return DS_ERR_ALIAS;
-    const unsigned blocks = grid_blocks(l->tiles, kListBlock);
+    const unsigned blocks = grid_blocks(list_parts(l->tiles), kListBlock);
     const unsigned char* table = static_cast<const unsigned char*>(l->table);
     const int32_t tiles = static_cast<int32_t>(l->tiles);
     double* part = static_cast<double*>(ws);
@@ -599,7 +770,7 @@ ds_status list_check(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws
     list_check_kernel<true><<<blocks, kListBlock, 0, s>>>(st, table, l->count, tiles, part);
     if (launched() != DS_OK)
         return DS_ERR_HIP;
-    return launch_finish(st, part, l->tiles, s);
+    return launch_finish(st, part, list_parts(l->tiles), s);
 }
 
 template <bool E8, bool DITHER, bool NT>
@@ -644,11 +815,17 @@ ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, 
     const ListHyper hp{h, beta1, beta2, dither_mix(dither_mix(static_cast<uint32_t>(seed >> 32)) ^ static_cast<uint32_t>(seed))};
     const bool nt = variant_nt(l->elems);
     const unsigned blocks = grid_blocks(l->tiles, kListBlock);
+    const bool fuse = end_step && blocks <= kFuseBlocks;
     if (l->sdt == DS_FP32)
-        launch_list_adam<false, false>(nt, end_step, blocks, s, st, l, hp);
+        launch_list_adam<false, false>(nt, fuse, blocks, s, st, l, hp);
     else if (rounding == DS_ROUND_DITHER)
-        launch_list_adam<true, true>(nt, end_step, blocks, s, st, l, hp);
+        launch_list_adam<true, true>(nt, fuse, blocks, s, st, l, hp);
     else
-        launch_list_adam<true, false>(nt, end_step, blocks, s, st, l, hp);
+        launch_list_adam<true, false>(nt, fuse, blocks, s, st, l, hp);
+    if (end_step && !fuse) {
+        if (launched() != DS_OK)
+            return DS_ERR_HIP;
+        update_scale_kernel<<<1, 1, 0, s>>>(st);
+    }
     return launched();
 }

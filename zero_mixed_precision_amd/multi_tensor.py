@@ -16,14 +16,21 @@ synchronisation; it can be captured into a graph.
 """
 from __future__ import annotations
 
+import ctypes
+
 from . import _lib
 from .config import ZeroMPConfig
 
 ALIGN = _lib.DS_STATE_BLOCK     # elements: where each tensor starts in the flat state arrays
 
 
+_CODES: dict = {}
+
+
 def _dtype_of(t, torch, what):
-    code = {torch.float16: _lib.DS_FP16, torch.bfloat16: _lib.DS_BF16, torch.float32: _lib.DS_FP32}.get(t.dtype)
+    if not _CODES:
+        _CODES.update({torch.float16: _lib.DS_FP16, torch.bfloat16: _lib.DS_BF16, torch.float32: _lib.DS_FP32})
+    code = _CODES.get(t.dtype)
     if code is None:
         raise ValueError(f"{what}: dtype {t.dtype} is not float16, bfloat16 or float32")
     return code
@@ -107,11 +114,14 @@ class MultiTensorStep:
             self.state = state
             if state is None:
                 self.state = torch.zeros(_lib.ds_scaler_size(), dtype=torch.uint8, device=device)
-            self.ws = None
-            if self.clip > 0:                   # one fp64 per tile of 4096 and per 4096 tiles, no initial contents
-                tiles = sum((n + 4095) // 4096 for n in self.numels)
-                self.ws = torch.empty(tiles + tiles // 4096 + 1, dtype=torch.float64, device=device)
             self._table = torch.zeros(max(_lib.ds_tensor_list_bytes(count), 16), dtype=torch.uint8, device=device)
+            self.ws = None
+            if self.clip > 0:                   # of the list that set_gradients() writes; no initial contents
+                tiles = sum((n + 4095) // 4096 for n in self.numels)
+                shape = _lib.DsTensorList(table=self._table.data_ptr(), tiles=tiles, elems=sum(self.numels),
+                                          count=count, sdt=self._sdt)
+                need = _lib.ds_tensor_list_workspace_bytes(shape)
+                self.ws = torch.empty(max(need // 8, 1), dtype=torch.float64, device=device)
         if state is None:
             _lib.ds_state_init(self.state, cfg.init_scale, cfg.min_loss_scale, cfg.loss_scale_window, cfg.hysteresis,
                                int(cfg.consecutive_hysteresis), int(cfg.dynamic), self.stream)
@@ -129,7 +139,12 @@ class MultiTensorStep:
                 t.v_scale = self.v_scale.data_ptr() + 4 * (at // ALIGN)
             t.n, t.weight_decay, t.lr_scale = self.numels[i], decay[i], rates[i]
             t.pdt = _dtype_of(p, torch, f"parameter {i}")
-        self._grads, self._list = None, None
+        self._grads, self._list, self._list_at = None, None, None
+        # what every step passes: this object's own arrays, sized and placed here
+        self._state_at = self.state.data_ptr()
+        self._ws_at = None if self.ws is None else self.ws.data_ptr()
+        self._ws_bytes = 0 if self.ws is None else self.ws.numel() * 8
+        self._sched_at = None if self.sched is None else ctypes.byref(self.sched)
 
     def _torch_stream(self):
         from .checkpoint import torch_stream
@@ -157,20 +172,19 @@ class MultiTensorStep:
         self._list = None
         tensors = self._tensors if grads else []
         self._list = _lib.ds_tensor_list_write(self._table, tensors, self._sdt, self.stream)
+        self._list_at = ctypes.byref(self._list)
         self._grads = grads
 
     def step(self) -> None:
         """One step on the gradients set: overflow check (with the joint norm if clipped), gated Adam, scaler."""
         if self._list is None:
             raise RuntimeError("set_gradients() before step()")
-        c = self.cfg
-        st = self.state.data_ptr()
-        if self.ws is not None:
-            _lib.ds_check_overflow_list(st, self._list, self.ws, stream=self.stream)
-        else:
-            _lib.ds_check_overflow_list(st, self._list, stream=self.stream)
-        _lib.ds_adam_step_list(st, self._list, c.lr, self.sched, c.betas[0], c.betas[1], c.eps, c.gradient_clipping,
-                               c.gradient_accumulation_steps, self._rounding, self._seed, self.end_step, self.stream)
+        c, lib, ok, s = self.cfg, _lib.lib, _lib._ok, _lib._s(self.stream)
+        st, lst = self._state_at, self._list_at
+        ok(lib.ds_check_overflow_list(st, lst, self._ws_at, self._ws_bytes, s), "ds_check_overflow_list")
+        ok(lib.ds_adam_step_list(st, lst, c.lr, self._sched_at, c.betas[0], c.betas[1], c.eps, c.gradient_clipping,
+                                 c.gradient_accumulation_steps, self._rounding, self._seed, self.end_step, s),
+           "ds_adam_step_list")
 
     def scaler(self) -> _lib.DsScaler:
         return _lib.ds_state_read(self.state, self.stream)
@@ -200,8 +214,6 @@ class MultiTensorStep:
 
     def state_dict(self) -> dict:
         """Host copies of the states, masters and scaler (the parameters themselves are the caller's)."""
-        import ctypes
-
         sc = self.scaler()                      # synchronises the step's stream
         raw = ctypes.string_at(ctypes.addressof(sc), ctypes.sizeof(sc))
         torch = self.torch
