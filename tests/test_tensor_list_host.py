@@ -48,7 +48,7 @@ def test_structs():
 def test_table_bytes():
     assert _lib.ds_tensor_list_bytes(0) == 0 and L.ds_tensor_list_bytes(-1) == 0
     for count in (1, 4, 5, 1000):
-        assert _lib.ds_tensor_list_bytes(count) == -(-4 * count // 16) * 16 + 96 * count
+        assert _lib.ds_tensor_list_bytes(count) == 64 * 128 + -(-4 * count // 16) * 16 + 96 * count
 
 
 def test_an_empty_list_is_written_without_a_launch():

@@ -250,6 +250,22 @@ def _s(stream):
     return stream.cuda_stream
 
 
+_raw_stream = None
+
+
+def _stream_on(stream, device_index: int) -> int:
+    """The hipStream_t of ``stream``; None is torch's current stream of that device.  torch's own accessor of the raw
+    handle takes 0.1 us, building its Stream object 2.8 us of a small call's 8."""
+    global _raw_stream
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device_index)
+
+
 def _ok(rc: int, where: str) -> None:
     if rc != DS_OK:
         raise DsError(rc, where)

@@ -37,6 +37,7 @@ class ExpertBalance:
             # enough for any number of tokens (2.1 MB for 512 experts)
             need = _lib.ds_balance_workspace_bytes(1 << 30, self.E)
             self._ws = torch.empty((need + 7) // 8, dtype=torch.float64, device=device)
+        self._device = self.counts.device.index
         self._at = (self.counts.data_ptr(), self.mean_prob.data_ptr(), self.value.data_ptr(), self.used.data_ptr(),
                     self._ws.data_ptr(), self._ws.numel() * 8)
 
@@ -75,7 +76,7 @@ class ExpertBalance:
         T = logits.shape[0]
         counts, mean, value, used, ws, ws_bytes = self._at
         _lib._ok(_lib.lib.ds_balance_loss(z, dt, T, self.E, stride, self._mask(mask, T), self.k, self.coef, counts, mean,
-                                          value, used, ws, ws_bytes, _lib._s(self.stream)), "ds_balance_loss")
+                                          value, used, ws, ws_bytes, _lib._stream_on(self.stream, self._device)), "ds_balance_loss")
         return self.value
 
     def gradient(self, logits, out, mask=None, scaler=None, accumulate=False):
@@ -89,5 +90,5 @@ class ExpertBalance:
         T = logits.shape[0]
         _lib._ok(_lib.lib.ds_balance_loss_grad(_lib._scaler(scaler), z, dt, T, self.E, stride, self._mask(mask, T),
                                                self.k, self.coef, self._at[0], self._at[3], d, gstride, accumulate,
-                                               _lib._s(self.stream)), "ds_balance_loss_grad")
+                                               _lib._stream_on(self.stream, self._device)), "ds_balance_loss_grad")
         return out

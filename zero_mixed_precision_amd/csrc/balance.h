@@ -31,32 +31,55 @@ struct BalWork {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// The lane's V logits of one row (absent experts: -infinity).
+// The lane's V logits of one row (a row that is off, and absent experts:
+// -infinity).  Either kind of access is one run of loads, converted once they
+// are all on their way.
 template <int GF, int G, int V>
-__device__ __forceinline__ void bal_load(const void* row, const BalShape& s, int g, float (&z)[V])
+__device__ __forceinline__ void bal_load(const void* row, const BalShape& s, int g, bool on, float (&z)[V])
 {
+    if (s.vec) {
+        if constexpr (GF == kF32) {
+            f32x4 x[V / 4];
 #pragma unroll
-    for (int c = 0; c < V / 4; ++c) {
-        const int e0 = 4 * (c * G + g);
-        if (s.vec && e0 + 4 <= s.experts) {
-            f32x4 x;
-            if constexpr (GF == kF32)
-                x = *reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + e0);
-            else
-                x = widen4<GF>(*reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(row) + e0));
+            for (int c = 0; c < V / 4; ++c) {
+                x[c] = f32x4{kNegInf, kNegInf, kNegInf, kNegInf};
+                if (on && 4 * (c * G + g) < s.experts)
+                    x[c] = static_cast<const f32x4*>(row)[c * G + g];
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                z[4 * c + j] = x[j];
+            for (int v = 0; v < V; ++v)
+                z[v] = x[v / 4][v % 4];
         } else {
+            u32x2 x[V / 4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                z[4 * c + j] = e0 + j < s.experts ? load_grad1<GF>(row, e0 + j) : kNegInf;
+            for (int c = 0; c < V / 4; ++c) {
+                constexpr uint32_t kNone = GF == kBF16 ? 0xFF80FF80u : 0xFC00FC00u;
+                x[c] = u32x2{kNone, kNone};
+                if (on && 4 * (c * G + g) < s.experts)
+                    x[c] = static_cast<const u32x2*>(row)[c * G + g];
+            }
+#pragma unroll
+            for (int c = 0; c < V / 4; ++c) {
+                const f32x4 y = widen4<GF>(x[c]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    z[4 * c + j] = y[j];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 4 * ((v / 4) * G + g) + v % 4;
+            z[v] = kNegInf;
+            if (on && e < s.experts)
+                z[v] = load_grad1<GF>(row, e);
         }
     }
 }
 
 // z becomes exp(z - max); returns 1 / sum.  `top` is the row's maximum (NaN
 // left out); a NaN or +infinity in the row makes the sum, so 1 / sum, NaN.
+// A row that is not used passes top 0 and comes back as zeros.
 template <int G, int V>
 __device__ __forceinline__ float bal_softmax(float (&z)[V], float top)
 {
@@ -90,8 +113,9 @@ __device__ __forceinline__ bool bal_used(const float (&z)[V], float top)
     return top > kNegInf || row_sum_int<G>(any) != 0;
 }
 
-// The KK largest of two lanes' falling lists, falling.
-template <int OFF, int KK>
+// The KK largest of two lanes' falling lists: rising then falling, and sorted
+// if SORT.
+template <int OFF, int KK, bool SORT>
 __device__ __forceinline__ void bal_merge(float (&best)[KK])
 {
     float other[KK];
@@ -99,28 +123,33 @@ __device__ __forceinline__ void bal_merge(float (&best)[KK])
     for (int i = 0; i < KK; ++i)
         other[i] = row_other<OFF>(best[i]);
 #pragma unroll
-    for (int i = 0; i < KK; ++i)       // the KK largest of both, rising then falling
+    for (int i = 0; i < KK; ++i)
         best[i] = fmaxf(best[i], other[KK - 1 - i]);
+    if constexpr (SORT) {
 #pragma unroll
-    for (int d = KK / 2; d > 0; d >>= 1)
+        for (int d = KK / 2; d > 0; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < KK; ++i)
-            if ((i & d) == 0) {
-                const float hi = fmaxf(best[i], best[i + d]), lo = fminf(best[i], best[i + d]);
-                best[i] = hi;
-                best[i + d] = lo;
-            }
+            for (int i = 0; i < KK; ++i)
+                if ((i & d) == 0) {
+                    const float hi = fmaxf(best[i], best[i + d]), lo = fminf(best[i], best[i + d]);
+                    best[i] = hi;
+                    best[i + d] = lo;
+                }
+    }
 }
 
-// KK largest of the row in falling order, the same in each of its G lanes:
-// first of the lane's own values (insertion, one median per place), then by
-// merging the lists of lanes 1, 2, 4 .. apart.
+// The k-th largest of the row, the same in each of its G lanes.  Every lane
+// keeps the KK largest of its own values in falling order (insertion, one
+// median per place), the lists of lanes 1, 2, 4 .. apart are merged, and the
+// smallest of the last merge is it: the row's first lane starts with KK - k
+// infinities, so that the KK-th largest is the k-th of the row.
 template <int G, int V, int KK>
-__device__ __forceinline__ void bal_largest(const float (&z)[V], float (&best)[KK])
+__device__ __forceinline__ float bal_cut(const float (&z)[V], int k, int g)
 {
+    float best[KK];
 #pragma unroll
     for (int i = 0; i < KK; ++i)
-        best[i] = kNegInf;
+        best[i] = g == 0 && i < KK - k ? -kNegInf : kNegInf;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
@@ -128,11 +157,18 @@ __device__ __forceinline__ void bal_largest(const float (&z)[V], float (&best)[K
             best[i] = __builtin_amdgcn_fmed3f(best[i - 1], best[i], z[v]);
         best[0] = fmaxf(best[0], z[v]);
     }
-    bal_merge<1, KK>(best);
-    bal_merge<2, KK>(best);
-    bal_merge<4, KK>(best);
-    if constexpr (G == 16)
-        bal_merge<8, KK>(best);
+    bal_merge<1, KK, true>(best);
+    bal_merge<2, KK, true>(best);
+    bal_merge<4, KK, (G > 8)>(best);
+    if constexpr (G > 8)
+        bal_merge<8, KK, (G > 16)>(best);
+    if constexpr (G > 16)
+        bal_merge<16, KK, false>(best);
+    float cut = best[0];
+#pragma unroll
+    for (int i = 1; i < KK; ++i)
+        cut = fminf(cut, best[i]);
+    return cut;
 }
 
 // What the forward pass leaves, and what it is scaled by.
@@ -170,8 +206,9 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
 {
     constexpr int kRows = 64 / G;          // rows of a wave
     constexpr int kWaves = kBalBlock / 64;
-    __shared__ int32_t lds_count[kWaves][G * V];
-    __shared__ float lds_prob[kWaves][G * V];
+    constexpr int kSpan = G > 16 ? G : 16; // lanes whose sums share a row of the shared arrays
+    __shared__ int32_t lds_count[kBalBlock / kSpan][G * V];
+    __shared__ float lds_prob[kBalBlock / kSpan][G * V];
     __shared__ int32_t lds_used[kWaves];
     __shared__ double lds_loss[2 * kWaves];
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64, g = lane % G;
@@ -191,87 +228,82 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
         if (on && mask != nullptr)
             on = mask[t] != 0;
         float z[V];
-        if (on) {
-            bal_load<GF, G, V>(static_cast<const unsigned char*>(logits) + t * s.stride * es, s, g, z);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                z[v] = kNegInf;
-        }
-        const float top = bal_top<G, V>(z);
-        on = on && bal_used<G, V>(z, top);
-        float best[KK];
-        bal_largest<G, V, KK>(z, best);
-        float cut = best[0];               // the k-th largest
-#pragma unroll
-        for (int i = 1; i < KK; ++i)
-            cut = i == s.k - 1 ? best[i] : cut;
-        // rows above the cut are chosen; of those equal to it as many as are
-        // left of k, the lowest indices first
-        int above = 0;
-#pragma unroll
-        for (int i = 0; i < KK; ++i)
-            above += i < s.k && best[i] > cut ? 1 : 0;
-        const int want = cut > kNegInf ? s.k - above : 0;
-        int equal = 0;
+        bal_load<GF, G, V>(static_cast<const unsigned char*>(logits) + t * s.stride * es, s, g, on, z);
+        float top = bal_top<G, V>(z);
+        if (__ballot(on && !(top > kNegInf)) != 0ull)
+            on = on && bal_used<G, V>(z, top);
+        float cut = bal_cut<G, V, KK>(z, s.k, g);
+        cut = fmaxf(cut, -3.402823466e+38f);   // -infinity is never chosen
+        uint32_t chosen = 0u;              // bit V - 1 - v: the lane's value v
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            equal += z[v] == cut ? 1 : 0;
-        equal = row_sum_int<G>(equal);
-        uint32_t chosen = 0u;              // bit v: the lane's value v is chosen
-        if (__ballot(on && equal != want) == 0ull) {
+            chosen = chosen + chosen + (z[v] >= cut ? 1u : 0u);
+        // more than k of them: of those equal to the cut the highest indices go
+        int over = on ? row_sum_int<G>(__popc(chosen)) - s.k : 0;
+        if (__ballot(over > 0) != 0ull) {
+            uint32_t equal = 0u;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                chosen |= z[v] >= cut && z[v] > kNegInf ? 1u << v : 0u;
-        } else {
-            int left = want;
-#pragma unroll
-            for (int c = 0; c < V / 4; ++c) {
-                int mine = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mine += z[4 * c + j] == cut ? 1 : 0;
-                int before = mine;         // inclusive prefix over the row's lanes
-#pragma unroll
-                for (int off = 1; off < G; off <<= 1) {
-                    const int x = __shfl_up(before, off, G);
-                    before += g >= off ? x : 0;
+                equal = equal + equal + (z[v] == cut ? 1u : 0u);
+            if (__ballot(over > 3) == 0ull) {
+                while (__ballot(over > 0) != 0ull) {   // at most three turns
+                    const int v = V - __ffs(static_cast<int>(equal));
+                    const int e = equal != 0u ? 4 * ((v / 4) * G + g) + v % 4 : -1;
+                    if (over > 0 && e == row_max_int<G>(e)) {
+                        chosen &= ~(equal & -equal);
+                        equal &= equal - 1u;
+                    }
+                    over -= 1;
                 }
-                const int all = __shfl(before, G - 1, G);
-                int rank = before - mine;
+            } else {
+                // by ranks: chunk by chunk, the number of equal ones before a lane's own
+                int left = row_sum_int<G>(__popc(equal)) - (over > 0 ? over : 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool tie = z[4 * c + j] == cut;
-                    if ((tie && rank < left) || (z[4 * c + j] > cut))
-                        chosen |= 1u << (4 * c + j);
-                    rank += tie ? 1 : 0;
+                for (int c = 0; c < V / 4; ++c) {
+                    const uint32_t mine = (equal >> (V - 4 - 4 * c)) & 15u;
+                    int before = __popc(mine);         // inclusive prefix over the row's lanes
+#pragma unroll
+                    for (int off = 1; off < G; off <<= 1) {
+                        const int x = __shfl_up(before, off, G);
+                        before += g >= off ? x : 0;
+                    }
+                    const int all = __shfl(before, G - 1, G);
+                    int rank = before - __popc(mine);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t bit = 8u >> j;
+                        if ((mine & bit) != 0u && rank >= left)
+                            chosen &= ~(bit << (V - 4 - 4 * c));
+                        rank += (mine & bit) != 0u ? 1 : 0;
+                    }
+                    left -= all;
                 }
-                left = left > all ? left - all : 0;
             }
         }
-        const float inv = bal_softmax<G, V>(z, top);
-        if (on) {
-            used += 1;
-            const bool fine = inv == inv;
+        float inv = bal_softmax<G, V>(z, on ? top : 0.0f);
+        if (!on)
+            inv = 0.0f;
+        if (!on || inv != inv)             // a row with a NaN or +infinity counts nothing
+            chosen = 0u;
+        used += on ? 1 : 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                prob[v] = prob[v] + z[v] * inv;
-                cnt[v] += fine && ((chosen >> v) & 1u) ? 1 : 0;
-            }
+        for (int v = 0; v < V; ++v) {
+            prob[v] = __builtin_fmaf(z[v], inv, prob[v]);
+            cnt[v] += static_cast<int>((chosen >> (V - 1 - v)) & 1u);
         }
     }
-    // rows of the wave, then waves of the block, in a fixed order
+    // lanes of the same experts: in a row of 16 lanes by a rotation, then the
+    // block's rows and waves through shared memory, in a fixed order
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int off = G; off < 64; off <<= 1) {
-            cnt[v] += __shfl_xor(cnt[v], off);
-            prob[v] = prob[v] + __shfl_xor(prob[v], off);
+        if constexpr (G == 8) {
+            cnt[v] += static_cast<int>(row_half(static_cast<uint32_t>(cnt[v])));
+            prob[v] = prob[v] + row_half(prob[v]);
         }
-        if (lane < G) {
+        if (G > 8 || lane % 16 < 8) {
             const int e = 4 * ((v / 4) * G + g) + v % 4;
-            lds_count[wave][e] = cnt[v];
-            lds_prob[wave][e] = prob[v];
+            lds_count[threadIdx.x / kSpan][e] = cnt[v];
+            lds_prob[threadIdx.x / kSpan][e] = prob[v];
         }
     }
 #pragma unroll
@@ -289,13 +321,13 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
         int n = 0;
         float p = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
+        for (int i = 0; i < kBalBlock / kSpan; ++i) {
             n += lds_count[i][e];
             p = p + lds_prob[i][e];
         }
         if (gridDim.x > 1) {
-            w.count[static_cast<int64_t>(blockIdx.x) * s.experts + e] = n;
-            w.prob[static_cast<int64_t>(blockIdx.x) * s.experts + e] = p;
+            w.count[blockIdx.x * s.experts + e] = n;
+            w.prob[blockIdx.x * s.experts + e] = p;
         } else {
             part = part + bal_expert(o, s.k, rows, e, n, static_cast<double>(p));
         }
@@ -311,18 +343,22 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
     }
 }
 
-// Sums the partial rows: 16 experts per block, 64 groups of rows, fp64.  The
-// block that finishes last adds the blocks' parts of the loss in order.
+// Sums the partial rows: COLS experts per block, 1024 / COLS groups of rows,
+// fp64.  The block that finishes last adds the blocks' parts of the loss in
+// order; one block of 64 columns, without that meeting, does up to 64 experts
+// (128 partial rows of 64: 5.8 us by four blocks of 16).
+template <int COLS>
 __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t parts, int32_t experts, int32_t k,
                                                                          BalWork w, BalOut o)
 {
-    constexpr int kGroups = kBalFinishBlock / kBalFinishCols, kWaves = kBalFinishBlock / 64, kDeep = 8;
-    __shared__ double lds_prob[kWaves][kBalFinishCols];
-    __shared__ int32_t lds_count[kWaves][kBalFinishCols];
+    constexpr int kGroups = kBalFinishBlock / COLS, kWaves = kBalFinishBlock / 64;
+    constexpr int kDeep = 10;
+    __shared__ double lds_prob[kWaves][COLS];
+    __shared__ int32_t lds_count[kWaves][COLS];
     __shared__ int32_t lds_used[kWaves];
-    const int col = threadIdx.x % kBalFinishCols, group = threadIdx.x / kBalFinishCols;
+    const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
-    const int e = blockIdx.x * kBalFinishCols + col;
+    const int e = blockIdx.x * COLS + col;
     int rows = 0;
     for (int i = threadIdx.x; i < parts; i += kBalFinishBlock)
         rows += w.used[i];
@@ -335,8 +371,8 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
         for (int u = 0; u < kDeep; ++u) {
             const int i = i0 + u * kGroups;
             const bool in = i < parts && e < experts;
-            c[u] = in ? w.count[static_cast<int64_t>(i) * experts + e] : 0;
-            q[u] = in ? w.prob[static_cast<int64_t>(i) * experts + e] : 0.0f;
+            c[u] = in ? w.count[i * experts + e] : 0;
+            q[u] = in ? w.prob[i * experts + e] : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < kDeep; ++u) {
@@ -345,14 +381,14 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
         }
     }
 #pragma unroll
-    for (int off = kBalFinishCols; off < 64; off <<= 1) {
+    for (int off = COLS; off < 64; off <<= 1) {
         n += __shfl_xor(n, off);
         p = p + __shfl_xor(p, off);
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1)
         rows += __shfl_xor(rows, off);
-    if (lane < kBalFinishCols) {
+    if (lane < COLS) {
         lds_count[wave][col] = n;
         lds_prob[wave][col] = p;
     }
@@ -370,9 +406,9 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
         n += lds_count[i][col];
         p = p + lds_prob[i][col];
     }
-    double part = lane < kBalFinishCols && e < experts ? bal_expert(o, k, rows, e, n, p) : 0.0;
+    double part = lane < COLS && e < experts ? bal_expert(o, k, rows, e, n, p) : 0.0;
 #pragma unroll
-    for (int off = 1; off < kBalFinishCols; off <<= 1)
+    for (int off = 1; off < COLS; off <<= 1)
         part = part + __shfl_xor(part, off);
     if (lane != 0)
         return;
@@ -389,15 +425,38 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
     bal_end(o, experts, rows, part);
 }
 
-template <int GF, bool ACC>
-__device__ __forceinline__ void bal_store1(void* row, int e, float d)
+// The lane's V values into (or, with ACC, added to) one row.
+template <int GF, int G, int V, bool ACC>
+__device__ __forceinline__ void bal_store(void* row, int experts, int32_t vec, int g, const float (&d)[V])
 {
-    if constexpr (GF == kF32) {
-        float* p = static_cast<float*>(row) + e;
-        *p = ACC ? *p + d : d;
+    if (vec) {
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) {
+            if (4 * (c * G + g) < experts) {
+                f32x4 x = {d[4 * c], d[4 * c + 1], d[4 * c + 2], d[4 * c + 3]};
+                if constexpr (GF == kF32) {
+                    f32x4* p = static_cast<f32x4*>(row) + c * G + g;
+                    *p = ACC ? *p + x : x;
+                } else {
+                    u32x2* p = static_cast<u32x2*>(row) + c * G + g;
+                    *p = narrow4<GF>(ACC ? widen4<GF>(*p) + x : x);
+                }
+            }
+        }
     } else {
-        uint16_t* p = static_cast<uint16_t*>(row) + e;
-        *p = static_cast<uint16_t>(enc1<GF>(ACC ? dec1<GF>(*p) + d : d));
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 4 * ((v / 4) * G + g) + v % 4;
+            if (e < experts) {
+                if constexpr (GF == kF32) {
+                    float* p = static_cast<float*>(row) + e;
+                    *p = ACC ? *p + d[v] : d[v];
+                } else {
+                    uint16_t* p = static_cast<uint16_t*>(row) + e;
+                    *p = static_cast<uint16_t>(enc1<GF>(ACC ? dec1<GF>(*p) + d[v] : d[v]));
+                }
+            }
+        }
     }
 }
 
@@ -422,23 +481,23 @@ __global__ __launch_bounds__(kBalBlock) void balance_grad_kernel(const ds_scaler
     const double some = rows > 0 ? static_cast<double>(rows) : 1.0;
     const float factor =
         rows > 0 ? static_cast<float>(scale * static_cast<double>(coef) * static_cast<double>(s.experts) / some) : 0.0f;
+    // f less its mean: (E c_e - sum c) / (E k T'), the difference exact
     float f[V];
-    int64_t total = 0;
+    double total = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = 4 * ((v / 4) * G + g) + v % 4;
-        total += e < s.experts ? counts[e] : 0;
+        f[v] = __int_as_float(e < s.experts ? counts[e] : 0);
+        total = total + static_cast<double>(__float_as_int(f[v]));
     }
 #pragma unroll
     for (int off = G / 2; off > 0; off >>= 1)
-        total += __shfl_xor(total, off);
+        total = total + __shfl_xor(total, off);
     const double unit = 1.0 / (static_cast<double>(s.experts) * some * static_cast<double>(s.k));
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = 4 * ((v / 4) * G + g) + v % 4;
-        const int64_t c = e < s.experts ? counts[e] : 0;
-        f[v] = static_cast<float>(static_cast<double>(c * s.experts - total) * unit);
-    }
+    for (int v = 0; v < V; ++v)
+        f[v] = static_cast<float>(
+            __builtin_fma(static_cast<double>(__float_as_int(f[v])), static_cast<double>(s.experts), -total) * unit);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kRows;
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kRows; t0 < s.tokens; t0 += step) {
         const int64_t t = t0 + lane / G;
@@ -447,55 +506,32 @@ __global__ __launch_bounds__(kBalBlock) void balance_grad_kernel(const ds_scaler
         if (on && mask != nullptr)
             on = mask[t] != 0;
         float z[V];
-        if (on) {
-            bal_load<GF, G, V>(static_cast<const unsigned char*>(logits) + t * s.stride * es, s, g, z);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                z[v] = kNegInf;
-        }
+        bal_load<GF, G, V>(static_cast<const unsigned char*>(logits) + t * s.stride * es, s, g, on, z);
         const float top = bal_top<G, V>(z);
-        on = on && bal_used<G, V>(z, top);
-        const float inv = bal_softmax<G, V>(z, top);
+        if (__ballot(on && !(top > kNegInf)) != 0ull)
+            on = on && bal_used<G, V>(z, top);
+        float inv = bal_softmax<G, V>(z, on ? top : 0.0f);
+        if (!on)
+            inv = 0.0f;
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             z[v] = z[v] * inv;
-            dot = dot + z[v] * f[v];
+            dot = __builtin_fmaf(z[v], f[v], dot);
         }
         dot = row_sum<G>(dot);
-        if (!in || (ACC && !on))
-            continue;
-        unsigned char* row = static_cast<unsigned char*>(dlogits) + t * dstride * es;
 #pragma unroll
-        for (int c = 0; c < V / 4; ++c) {
-            const int e0 = 4 * (c * G + g);
-            f32x4 d;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                d[j] = on ? factor * (z[4 * c + j] * (f[4 * c + j] - dot)) : 0.0f;
-            if (dvec && e0 + 4 <= s.experts) {
-                if constexpr (GF == kF32) {
-                    f32x4* p = reinterpret_cast<f32x4*>(row) + e0 / 4;
-                    *p = ACC ? *p + d : d;
-                } else {
-                    u32x2* p = reinterpret_cast<u32x2*>(row) + e0 / 4;
-                    *p = narrow4<GF>(ACC ? widen4<GF>(*p) + d : d);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (e0 + j < s.experts)
-                        bal_store1<GF, ACC>(row, e0 + j, d[j]);
-            }
-        }
+        for (int v = 0; v < V; ++v)
+            z[v] = factor * (z[v] * (f[v] - dot));
+        if (ACC ? on : in)
+            bal_store<GF, G, V, ACC>(static_cast<unsigned char*>(dlogits) + t * dstride * es, s.experts, dvec, g, z);
     }
 }
 
 // ---- host side ----
 
 // Blocks of the forward pass: one per 4 waves' rows, at most kBalMaxBlocks.
-int bal_lanes(int32_t experts) { return experts <= 256 ? 8 : 16; }
+int bal_lanes(int32_t experts) { return experts <= 128 ? 8 : experts <= 256 ? 16 : 32; }
 
 int64_t bal_blocks(int64_t tokens, int32_t experts)
 {
@@ -583,8 +619,8 @@ void launch_balance2(int64_t blocks, hipStream_t st, const void* z, const BalSha
     if (s.experts <= 32)       launch_balance3<GF, 8, 4>(blocks, st, z, s, mask, w, o);
     else if (s.experts <= 64)  launch_balance3<GF, 8, 8>(blocks, st, z, s, mask, w, o);
     else if (s.experts <= 128) launch_balance3<GF, 8, 16>(blocks, st, z, s, mask, w, o);
-    else if (s.experts <= 256) launch_balance3<GF, 8, 32>(blocks, st, z, s, mask, w, o);
-    else                       launch_balance3<GF, 16, 32>(blocks, st, z, s, mask, w, o);
+    else if (s.experts <= 256) launch_balance3<GF, 16, 16>(blocks, st, z, s, mask, w, o);
+    else                       launch_balance3<GF, 32, 16>(blocks, st, z, s, mask, w, o);
 }
 
 ds_status balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t experts, int64_t stride,
@@ -617,8 +653,13 @@ ds_status balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t 
         return DS_ERR_HIP;
     if (blocks == 1)
         return DS_OK;
-    const unsigned fb = static_cast<unsigned>((experts + kBalFinishCols - 1) / kBalFinishCols);
-    balance_finish_kernel<<<fb, kBalFinishBlock, 0, s>>>(static_cast<int32_t>(blocks), experts, k, w, o);
+    const int32_t parts = static_cast<int32_t>(blocks);
+    if (experts <= 64) {
+        balance_finish_kernel<64><<<1, kBalFinishBlock, 0, s>>>(parts, experts, k, w, o);
+    } else {
+        const unsigned fb = static_cast<unsigned>((experts + kBalFinishCols - 1) / kBalFinishCols);
+        balance_finish_kernel<kBalFinishCols><<<fb, kBalFinishBlock, 0, s>>>(parts, experts, k, w, o);
+    }
     return launched();
 }
 
@@ -630,8 +671,8 @@ void launch_balance_grad(unsigned b, hipStream_t s, const ds_scaler* st, const v
     if (sh.experts <= 32)       balance_grad_kernel<GF, 8, 4, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
     else if (sh.experts <= 64)  balance_grad_kernel<GF, 8, 8, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
     else if (sh.experts <= 128) balance_grad_kernel<GF, 8, 16, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
-    else if (sh.experts <= 256) balance_grad_kernel<GF, 8, 32, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
-    else                        balance_grad_kernel<GF, 16, 32, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
+    else if (sh.experts <= 256) balance_grad_kernel<GF, 16, 16, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
+    else                        balance_grad_kernel<GF, 32, 16, ACC><<<b, kBalBlock, 0, s>>>(st, z, sh, mask, coef, counts, used, d, ds, dv);
 }
 
 ds_status balance_grad(const ds_scaler* st, const void* logits, ds_dtype dt, int64_t tokens, int32_t experts,

@@ -287,7 +287,8 @@ __device__ __forceinline__ double sq4_exact32(const f32x4& x)
 // block sum) into part2[g]; every block then takes a ticket, and the block
 // that takes the last one adds the group sums in a fixed order into
 // st->grad_sumsq and sets the ticket count back to 0.  The chunking is fixed
-// by n, so the result depends on neither grid.  The fences order each
+// by n, so the result depends on neither grid.  A grid of one block needs no
+// ticket.  The fences order each
 // block's group sum before its ticket, and the last block's reads after it
 // (the L2 caches of the XCDs are not coherent with one another).
 __global__ __launch_bounds__(kFinishBlock) void sumsq_finish_kernel(ds_scaler* __restrict__ st,
@@ -315,12 +316,18 @@ __global__ __launch_bounds__(kFinishBlock) void sumsq_finish_kernel(ds_scaler* _
             part2[g] = s;
     }
     if (threadIdx.x == 0) {
-        __threadfence();
-        is_last = atomicAdd(&st->sumsq_blocks_done, 1u) == gridDim.x - 1u ? 1u : 0u;
+        if (gridDim.x > 1) {
+            __threadfence();
+            is_last = atomicAdd(&st->sumsq_blocks_done, 1u) == gridDim.x - 1u ? 1u : 0u;
+        } else {
+            __threadfence_block();
+            is_last = 1u;
+        }
     }
     __syncthreads();
     if (is_last) {
-        __threadfence();
+        if (gridDim.x > 1)
+            __threadfence();
         double s = 0.0;
         for (int64_t g = threadIdx.x; g < ngroups; g += kFinishBlock)
             s = s + part2[g];

@@ -11,10 +11,20 @@ constexpr int kListBlock = 256;                    // lanes: 4 quads each per ti
 constexpr int kListQuads = 4;
 static_assert(kListTile == 4 * kListBlock * kListQuads, "one tile per block");
 static_assert(DS_STATE_BLOCK == 4 * 64, "one quad per lane of a wave is one block of an 8-bit state");
-constexpr int kCheckTiles = 4;                     // tiles that share one partial sum of squares
-// A ticket per block, all from one address, costs about 13 ns each: past this
-// many blocks the scaler is advanced by a kernel of its own (2 us).
-constexpr unsigned kFuseBlocks = 1024;
+// Tiles that share one partial sum of squares, and a block's turn: four keep
+// enough loads on their way on a long list (four layers: 254 us, 369 us one by
+// one); a short one is over sooner one by one (363 tiles: 3.9 us, 6.4 us).
+constexpr int kCheckTiles = 4;
+constexpr int32_t kCheckFew = 2048;                // tiles: up to here one by one
+// Tickets of the blocks of one step: taken from one address they cost about
+// 13 ns each, one after another (2.5 ms for four layers' 197,636 blocks, more
+// than the 8-bit step itself), so block b takes one from counter b % 64, each
+// counter on a line of its own, and the last of each from the scaler's.
+constexpr unsigned kTicketLines = 64, kTicketBytes = 128;
+// With 8-bit states a block's short time is the longer for its ticket: past
+// this many blocks the scaler is advanced by a kernel of its own (one layer:
+// 522 + 2 us, 561 us with tickets; with 32-bit states 936 + 2 and 934 us).
+constexpr unsigned kFuseBlocks = 4096;
 constexpr int32_t kMaxTensors = 1 << 20;
 
 // One tensor in the device table.
@@ -33,8 +43,13 @@ struct ListEntry {
 };
 static_assert(sizeof(ListEntry) == 96, "table entry");
 
-// The table: first-tile numbers (count of them, padded to 16 bytes), then the entries.
-__host__ __device__ inline int64_t list_entries_at(int32_t count) { return (4 * int64_t(count) + 15) / 16 * 16; }
+// The table: ticket counters (0 between steps), first-tile numbers (count of
+// them, padded to 16 bytes), the entries.
+constexpr int64_t kTile0At = kTicketLines * kTicketBytes;
+__host__ __device__ inline int64_t list_entries_at(int32_t count)
+{
+    return kTile0At + (4 * int64_t(count) + 15) / 16 * 16;
+}
 
 // Entries that one table-writing kernel carries in its arguments (3.8 KB).
 constexpr int kListChunk = 40;
@@ -42,11 +57,14 @@ struct ListChunk {
     ListEntry e[kListChunk];
 };
 
-__global__ void list_write_kernel(unsigned char* table, int32_t count, int32_t first, int32_t n, ListChunk c)
+static_assert(kTicketLines == 64, "list_write_kernel clears one per lane of its wave");
+__global__ __launch_bounds__(64) void list_write_kernel(unsigned char* table, int32_t count, int32_t first, int32_t n, ListChunk c)
 {
-    int32_t* tile0 = reinterpret_cast<int32_t*>(table);
+    int32_t* tile0 = reinterpret_cast<int32_t*>(table + kTile0At);
     ListEntry* entries = reinterpret_cast<ListEntry*>(table + list_entries_at(count));
     const int i = threadIdx.x;
+    if (first == 0)
+        *reinterpret_cast<uint32_t*>(table + i * kTicketBytes) = 0u;
     if (i < n) {
         tile0[first + i] = c.e[i].tile0;
         entries[first + i] = c.e[i];
@@ -149,7 +167,9 @@ __device__ __forceinline__ void list_check_tile(const unsigned char* g, int gf, 
     }
 }
 
-// A group of four tiles per block and loop turn; with SUMSQ its sum goes to
+__host__ __device__ inline int list_turn(int64_t tiles) { return tiles <= kCheckFew ? 1 : kCheckTiles; }
+
+// A group of tiles per block and loop turn; with SUMSQ its sum goes to
 // part[group].  Four whole tiles of one 16-bit tensor go at once.
 template <bool SUMSQ>
 __global__ __launch_bounds__(kListBlock) void list_check_kernel(ds_scaler* __restrict__ st,
@@ -158,14 +178,14 @@ __global__ __launch_bounds__(kListBlock) void list_check_kernel(ds_scaler* __res
                                                                 double* __restrict__ part)
 {
     __shared__ double lds[2 * (kListBlock / 64)];
-    const int32_t* tile0 = reinterpret_cast<const int32_t*>(table);
+    const int32_t* tile0 = reinterpret_cast<const int32_t*>(table + kTile0At);
     const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
-    const int groups = (tiles + kCheckTiles - 1) / kCheckTiles;
+    const int turn = list_turn(tiles), groups = (tiles + turn - 1) / turn;
     uint32_t bad = 0u;
     int parity = 0;
     for (int group = blockIdx.x; group < groups; group += gridDim.x) {
-        int tile = group * kCheckTiles;
-        const int end = tile + kCheckTiles < tiles ? tile + kCheckTiles : tiles;
+        int tile = group * turn;
+        const int end = tile + turn < tiles ? tile + turn : tiles;
         double s = 0.0;
         while (tile < end) {
             const ListEntry e = entries[list_find(tile0, count, tile)];
@@ -554,18 +574,19 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
 template <bool E8, bool DITHER, bool NT, bool FUSE>
 __global__ __launch_bounds__(kListBlock) void list_adam_kernel(ds_scaler* __restrict__ st,
                                                                const unsigned char* __restrict__ table,
-                                                               int32_t count, int32_t tiles, ListHyper hp)
+                                                               uint32_t* __restrict__ tickets, int32_t count,
+                                                               int32_t tiles, ListHyper hp)
 {
-    const int32_t* tile0 = reinterpret_cast<const int32_t*>(table);
+    const int32_t* tile0 = reinterpret_cast<const int32_t*>(table + kTile0At);
     const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
-    int tile = blockIdx.x;
     ds_scaler now{};
     now.scale = st->scale;
     now.step = st->step;
     now.grad_sumsq = st->grad_sumsq;
     if (st->overflow == 0u) {
         ListStep q;
-        for (bool first = true; tile < tiles; tile += gridDim.x, first = false) {
+        bool first = true;
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const int j = list_find(tile0, count, tile);
             const ListEntry e = entries[j];
             const int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile;
@@ -577,6 +598,7 @@ __global__ __launch_bounds__(kListBlock) void list_adam_kernel(ds_scaler* __rest
                 list_load<E8, false, false>(e, base, r);
             if (first)
                 q = list_step(&now, hp);
+            first = false;
             list_tensor_consts(e, q);
             const uint32_t key = DITHER ? dither_mix(q.key + static_cast<uint32_t>(j) * kGold) : 0u;
             if (full)
@@ -587,9 +609,18 @@ __global__ __launch_bounds__(kListBlock) void list_adam_kernel(ds_scaler* __rest
     }
     if constexpr (FUSE) {
         __syncthreads();   // every lane of this block has read the scaler state
-        if (threadIdx.x == 0 && atomicAdd(&st->blocks_done, 1u) == gridDim.x - 1u) {
-            st->blocks_done = 0u;
-            advance_scaler(st);
+        if (threadIdx.x == 0) {
+            const unsigned line = blockIdx.x % kTicketLines;
+            const unsigned of_line = (gridDim.x - line + kTicketLines - 1) / kTicketLines;
+            uint32_t* ticket = tickets + line * (kTicketBytes / 4);
+            if (atomicAdd(ticket, 1u) == of_line - 1u) {
+                *ticket = 0u;
+                const unsigned lines = gridDim.x < kTicketLines ? gridDim.x : kTicketLines;
+                if (atomicAdd(&st->blocks_done, 1u) == lines - 1u) {
+                    st->blocks_done = 0u;
+                    advance_scaler(st);
+                }
+            }
         }
     }
 }
@@ -660,7 +691,7 @@ bool list_alias(ListRange* r, int64_t n)
 
 size_t list_bytes(int32_t count)
 {
-    return count < 0 ? 0 : static_cast<size_t>(list_entries_at(count)) + sizeof(ListEntry) * static_cast<size_t>(count);
+    return count <= 0 ? 0 : static_cast<size_t>(list_entries_at(count)) + sizeof(ListEntry) * static_cast<size_t>(count);
 }
 
 // A list that ds_tensor_list_write can have filled.
@@ -679,7 +710,7 @@ ds_status list_ok(const ds_tensor_list* l)
 }
 
 // Partial sums of squares of a list: one per group of tiles.
-int64_t list_parts(int64_t tiles) { return (tiles + kCheckTiles - 1) / kCheckTiles; }
+int64_t list_parts(int64_t tiles) { return (tiles + list_turn(tiles) - 1) / list_turn(tiles); }
 
 uint64_t list_ws_bytes(int64_t tiles)
 {
@@ -778,9 +809,10 @@ void launch_list_adam2(bool fuse, unsigned blocks, hipStream_t s, ds_scaler* st,
                        const ListHyper& hp)
 {
     const unsigned char* table = static_cast<const unsigned char*>(l->table);
-    const int32_t tiles = static_cast<int32_t>(l->tiles);
-    if (fuse) list_adam_kernel<E8, DITHER, NT, true><<<blocks, kListBlock, 0, s>>>(st, table, l->count, tiles, hp);
-    else      list_adam_kernel<E8, DITHER, NT, false><<<blocks, kListBlock, 0, s>>>(st, table, l->count, tiles, hp);
+    uint32_t* tickets = static_cast<uint32_t*>(l->table);
+    const int32_t tiles = static_cast<int32_t>(l->tiles), count = l->count;
+    if (fuse) list_adam_kernel<E8, DITHER, NT, true><<<blocks, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp);
+    else      list_adam_kernel<E8, DITHER, NT, false><<<blocks, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp);
 }
 
 template <bool E8, bool DITHER>
@@ -815,8 +847,8 @@ ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, 
     const ListHyper hp{h, beta1, beta2, dither_mix(dither_mix(static_cast<uint32_t>(seed >> 32)) ^ static_cast<uint32_t>(seed))};
     const bool nt = variant_nt(l->elems);
     const unsigned blocks = grid_blocks(l->tiles, kListBlock);
-    const bool fuse = end_step && blocks <= kFuseBlocks;
-    if (l->sdt == DS_FP32)
+    const bool e8 = l->sdt != DS_FP32, fuse = end_step && (!e8 || blocks <= kFuseBlocks);
+    if (!e8)
         launch_list_adam<false, false>(nt, fuse, blocks, s, st, l, hp);
     else if (rounding == DS_ROUND_DITHER)
         launch_list_adam<true, true>(nt, fuse, blocks, s, st, l, hp);

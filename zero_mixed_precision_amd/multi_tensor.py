@@ -87,6 +87,7 @@ class MultiTensorStep:
                 raise ValueError(f"parameter {i}: expected a tensor in the memory of one GPU, got one on {p.device}")
         device = self.params[0].device if count else torch.device("cuda", torch.cuda.current_device())
 
+        self._device = device.index
         self.numels = [p.numel() for p in self.params]
         self.offsets, total = [], 0
         for n in self.numels:
@@ -179,7 +180,7 @@ class MultiTensorStep:
         """One step on the gradients set: overflow check (with the joint norm if clipped), gated Adam, scaler."""
         if self._list is None:
             raise RuntimeError("set_gradients() before step()")
-        c, lib, ok, s = self.cfg, _lib.lib, _lib._ok, _lib._s(self.stream)
+        c, lib, ok, s = self.cfg, _lib.lib, _lib._ok, _lib._stream_on(self.stream, self._device)
         st, lst = self._state_at, self._list_at
         ok(lib.ds_check_overflow_list(st, lst, self._ws_at, self._ws_bytes, s), "ds_check_overflow_list")
         ok(lib.ds_adam_step_list(st, lst, c.lr, self._sched_at, c.betas[0], c.betas[1], c.eps, c.gradient_clipping,
