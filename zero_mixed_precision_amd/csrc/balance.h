@@ -358,7 +358,7 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
     __shared__ int32_t lds_used[kWaves];
     const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
-    const int e = blockIdx.x * COLS + col;
+    const int e = blockIdx.x * COLS + col, column = e < experts ? e : 0;
     int rows = 0;
     for (int i = threadIdx.x; i < parts; i += kBalFinishBlock)
         rows += w.used[i];
@@ -369,15 +369,16 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
         float q[kDeep];
 #pragma unroll
         for (int u = 0; u < kDeep; ++u) {
-            const int i = i0 + u * kGroups;
-            const bool in = i < parts && e < experts;
-            c[u] = in ? w.count[i * experts + e] : 0;
-            q[u] = in ? w.prob[i * experts + e] : 0.0f;
+            // past the end: the first row again, left out below (no branch between the loads)
+            const int i = i0 + u * kGroups < parts ? i0 + u * kGroups : 0;
+            c[u] = w.count[i * experts + column];
+            q[u] = w.prob[i * experts + column];
         }
 #pragma unroll
         for (int u = 0; u < kDeep; ++u) {
-            n += c[u];
-            p = p + static_cast<double>(q[u]);
+            const bool in = i0 + u * kGroups < parts;
+            n += in ? c[u] : 0;
+            p = p + static_cast<double>(in ? q[u] : 0.0f);
         }
     }
 #pragma unroll
@@ -410,19 +411,23 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
 #pragma unroll
     for (int off = 1; off < COLS; off <<= 1)
         part = part + __shfl_xor(part, off);
-    if (lane != 0)
-        return;
     if (gridDim.x > 1) {
-        w.loss[blockIdx.x] = part;
-        __threadfence();
-        if (atomicAdd(w.ticket, 1u) != gridDim.x - 1u)
+        uint32_t before = 0u;
+        if (lane == 0) {
+            w.loss[blockIdx.x] = part;
+            __threadfence();
+            before = atomicAdd(w.ticket, 1u);
+        }
+        if (__builtin_amdgcn_readfirstlane(before) != gridDim.x - 1u)
             return;
         __threadfence();
-        part = 0.0;
-        for (unsigned i = 0; i < gridDim.x; ++i)
-            part = part + __builtin_nontemporal_load(w.loss + i);
+        part = lane < static_cast<int>(gridDim.x) ? __builtin_nontemporal_load(w.loss + lane) : 0.0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            part = part + __shfl_xor(part, off);
     }
-    bal_end(o, experts, rows, part);
+    if (lane == 0)
+        bal_end(o, experts, rows, part);
 }
 
 // The lane's V values into (or, with ACC, added to) one row.
@@ -541,6 +546,7 @@ int64_t bal_blocks(int64_t tokens, int32_t experts)
 }
 
 constexpr int kBalLossParts = DS_MAX_EXPERTS / kBalFinishCols;
+static_assert(kBalLossParts <= 64, "one wave adds them");
 
 uint64_t bal_ws_bytes(int64_t blocks, int32_t experts)
 {
