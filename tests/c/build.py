@@ -53,6 +53,22 @@ def build_host_checks() -> str:
     return HOST_OUT
 
 
+LIST_SRC = os.path.join(HERE, "list_checks.c")
+LIST_OUT = os.path.join(HERE, "list_checks")
+
+
+def build_list_checks() -> str:
+    """The host paths of the tensor-list and balance-loss entry points (refusals, the overlap search over many
+    tensors), linked against the sanitized library that build_host_checks() made."""
+    clang = os.path.join(ROCM, "llvm", "bin", "clang")
+    cmd = [clang, "-std=c11", "-O1", "-g", "-Wall", "-Wextra", "-Werror", "-fsanitize=address,undefined",
+           "-fno-omit-frame-pointer", "-I", os.path.join(ROOT, "include"), LIST_SRC, "-o", LIST_OUT,
+           "-L", HERE, "-l:libdszero_asan.so", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    return LIST_OUT
+
+
 if __name__ == "__main__":
     print(build_driver())
     print(build_host_checks())
+    print(build_list_checks())

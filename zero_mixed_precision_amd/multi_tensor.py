@@ -187,6 +187,11 @@ class MultiTensorStep:
                                  c.gradient_accumulation_steps, self._rounding, self._seed, self.end_step, s),
            "ds_adam_step_list")
 
+    @property
+    def loss_scale(self):
+        """The loss scale S as an fp32 scalar on the device (a view of the scaler state: no synchronisation)."""
+        return self.state[:4].view(self.torch.float32)[0]
+
     def scaler(self) -> _lib.DsScaler:
         return _lib.ds_state_read(self.state, self.stream)
 
