@@ -586,7 +586,8 @@ ds_status ds_tensor_list_write(ds_tensor_list* list, void* table, size_t table_b
                                int32_t count, ds_dtype sdt, void* stream);
 
 /* Workspace of ds_check_overflow_list with the sum of squares: one fp64 per
- * four tiles and per 4096 of those (0 for list NULL). */
+ * group of tiles (of one tile up to 2048 of them, of four above) and per 4096
+ * groups (0 for list NULL). */
 size_t ds_tensor_list_workspace_bytes(const ds_tensor_list* list);
 
 /*
@@ -618,6 +619,19 @@ ds_status ds_adam_step_list(ds_scaler* st, const ds_tensor_list* list, float lr,
                             const ds_lr_schedule* sched_or_null, double beta1, double beta2, float eps,
                             float max_grad_norm, int32_t accum_steps, ds_rounding rounding, uint64_t seed,
                             int32_t end_step, void* stream);
+
+/*
+ * A whole step over one list: ds_check_overflow_list, then ds_adam_step_list
+ * with end_step, to the same bits.  Short lists take fewer launches: one up to
+ * 8 tiles, where every block of the update checks the whole list itself, and
+ * with a workspace two up to 2048 tiles, where it adds the check's partial
+ * sums itself.  What was checked before in the same step (a flat partition,
+ * another list) counts here as for ds_adam_step_list.  Errors as for the two
+ * calls; refused as a whole.
+ */
+ds_status ds_step_list(ds_scaler* st, const ds_tensor_list* list, void* workspace_or_null, size_t workspace_bytes,
+                       float lr, const ds_lr_schedule* sched_or_null, double beta1, double beta2, float eps,
+                       float max_grad_norm, int32_t accum_steps, ds_rounding rounding, uint64_t seed, void* stream);
 
 /*
  * ---------------------------------------------------------------------------

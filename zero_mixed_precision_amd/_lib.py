@@ -27,7 +27,7 @@ EXPORTED = (
     "ds_adam_step_fused", "ds_accumulate_multi", "ds_check_overflow_sumsq_noalloc", "ds_adam_step_double_buffered",
     "ds_accumulate_adam_double_buffered", "ds_update_loss_scale_double_buffered",
     "ds_tensor_list_bytes", "ds_tensor_list_write", "ds_tensor_list_workspace_bytes", "ds_check_overflow_list",
-    "ds_adam_step_list", "ds_balance_workspace_bytes", "ds_balance_loss", "ds_balance_loss_grad",
+    "ds_adam_step_list", "ds_step_list", "ds_balance_workspace_bytes", "ds_balance_loss", "ds_balance_loss_grad",
 )
 DS_NOALLOC_MAX_ELEMS = 17175674880
 DS_LR_WARMUP, DS_LR_WARMUP_DECAY = 1, 2
@@ -181,6 +181,9 @@ def _load():
         "ds_check_overflow_list": ([vp, ctypes.POINTER(DsTensorList), vp, ctypes.c_size_t, vp], ctypes.c_int),
         "ds_adam_step_list": ([vp, ctypes.POINTER(DsTensorList), f32, ctypes.POINTER(DsLrSchedule), ctypes.c_double,
                                ctypes.c_double, f32, f32, i32, ctypes.c_int, ctypes.c_uint64, i32, vp], ctypes.c_int),
+        "ds_step_list": ([vp, ctypes.POINTER(DsTensorList), vp, ctypes.c_size_t, f32, ctypes.POINTER(DsLrSchedule),
+                          ctypes.c_double, ctypes.c_double, f32, f32, i32, ctypes.c_int, ctypes.c_uint64, vp],
+                         ctypes.c_int),
         "ds_balance_workspace_bytes": ([i64, i32], ctypes.c_size_t),
         "ds_balance_loss": ([vp, ctypes.c_int, i64, i32, i64, vp, i32, f32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
                             ctypes.c_int),
@@ -470,6 +473,16 @@ def ds_adam_step_list(st, tensors: DsTensorList, lr, sched, beta1, beta2, eps, m
     _ok(lib.ds_adam_step_list(_scaler(st), ctypes.byref(tensors), lr, sched_p, beta1, beta2, eps, max_grad_norm,
                               int(accum_steps), int(rounding), int(seed), int(bool(end_step)), _s(stream)),
         "ds_adam_step_list")
+
+
+def ds_step_list(st, tensors: DsTensorList, workspace, lr, sched, beta1, beta2, eps, max_grad_norm, accum_steps,
+                 rounding=DS_ROUND_NEAREST, seed=0, workspace_bytes=None, stream=None) -> None:
+    """ds_check_overflow_list and ds_adam_step_list(end_step=True) in one call."""
+    ws_bytes = 0 if workspace is None else _nbytes(workspace, workspace_bytes)
+    ws = None if workspace is None else _p(workspace, ds_tensor_list_workspace_bytes(tensors), "workspace")
+    sched_p = ctypes.byref(sched) if sched is not None else None
+    _ok(lib.ds_step_list(_scaler(st), ctypes.byref(tensors), ws, ws_bytes, lr, sched_p, beta1, beta2, eps,
+                         max_grad_norm, int(accum_steps), int(rounding), int(seed), _s(stream)), "ds_step_list")
 
 
 def ds_balance_workspace_bytes(tokens, experts) -> int:

@@ -343,9 +343,9 @@ __global__ __launch_bounds__(kFinishBlock) void sumsq_finish_kernel(ds_scaler* _
 // loss-scaler state machine ([Guide] section 4.2), one work-item
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void advance_scaler_with(ds_scaler* st, uint32_t flag)
+// The state after a step that ends with `flag` in state `s`.
+__device__ __forceinline__ ds_scaler advanced(ds_scaler s, uint32_t flag)
 {
-    ds_scaler s = *st;
     const uint32_t ov = flag != 0u ? 1u : 0u;
     s.iter += 1;
     if (ov) {
@@ -376,8 +376,10 @@ __device__ __forceinline__ void advance_scaler_with(ds_scaler* st, uint32_t flag
     s.overflow = 0u;
     s.last_grad_sumsq = s.grad_sumsq;
     s.grad_sumsq = 0.0;
-    *st = s;
+    return s;
 }
+
+__device__ __forceinline__ void advance_scaler_with(ds_scaler* st, uint32_t flag) { *st = advanced(*st, flag); }
 
 __device__ __forceinline__ void advance_scaler(ds_scaler* st) { advance_scaler_with(st, st->overflow); }
 
@@ -2097,18 +2099,21 @@ ds_status ds_adam_step_list(ds_scaler* st, const ds_tensor_list* list, float lr,
                             float max_grad_norm, int32_t accum_steps, ds_rounding rounding, uint64_t seed,
                             int32_t end_step, void* stream)
 {
-    AdamHyper hp{lr, static_cast<float>(beta1), static_cast<float>(beta2), eps, 0.0f, max_grad_norm, accum_steps,
-                 0, 0.0f, 0, 0};
-    if (sched_or_null != nullptr) {
-        if (!schedule_ok(*sched_or_null))
-            return DS_ERR_HPARAM;
-        hp.lr = sched_or_null->warmup_max_lr;
-        hp.lr_kind = sched_or_null->kind;
-        hp.lr_min = sched_or_null->warmup_min_lr;
-        hp.lr_warmup = sched_or_null->warmup_num_steps;
-        hp.lr_total = sched_or_null->total_num_steps;
-    }
+    AdamHyper hp;
+    if (!list_adam_hyper(lr, sched_or_null, beta1, beta2, eps, max_grad_norm, accum_steps, &hp))
+        return DS_ERR_HPARAM;
     return list_adam(st, list, hp, beta1, beta2, rounding, seed, end_step != 0, static_cast<hipStream_t>(stream));
+}
+
+ds_status ds_step_list(ds_scaler* st, const ds_tensor_list* list, void* workspace_or_null, size_t workspace_bytes,
+                       float lr, const ds_lr_schedule* sched_or_null, double beta1, double beta2, float eps,
+                       float max_grad_norm, int32_t accum_steps, ds_rounding rounding, uint64_t seed, void* stream)
+{
+    AdamHyper hp;
+    if (!list_adam_hyper(lr, sched_or_null, beta1, beta2, eps, max_grad_norm, accum_steps, &hp))
+        return DS_ERR_HPARAM;
+    return list_step_all(st, list, workspace_or_null, workspace_bytes, hp, beta1, beta2, rounding, seed,
+                         static_cast<hipStream_t>(stream));
 }
 
 size_t ds_balance_workspace_bytes(int64_t tokens, int32_t experts)

@@ -123,6 +123,17 @@ __device__ __forceinline__ float list_grad1(int gf, const void* grad, int64_t i)
 
 // ---- overflow check and sum of squares ----
 
+template <int GF, bool SUMSQ>
+__device__ __forceinline__ void list_check_vec(const u32x4& w, uint32_t& bad, double& s)
+{
+    if constexpr (SUMSQ)
+        check_sq_vec<GF>(w, bad, s);
+    else if constexpr (GF == kF32)
+        bad |= nonfinite_f32(w.x) | nonfinite_f32(w.y) | nonfinite_f32(w.z) | nonfinite_f32(w.w);
+    else
+        bad |= nonfinite16x2<GF>(w.x) | nonfinite16x2<GF>(w.y) | nonfinite16x2<GF>(w.z) | nonfinite16x2<GF>(w.w);
+}
+
 // TILES whole, aligned tiles at `grad`: every load before the arithmetic.
 template <int GF, bool SUMSQ, int TILES>
 __device__ __forceinline__ void list_check_tiles(const void* grad, uint32_t& bad, double& s)
@@ -135,15 +146,8 @@ __device__ __forceinline__ void list_check_tiles(const void* grad, uint32_t& bad
     for (int j = 0; j < kVecs; ++j)
         w[j] = gload(G + j * kListBlock);
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        if constexpr (SUMSQ)
-            check_sq_vec<GF>(w[j], bad, s);
-        else if constexpr (GF == kF32)
-            bad |= nonfinite_f32(w[j].x) | nonfinite_f32(w[j].y) | nonfinite_f32(w[j].z) | nonfinite_f32(w[j].w);
-        else
-            bad |= nonfinite16x2<GF>(w[j].x) | nonfinite16x2<GF>(w[j].y) | nonfinite16x2<GF>(w[j].z) |
-                   nonfinite16x2<GF>(w[j].w);
-    }
+    for (int j = 0; j < kVecs; ++j)
+        list_check_vec<GF, SUMSQ>(w[j], bad, s);
 }
 
 // Tile `left` elements from its tensor's end (whole and aligned, or not).
@@ -377,7 +381,7 @@ __device__ __forceinline__ void adam1_fp8(float graw, float& p, float& m, float&
     p = __builtin_fmaf(-c.step_size, m * __builtin_amdgcn_rcpf(den), p);
 }
 
-// One tile's data in registers: four quads per lane.
+// A tile's quads in registers, four per lane.
 template <bool E8>
 struct ListRegs {
     f32x4 g[kListQuads], p[kListQuads], m[kListQuads], v[kListQuads];
@@ -390,20 +394,19 @@ struct ListRegs<true> {
     float m_scale[kListQuads], v_scale[kListQuads];
 };
 
-// Scale block of the wave's quad u in the tile at element `base`.
+// Scale block of the wave's quad u from element `base` on.
 __device__ __forceinline__ int64_t list_block(int64_t base, int u)
 {
     return base / DS_STATE_BLOCK + u * (kListBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 }
 
-// Loads of a tile.  FULL: whole and aligned, vectors of four throughout.
-// Else quad by quad: a vector where the tensor is aligned and the quad whole,
-// single elements otherwise, zeros past the end (so that a short block's top
-// is right).
-template <bool E8, bool NT, bool FULL>
+// Loads of U quads per lane, into the first U, from element `base` on.  FULL: whole and aligned,
+// vectors of four throughout.  Else a vector where the tensor is aligned and
+// the quad whole, single elements otherwise, zeros past the end (so that a
+// short block's top is right).
+template <bool E8, bool NT, bool FULL, int U>
 __device__ __forceinline__ void list_load(const ListEntry& e, int64_t base, ListRegs<E8>& r)
 {
-    constexpr int U = kListQuads;
     const int64_t q0 = base / 4 + threadIdx.x;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -477,27 +480,27 @@ __device__ __forceinline__ void list_load(const ListEntry& e, int64_t base, List
     }
 }
 
-template <bool E8>
+template <bool E8, int U>
 __device__ __forceinline__ void list_widen(int gf, ListRegs<E8>& r)
 {
     if (gf == kF32)
         return;
 #pragma unroll
-    for (int u = 0; u < kListQuads; ++u) {
+    for (int u = 0; u < U; ++u) {
         const u32x2 w = {__float_as_uint(r.g[u].x), __float_as_uint(r.g[u].y)};
         r.g[u] = gf == kBF16 ? widen4<kBF16>(w) : widen4<kF16>(w);
     }
 }
 
-// Update and stores of a tile loaded by list_load.
-template <bool E8, bool DITHER, bool NT, bool FULL>
+// Update and stores of the U quads loaded by list_load.
+template <bool E8, bool DITHER, bool NT, bool FULL, int U>
 __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, ListRegs<E8>& r, const AdamConsts& c,
                                             uint32_t key)
 {
     const int64_t q0 = base / 4 + threadIdx.x;
-    list_widen<E8>(e.gf, r);
+    list_widen<E8, U>(e.gf, r);
 #pragma unroll
-    for (int u = 0; u < kListQuads; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t q = q0 + u * kListBlock, blk = list_block(base, u);
         if (!FULL && blk * DS_STATE_BLOCK >= e.n)   // uniform over the wave
             return;
@@ -566,63 +569,287 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
     }
 }
 
+// The tile of one block in flight.  A whole aligned one is loaded at once; any
+// other goes one quad per lane after another when its turn comes (its code
+// once, not four times: a short list's time is in part the fetching of code
+// that no block has run before).
+template <bool E8, bool DITHER, bool NT>
+struct ListTile {
+    ListEntry e;
+    int64_t base;
+    bool full;
+    uint32_t index;
+    ListRegs<E8> r;
+
+    __device__ __forceinline__ void load(const int32_t* tile0, const ListEntry* entries, int count, int tile)
+    {
+        const int j = list_find(tile0, count, tile);
+        e = entries[j];
+        index = static_cast<uint32_t>(j);
+        base = static_cast<int64_t>(tile - e.tile0) * kListTile;
+        full = e.vec && e.n - base >= kListTile;
+        if (full)
+            list_load<E8, NT, true, kListQuads>(e, base, r);
+    }
+
+    __device__ __forceinline__ void finish(ListStep& q)
+    {
+        list_tensor_consts(e, q);
+        const uint32_t key = DITHER ? dither_mix(q.key + index * kGold) : 0u;
+        if (full) {
+            list_finish<E8, DITHER, NT, true, kListQuads>(e, base, r, q.c, key);
+            return;
+        }
+        const int64_t end = e.n - base < kListTile ? e.n : base + kListTile;
+#pragma unroll 1
+        for (int64_t at = base; at < end; at += 4 * kListBlock) {
+            list_load<E8, false, false, 1>(e, at, r);
+            list_finish<E8, DITHER, false, false, 1>(e, at, r, q.c, key);
+        }
+    }
+};
+
+// The part of the scaler that a step's end changes or goes by: all before the
+// counters.  Read by scalar loads at a kernel's start and held in scalar
+// registers; the compiler would move the loads of what only the last block
+// needs behind the tickets and make them vector loads there, and such a load
+// per wave of the line that tickets are taken from made the kernel 4.6 times
+// slower.
+constexpr int kScalerWords = offsetof(ds_scaler, blocks_done) / 4;
+static_assert(kScalerWords == 20, "whole 16-byte vectors");
+
+__device__ __forceinline__ ds_scaler list_scaler(const ds_scaler* st)
+{
+    const auto* w = (const __attribute__((address_space(4))) uint32_t*)reinterpret_cast<const uint32_t*>(st);
+    uint32_t x[kScalerWords];
+#pragma unroll
+    for (int i = 0; i < kScalerWords; ++i)
+        x[i] = w[i];
+#pragma unroll
+    for (int i = 0; i < kScalerWords; ++i)
+        asm volatile("" : "+s"(x[i]));
+    ds_scaler s{};
+    __builtin_memcpy(&s, x, sizeof(x));
+    return s;
+}
+
+// Takes this block's ticket; the last block advances the scaler from `now`,
+// the state as it was when the kernel started.  Up to kTicketLines blocks take
+// it from the scaler's counter at once.
+__device__ __forceinline__ void list_end_step(ds_scaler* st, const ds_scaler& now, uint32_t* tickets)
+{
+    const unsigned lines = gridDim.x < kTicketLines ? gridDim.x : kTicketLines;
+    if (gridDim.x > kTicketLines) {
+        const unsigned line = blockIdx.x % kTicketLines;
+        const unsigned of_line = (gridDim.x - line + kTicketLines - 1) / kTicketLines;
+        uint32_t* ticket = tickets + line * (kTicketBytes / 4);
+        if (atomicAdd(ticket, 1u) != of_line - 1u)
+            return;
+        *ticket = 0u;
+    }
+    if (atomicAdd(&st->blocks_done, 1u) == lines - 1u) {
+        const ds_scaler s = advanced(now, now.overflow);
+        u32x4 x[kScalerWords / 4];
+        __builtin_memcpy(x, &s, sizeof(x));
+#pragma unroll
+        for (int i = 0; i < kScalerWords / 4; ++i)
+            reinterpret_cast<u32x4*>(st)[i] = x[i];
+        st->blocks_done = 0u;
+    }
+}
+
 // One tile per block and loop turn.  The step's constants (fp64 powers and
-// divisions) are formed while the first tile's loads are on their way; the
-// scaler's values that they need are read before anything is written, when
-// scalar loads may serve them (a vector load per wave of the line that the
-// tickets are taken from made the kernel 4.6 times slower).
+// divisions) are formed while the first tile's loads are on their way.
 template <bool E8, bool DITHER, bool NT, bool FUSE>
-__global__ __launch_bounds__(kListBlock) void list_adam_kernel(ds_scaler* __restrict__ st,
+__global__ __launch_bounds__(kListBlock, 4) void list_adam_kernel(ds_scaler* __restrict__ st,
                                                                const unsigned char* __restrict__ table,
                                                                uint32_t* __restrict__ tickets, int32_t count,
                                                                int32_t tiles, ListHyper hp)
 {
     const int32_t* tile0 = reinterpret_cast<const int32_t*>(table + kTile0At);
     const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
-    ds_scaler now{};
-    now.scale = st->scale;
-    now.step = st->step;
-    now.grad_sumsq = st->grad_sumsq;
-    if (st->overflow == 0u) {
+    const ds_scaler now = list_scaler(st);
+    if (now.overflow == 0u) {
         ListStep q;
         bool first = true;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const int j = list_find(tile0, count, tile);
-            const ListEntry e = entries[j];
-            const int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile;
-            const bool full = e.vec && e.n - base >= kListTile;
-            ListRegs<E8> r;
-            if (full)
-                list_load<E8, NT, true>(e, base, r);
-            else
-                list_load<E8, false, false>(e, base, r);
+            ListTile<E8, DITHER, NT> t;
+            t.load(tile0, entries, count, tile);
             if (first)
                 q = list_step(&now, hp);
             first = false;
-            list_tensor_consts(e, q);
-            const uint32_t key = DITHER ? dither_mix(q.key + static_cast<uint32_t>(j) * kGold) : 0u;
-            if (full)
-                list_finish<E8, DITHER, NT, true>(e, base, r, q.c, key);
-            else
-                list_finish<E8, DITHER, false, false>(e, base, r, q.c, key);
+            t.finish(q);
         }
     }
     if constexpr (FUSE) {
         __syncthreads();   // every lane of this block has read the scaler state
-        if (threadIdx.x == 0) {
-            const unsigned line = blockIdx.x % kTicketLines;
-            const unsigned of_line = (gridDim.x - line + kTicketLines - 1) / kTicketLines;
-            uint32_t* ticket = tickets + line * (kTicketBytes / 4);
-            if (atomicAdd(ticket, 1u) == of_line - 1u) {
-                *ticket = 0u;
-                const unsigned lines = gridDim.x < kTicketLines ? gridDim.x : kTicketLines;
-                if (atomicAdd(&st->blocks_done, 1u) == lines - 1u) {
-                    st->blocks_done = 0u;
-                    advance_scaler(st);
+        if (threadIdx.x == 0)
+            list_end_step(st, now, tickets);
+    }
+}
+
+// ---- a whole step over a short list ----
+
+// Up to kStepParts tiles every block adds the check's partial sums itself,
+// instead of a kernel between the check and the update; up to kStepCheck tiles
+// every block also checks the whole list itself, instead of a kernel before.
+constexpr int kStepParts = 2048, kStepCheck = 8;
+static_assert(kStepParts <= kCheckFew && kStepParts <= kGroup && kFinishBlock == kListBlock,
+              "one group of one tile's sums each: the order of sumsq_finish_kernel");
+enum ListFront { kFrontParts, kFrontCheck, kFrontCheckSum };
+
+// The sum over part[0 .. parts): sumsq_finish_kernel's, in its order.  In every thread.
+__device__ __forceinline__ double list_sum_parts(const double* part, int parts, double* lds)
+{
+    double x[kStepParts / kListBlock];
+#pragma unroll
+    for (int j = 0; j < kStepParts / kListBlock; ++j) {
+        const int i = j * kListBlock + static_cast<int>(threadIdx.x);
+        x[j] = i < parts ? part[i] : 0.0;
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < kStepParts / kListBlock; ++j)
+        s = s + x[j];
+    s = block_sum_fixed<kListBlock>(s, lds, 0);
+    if (threadIdx.x == 0)
+        lds[kListBlock / 64] = s;
+    __syncthreads();
+    return lds[kListBlock / 64];
+}
+
+// One tile checked by one wave, lane by lane as the four waves of
+// list_check_kernel's block do it: s[w] is what lane `lane` of its wave w sums.
+template <int GF, bool SUMSQ>
+__device__ __forceinline__ void list_wave_tile(const void* grad, int lane, uint32_t& bad, double (&s)[kListBlock / 64])
+{
+    constexpr int kPer = GF == kF32 ? 4 : 8, kWaves = kListBlock / 64;
+    constexpr int kVecs = static_cast<int>(kListTile) / (kListBlock * kPer);
+    const u32x4* G = static_cast<const u32x4*>(grad) + lane;
+#pragma unroll 1
+    for (int i = 0; i < kVecs; i += 2) {   // 8 vectors at once: the block's own tile is in registers meanwhile
+        u32x4 x[2][kWaves];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                x[j][w] = gload(G + (i + j) * kListBlock + w * 64);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                list_check_vec<GF, SUMSQ>(x[j][w], bad, s[w]);
+    }
+}
+
+// The sum of squares of one tile (in every lane of the wave), and its check.
+template <bool SUMSQ>
+__device__ __forceinline__ double list_wave_check(const int32_t* tile0, const ListEntry* entries, int count, int tile,
+                                                  uint32_t& bad)
+{
+    constexpr int kWaves = kListBlock / 64;
+    const ListEntry e = entries[list_find(tile0, count, tile)];
+    const int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile, left = e.n - base;
+    const unsigned char* g = static_cast<const unsigned char*>(e.grad) + base * (e.gf == kF32 ? 4 : 2);
+    const int lane = static_cast<int>(__lane_id());
+    double s[kWaves] = {};
+    if (left >= kListTile && (reinterpret_cast<uintptr_t>(g) & 15) == 0) {
+        if (e.gf == kF32)
+            list_wave_tile<kF32, SUMSQ>(g, lane, bad, s);
+        else if (e.gf == kBF16)
+            list_wave_tile<kBF16, SUMSQ>(g, lane, bad, s);
+        else
+            list_wave_tile<kF16, SUMSQ>(g, lane, bad, s);
+    } else {
+        const int n = static_cast<int>(left < kListTile ? left : kListTile);
+#pragma unroll 1
+        for (int at = 0; at < n; at += 2 * kListBlock) {
+            float x[2][kWaves];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    const int i = at + j * kListBlock + w * 64 + lane;
+                    x[j][w] = i < n ? list_grad1(e.gf, g, i) : 0.0f;
                 }
-            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    bad |= nonfinite_f32(__float_as_uint(x[j][w]));
+                    if constexpr (SUMSQ)
+                        s[w] = s[w] + sq(x[j][w]);
+                }
         }
     }
+    if constexpr (!SUMSQ)
+        return 0.0;
+    static_assert(kWaves == 4, "the butterfly of block_sum_fixed over the waves");
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            s[w] = s[w] + __shfl_xor(s[w], off);
+    return (s[0] + s[2]) + (s[1] + s[3]);
+}
+
+// The check of all (at most kStepCheck) tiles by one block, a tile per wave in
+// turn.  The flag and the sum of squares are in every thread.
+template <bool SUMSQ>
+__device__ __forceinline__ uint32_t list_check_all(const int32_t* tile0, const ListEntry* entries, int count, int tiles,
+                                                   double* lds, double& sum)
+{
+    static_assert(kStepCheck <= 64, "one lane per tile below");
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = static_cast<int>(__lane_id());
+    uint32_t bad = 0u;
+#pragma unroll 1
+    for (int tile = wave; tile < tiles; tile += kListBlock / 64) {
+        const double s = list_wave_check<SUMSQ>(tile0, entries, count, tile, bad);
+        if (SUMSQ && lane == 0)
+            lds[tile] = s;
+    }
+    bad = static_cast<uint32_t>(__syncthreads_or(static_cast<int>(bad)));
+    if constexpr (SUMSQ) {
+        double s = lane < tiles ? lds[lane] : 0.0;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1)
+            s = s + __shfl_xor(s, off);
+        sum = s;
+    }
+    return bad;
+}
+
+// A block per tile: the step's end (and, but for kFrontParts, its check) in
+// one kernel.  The gradients are only read, so the blocks need not meet: each
+// comes to the same flag and sum.
+template <bool E8, bool DITHER, int FRONT>
+__global__ __launch_bounds__(kListBlock, FRONT == kFrontParts ? 4 : 2) void list_step_kernel(ds_scaler* __restrict__ st,
+                                                               const unsigned char* __restrict__ table,
+                                                               uint32_t* __restrict__ tickets, int32_t count,
+                                                               int32_t tiles, ListHyper hp,
+                                                               const double* __restrict__ part)
+{
+    __shared__ double lds[FRONT == kFrontParts ? kListBlock / 64 + 1 : kStepCheck];
+    const int32_t* tile0 = reinterpret_cast<const int32_t*>(table + kTile0At);
+    const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
+    ds_scaler now = list_scaler(st);
+    ListTile<E8, DITHER, false> t;
+    t.load(tile0, entries, count, blockIdx.x);
+    if constexpr (FRONT == kFrontParts) {
+        now.grad_sumsq = now.grad_sumsq + list_sum_parts(part, tiles, lds);
+    } else {
+        double sum = 0.0;
+        now.overflow |= list_check_all<FRONT == kFrontCheckSum>(tile0, entries, count, tiles, lds, sum);
+        if constexpr (FRONT == kFrontCheckSum)
+            now.grad_sumsq = now.grad_sumsq + sum;
+    }
+    if (now.overflow == 0u) {
+        ListStep q = list_step(&now, hp);
+        t.finish(q);
+    }
+    __syncthreads();   // every lane of this block has read the scaler state
+    if (threadIdx.x == 0)
+        list_end_step(st, now, tickets);
 }
 
 // ---- host side ----
@@ -774,7 +1001,7 @@ ds_status list_write(ds_tensor_list* list, void* table, size_t table_bytes, cons
     return DS_OK;
 }
 
-ds_status list_check(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws_bytes, hipStream_t s)
+ds_status list_check_args(const ds_scaler* st, const ds_tensor_list* l, const void* ws, size_t ws_bytes)
 {
     if (const ds_status rc = list_ok(l); rc != DS_OK)
         return rc;
@@ -790,6 +1017,15 @@ ds_status list_check(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws
     if (overlap(st, sizeof(ds_scaler), l->table, tb) || overlap(ws, list_ws_bytes(l->tiles), l->table, tb) ||
         overlap(ws, list_ws_bytes(l->tiles), st, sizeof(ds_scaler)))
         return DS_ERR_ALIAS;
+    return DS_OK;
+}
+
+ds_status list_check(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws_bytes, hipStream_t s)
+{
+    if (const ds_status rc = list_check_args(st, l, ws, ws_bytes); rc != DS_OK)
+        return rc;
+    if (l->tiles == 0)
+        return DS_OK;
     const unsigned blocks = grid_blocks(list_parts(l->tiles), kListBlock);
     const unsigned char* table = static_cast<const unsigned char*>(l->table);
     const int32_t tiles = static_cast<int32_t>(l->tiles);
@@ -823,14 +1059,42 @@ void launch_list_adam(bool nt, bool fuse, unsigned blocks, hipStream_t s, ds_sca
     else    launch_list_adam2<E8, DITHER, false>(fuse, blocks, s, st, l, hp);
 }
 
+// The kernels' hyperparameters from a call's; false: a schedule that is not one.
+bool list_adam_hyper(float lr, const ds_lr_schedule* sched, double beta1, double beta2, float eps, float max_grad_norm,
+                     int32_t accum_steps, AdamHyper* hp)
+{
+    *hp = AdamHyper{lr, static_cast<float>(beta1), static_cast<float>(beta2), eps, 0.0f, max_grad_norm, accum_steps,
+                    0, 0.0f, 0, 0};
+    if (sched == nullptr)
+        return true;
+    if (!schedule_ok(*sched))
+        return false;
+    hp->lr = sched->warmup_max_lr;
+    hp->lr_kind = sched->kind;
+    hp->lr_min = sched->warmup_min_lr;
+    hp->lr_warmup = sched->warmup_num_steps;
+    hp->lr_total = sched->total_num_steps;
+    return true;
+}
+
+bool list_hyper_ok(const AdamHyper& h, double beta1, double beta2, ds_rounding rounding)
+{
+    return finite_ge0(h.lr) && beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && std::isfinite(h.eps) &&
+           h.eps > 0.0f && finite_ge0(h.max_grad_norm) && h.accum_steps >= 1 &&
+           (rounding == DS_ROUND_NEAREST || rounding == DS_ROUND_DITHER);
+}
+
+ListHyper list_hyper(const AdamHyper& h, double beta1, double beta2, uint64_t seed)
+{
+    return ListHyper{h, beta1, beta2, dither_mix(dither_mix(static_cast<uint32_t>(seed >> 32)) ^ static_cast<uint32_t>(seed))};
+}
+
 ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, double beta1, double beta2,
                     ds_rounding rounding, uint64_t seed, bool end_step, hipStream_t s)
 {
     if (const ds_status rc = list_ok(l); rc != DS_OK)
         return rc;
-    if (!finite_ge0(h.lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(h.eps) || h.eps <= 0.0f ||
-        !finite_ge0(h.max_grad_norm) || h.accum_steps < 1 ||
-        (rounding != DS_ROUND_NEAREST && rounding != DS_ROUND_DITHER))
+    if (!list_hyper_ok(h, beta1, beta2, rounding))
         return DS_ERR_HPARAM;
     if (st == nullptr)
         return DS_ERR_NULL;
@@ -844,7 +1108,7 @@ ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, 
     }
     if (overlap(st, sizeof(ds_scaler), l->table, list_bytes(l->count)))
         return DS_ERR_ALIAS;
-    const ListHyper hp{h, beta1, beta2, dither_mix(dither_mix(static_cast<uint32_t>(seed >> 32)) ^ static_cast<uint32_t>(seed))};
+    const ListHyper hp = list_hyper(h, beta1, beta2, seed);
     const bool nt = variant_nt(l->elems);
     const unsigned blocks = grid_blocks(l->tiles, kListBlock);
     const bool e8 = l->sdt != DS_FP32, fuse = end_step && (!e8 || blocks <= kFuseBlocks);
@@ -858,6 +1122,53 @@ ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, 
         if (launched() != DS_OK)
             return DS_ERR_HIP;
         update_scale_kernel<<<1, 1, 0, s>>>(st);
+    }
+    return launched();
+}
+
+template <int FRONT>
+void launch_list_step(hipStream_t s, ds_scaler* st, const ds_tensor_list* l, bool dither, const ListHyper& hp,
+                      const double* part)
+{
+    const unsigned char* table = static_cast<const unsigned char*>(l->table);
+    uint32_t* tickets = static_cast<uint32_t*>(l->table);
+    const int32_t tiles = static_cast<int32_t>(l->tiles), count = l->count;
+    const unsigned b = static_cast<unsigned>(tiles);
+    if (l->sdt == DS_FP32) list_step_kernel<false, false, FRONT><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
+    else if (dither)       list_step_kernel<true, true, FRONT><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
+    else                   list_step_kernel<true, false, FRONT><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
+}
+
+ds_status list_step_all(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws_bytes, const AdamHyper& h,
+                        double beta1, double beta2, ds_rounding rounding, uint64_t seed, hipStream_t s)
+{
+    if (const ds_status rc = list_ok(l); rc != DS_OK)
+        return rc;
+    if (!list_hyper_ok(h, beta1, beta2, rounding))
+        return DS_ERR_HPARAM;
+    // a pinned grid (DSZERO_GRID) is for the kernels that loop over their tiles
+    if (l->tiles < 1 || l->tiles > (ws != nullptr ? kStepParts : kStepCheck) || env_long("DSZERO_GRID", 0) > 0) {
+        if (const ds_status rc = list_check(st, l, ws, ws_bytes, s); rc != DS_OK)
+            return rc;
+        return list_adam(st, l, h, beta1, beta2, rounding, seed, true, s);
+    }
+    const bool alone = l->tiles <= kStepCheck;
+    const ListHyper hp = list_hyper(h, beta1, beta2, seed);
+    if (const ds_status rc = list_check_args(st, l, ws, ws_bytes); rc != DS_OK)
+        return rc;
+    const bool dither = rounding == DS_ROUND_DITHER;
+    double* part = static_cast<double*>(ws);
+    if (alone && ws == nullptr) {
+        launch_list_step<kFrontCheck>(s, st, l, dither, hp, nullptr);
+    } else if (alone) {
+        launch_list_step<kFrontCheckSum>(s, st, l, dither, hp, nullptr);
+    } else {
+        const int32_t tiles = static_cast<int32_t>(l->tiles);
+        list_check_kernel<true><<<static_cast<unsigned>(list_parts(tiles)), kListBlock, 0, s>>>(
+            st, static_cast<const unsigned char*>(l->table), l->count, tiles, part);
+        if (launched() != DS_OK)
+            return DS_ERR_HIP;
+        launch_list_step<kFrontParts>(s, st, l, dither, hp, part);
     }
     return launched();
 }

@@ -11,8 +11,8 @@ per 256 elements: 2.03 bytes per element for both states instead of 8).
     step.set_gradients([p.grad for p in params])     # again when a gradient's address changes
     step.step()                                      # check, norm (if clipped), Adam, scaler
 
-A step is two kernels (check, Adam), four with clipping, and no host
-synchronisation; it can be captured into a graph.
+A step is one to four kernels (a short list is checked by the kernel that
+updates it) and no host synchronisation; it can be captured into a graph.
 """
 from __future__ import annotations
 
@@ -57,7 +57,8 @@ class MultiTensorStep:
     ``m`` is float8_e4m3fn and ``v`` float8_e5m2, and ``m_scale``, ``v_scale`` hold one scale per 256 elements.
     ``dither_seed`` (8-bit states): None rounds to nearest, a number rounds with the dither of that seed.
     ``weight_decay`` and ``lr_scale``: one number, or one per tensor (default: the configuration's decay, and 1).
-    ``state``: share another step's scaler (then ``end_step`` says which call of a step advances it)."""
+    ``state``: share another step's scaler.  Then check() is called on every step that shares it before update() on
+    the first, and only the last has ``end_step``."""
 
     def __init__(self, params, cfg: ZeroMPConfig, states="fp32", weight_decay=None, lr_scale=None, dither_seed=None,
                  stream=None, state=None, end_step=True):
@@ -112,6 +113,8 @@ class MultiTensorStep:
                 for i, p in enumerate(self.params):
                     if p.dtype != torch.float32:
                         self.view(self.master, i).copy_(p.detach().reshape(-1))
+            if state is not None and state.device != device:
+                raise ValueError(f"state: expected a scaler on {device}, got one on {state.device}")
             self.state = state
             if state is None:
                 self.state = torch.zeros(_lib.ds_scaler_size(), dtype=torch.uint8, device=device)
@@ -142,7 +145,7 @@ class MultiTensorStep:
             t.pdt = _dtype_of(p, torch, f"parameter {i}")
         self._grads, self._list, self._list_at = None, None, None
         # what every step passes: this object's own arrays, sized and placed here
-        self._state_at = self.state.data_ptr()
+        self._state_at = _lib._scaler(self.state)
         self._ws_at = None if self.ws is None else self.ws.data_ptr()
         self._ws_bytes = 0 if self.ws is None else self.ws.numel() * 8
         self._sched_at = None if self.sched is None else ctypes.byref(self.sched)
@@ -178,14 +181,35 @@ class MultiTensorStep:
 
     def step(self) -> None:
         """One step on the gradients set: overflow check (with the joint norm if clipped), gated Adam, scaler."""
+        if not self.end_step:
+            self.check()
+            self.update()
+            return
         if self._list is None:
             raise RuntimeError("set_gradients() before step()")
-        c, lib, ok, s = self.cfg, _lib.lib, _lib._ok, _lib._stream_on(self.stream, self._device)
-        st, lst = self._state_at, self._list_at
-        ok(lib.ds_check_overflow_list(st, lst, self._ws_at, self._ws_bytes, s), "ds_check_overflow_list")
-        ok(lib.ds_adam_step_list(st, lst, c.lr, self._sched_at, c.betas[0], c.betas[1], c.eps, c.gradient_clipping,
-                                 c.gradient_accumulation_steps, self._rounding, self._seed, self.end_step, s),
-           "ds_adam_step_list")
+        c = self.cfg
+        _lib._ok(_lib.lib.ds_step_list(self._state_at, self._list_at, self._ws_at, self._ws_bytes, c.lr, self._sched_at,
+                                       c.betas[0], c.betas[1], c.eps, c.gradient_clipping, c.gradient_accumulation_steps,
+                                       self._rounding, self._seed, _lib._stream_on(self.stream, self._device)),
+                 "ds_step_list")
+
+    def check(self) -> None:
+        """The first half of step(): the overflow check, with the sum of squares if clipped.  Where several steps share
+        a scaler, every check() comes before the first update(), so that all of them see one flag and one norm."""
+        if self._list is None:
+            raise RuntimeError("set_gradients() before check()")
+        _lib._ok(_lib.lib.ds_check_overflow_list(self._state_at, self._list_at, self._ws_at, self._ws_bytes,
+                                                 _lib._stream_on(self.stream, self._device)), "ds_check_overflow_list")
+
+    def update(self) -> None:
+        """The second half of step(): gated Adam and, with ``end_step``, the scaler."""
+        if self._list is None:
+            raise RuntimeError("set_gradients() before update()")
+        c = self.cfg
+        _lib._ok(_lib.lib.ds_adam_step_list(self._state_at, self._list_at, c.lr, self._sched_at, c.betas[0], c.betas[1],
+                                            c.eps, c.gradient_clipping, c.gradient_accumulation_steps, self._rounding,
+                                            self._seed, self.end_step, _lib._stream_on(self.stream, self._device)),
+                 "ds_adam_step_list")
 
     @property
     def loss_scale(self):
