@@ -624,8 +624,8 @@ ds_status ds_adam_step_list(ds_scaler* st, const ds_tensor_list* list, float lr,
  * A whole step over one list: ds_check_overflow_list, then ds_adam_step_list
  * with end_step, to the same bits.  Short lists take fewer launches: one up to
  * 8 tiles, where every block of the update checks the whole list itself, and
- * with a workspace two up to 2048 tiles, where it adds the check's partial
- * sums itself.  What was checked before in the same step (a flat partition,
+ * with a workspace two up to 2048 tiles, where every block adds the check's
+ * partial sums itself.  What was checked before in the same step (a flat partition,
  * another list) counts here as for ds_adam_step_list.  Errors as for the two
  * calls; refused as a whole.
  */

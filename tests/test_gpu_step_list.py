@@ -9,12 +9,14 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
 TILE = 4096
-# tiles: 1, 2, 4, 8 (checked by the update), 9 and 300 (partial sums added by the update), 2048, 2049 (either side)
+# tiles: 1, 4, 8 (checked by the update), 9, 100 and 300 (a quarter of a tile a block, a whole one), 2048, 2049 (partial
+# sums added by the update, or by a kernel of their own)
 LISTS = {
     "one": [1],
     "few": [TILE, TILE, 64, 1],
     "eight": [3 * TILE, 0, 2 * TILE + 5, TILE - 1, 77],
     "nine": [8 * TILE, 1],
+    "hundred": [TILE + 3 * k for k in range(49)] + [TILE - 1, 3, 0, 257],
     "three hundred": [TILE + 3 * k for k in range(148)] + [4 * TILE],
     "2048": [2000 * TILE, 48 * TILE],
     "2049": [2000 * TILE, 48 * TILE, 3],

@@ -88,6 +88,20 @@ __device__ __forceinline__ int list_find(const int32_t* __restrict__ tile0, int 
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// list_find of two tiles (at once where one load serves both).
+__device__ __forceinline__ void list_find2(const int32_t* __restrict__ tile0, int count, int a, int b, int& of_a, int& of_b)
+{
+    if (count > 64) {
+        of_a = list_find(tile0, count, a);
+        of_b = list_find(tile0, count, b);
+        return;
+    }
+    const int lane = static_cast<int>(__lane_id());
+    const int first = lane < count ? tile0[lane] : 0x7FFFFFFF;
+    of_a = __popcll(__ballot(first <= a)) - 1;
+    of_b = __popcll(__ballot(first <= b)) - 1;
+}
+
 // Loads and stores through pointers that come from the table: they are known
 // to be global memory, not the generic pointers that the compiler must take
 // them for (whose accesses also occupy the shared memory's counters).
@@ -150,25 +164,50 @@ __device__ __forceinline__ void list_check_tiles(const void* grad, uint32_t& bad
         list_check_vec<GF, SUMSQ>(w[j], bad, s);
 }
 
-// Tile `left` elements from its tensor's end (whole and aligned, or not).
+template <bool SUMSQ>
+__device__ __forceinline__ void list_check_any(int gf, const u32x4& w, uint32_t& bad, double& s)
+{
+    if (gf == kF32)
+        list_check_vec<kF32, SUMSQ>(w, bad, s);
+    else if (gf == kBF16)
+        list_check_vec<kBF16, SUMSQ>(w, bad, s);
+    else
+        list_check_vec<kF16, SUMSQ>(w, bad, s);
+}
+
+template <bool SUMSQ>
+__device__ __forceinline__ void list_check1(float x, uint32_t& bad, double& s)
+{
+    bad |= nonfinite_f32(__float_as_uint(x));
+    if constexpr (SUMSQ)
+        s = s + sq(x);
+}
+
+// Tile `left` elements from its tensor's end.  Aligned: whole vectors, vector
+// j * kListBlock + l by lane l in j order, then the elements left over, one a
+// lane; else element j * kListBlock + l by lane l.
 template <bool SUMSQ>
 __device__ __forceinline__ void list_check_tile(const unsigned char* g, int gf, int64_t left, uint32_t& bad, double& s)
 {
-    if (left >= kListTile && (reinterpret_cast<uintptr_t>(g) & 15) == 0) {
+    const bool fast = (reinterpret_cast<uintptr_t>(g) & 15) == 0;
+    if (fast && left >= kListTile) {
         if (gf == kF32)
             list_check_tiles<kF32, SUMSQ, 1>(g, bad, s);
         else if (gf == kBF16)
             list_check_tiles<kBF16, SUMSQ, 1>(g, bad, s);
         else
             list_check_tiles<kF16, SUMSQ, 1>(g, bad, s);
-    } else {
-        for (int64_t i = threadIdx.x; i < left && i < kListTile; i += kListBlock) {
-            const float x = list_grad1(gf, g, i);
-            bad |= nonfinite_f32(__float_as_uint(x));
-            if constexpr (SUMSQ)
-                s = s + sq(x);
-        }
+        return;
     }
+    const int n = static_cast<int>(left < kListTile ? left : kListTile), per = gf == kF32 ? 4 : 8, me = threadIdx.x;
+    int done = 0;
+    if (fast) {
+        for (int v = me; v < n / per; v += kListBlock)
+            list_check_any<SUMSQ>(gf, gload(reinterpret_cast<const u32x4*>(g) + v), bad, s);
+        done = n / per * per;
+    }
+    for (int i = done + me; i < n; i += kListBlock)
+        list_check1<SUMSQ>(list_grad1(gf, g, i), bad, s);
 }
 
 __host__ __device__ inline int list_turn(int64_t tiles) { return tiles <= kCheckFew ? 1 : kCheckTiles; }
@@ -384,12 +423,14 @@ __device__ __forceinline__ void adam1_fp8(float graw, float& p, float& m, float&
 // A tile's quads in registers, four per lane.
 template <bool E8>
 struct ListRegs {
-    f32x4 g[kListQuads], p[kListQuads], m[kListQuads], v[kListQuads];
+    u32x2 g[kListQuads], g2[kListQuads];
+    f32x4 p[kListQuads], m[kListQuads], v[kListQuads];
 };
 
 template <>
 struct ListRegs<true> {
-    f32x4 g[kListQuads], p[kListQuads];
+    u32x2 g[kListQuads], g2[kListQuads];
+    f32x4 p[kListQuads];
     uint32_t m[kListQuads], v[kListQuads];
     float m_scale[kListQuads], v_scale[kListQuads];
 };
@@ -427,69 +468,67 @@ __device__ __forceinline__ void list_load(const ListEntry& e, int64_t base, List
                 r.v[u] = gload<NT>(static_cast<const f32x4*>(e.v) + q);
             }
         } else {
-            r.p[u] = f32x4{0, 0, 0, 0};
-            r.m[u] = r.v[u] = {};
+            f32x4 p = {0, 0, 0, 0};
+            decltype(r.m[0] + r.m[0]) m = {}, v = {};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int64_t i = 4 * q + k;
                 if (i < e.n) {
-                    r.p[u][k] = gload(e.master + i);
+                    p[k] = gload(e.master + i);
                     if constexpr (E8) {
-                        r.m[u] |= static_cast<uint32_t>(gload(static_cast<const uint8_t*>(e.m) + i)) << (8 * k);
-                        r.v[u] |= static_cast<uint32_t>(gload(static_cast<const uint8_t*>(e.v) + i)) << (8 * k);
+                        m |= static_cast<uint32_t>(gload(static_cast<const uint8_t*>(e.m) + i)) << (8 * k);
+                        v |= static_cast<uint32_t>(gload(static_cast<const uint8_t*>(e.v) + i)) << (8 * k);
                     } else {
-                        r.m[u][k] = gload(static_cast<const float*>(e.m) + i);
-                        r.v[u][k] = gload(static_cast<const float*>(e.v) + i);
+                        m[k] = gload(static_cast<const float*>(e.m) + i);
+                        v[k] = gload(static_cast<const float*>(e.v) + i);
                     }
                 }
             }
+            r.p[u] = p;
+            r.m[u] = m;
+            r.v[u] = v;
         }
     }
-    // the gradients last: what converts them waits for all of the loads
-    if (e.gf == kF32) {
+    // The gradient's bits: the first two words hold a 16-bit quad, and all four
+    // an fp32 one (two loads: with one of four words for fp32 alone, merging
+    // the two kinds of registers would wait here for every load).  Widened by
+    // list_widen, once all loads are on their way and the constants formed.
+    const bool wide = e.gf == kF32;
+    const unsigned char* grad = static_cast<const unsigned char*>(e.grad);
+    if (FULL || (e.vec && 4 * (q0 + (U - 1) * kListBlock) + 4 <= e.n)) {
+        const int64_t size = wide ? 16 : 8;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t q = q0 + u * kListBlock;
-            if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
-                r.g[u] = gload<NT>(static_cast<const f32x4*>(e.grad) + q);
-            } else {
-                r.g[u] = f32x4{0, 0, 0, 0};
+        for (int u = 0; u < U; ++u)
+            r.g[u] = gload<NT>(reinterpret_cast<const u32x2*>(grad + (q0 + u * kListBlock) * size));
+        if (wide) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (4 * q + k < e.n)
-                        r.g[u][k] = gload(static_cast<const float*>(e.grad) + 4 * q + k);
-            }
+            for (int u = 0; u < U; ++u)
+                r.g2[u] = gload<NT>(reinterpret_cast<const u32x2*>(grad + (q0 + u * kListBlock) * 16 + 8));
         }
     } else {
+        static_assert(FULL || U == 1, "one quad");
+        uint32_t x[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t q = q0 + u * kListBlock;
-            u32x2 w = {0u, 0u};
-            if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
-                w = gload<NT>(static_cast<const u32x2*>(e.grad) + q);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (4 * q + k < e.n)
-                        w[k / 2] |= static_cast<uint32_t>(gload(static_cast<const uint16_t*>(e.grad) + 4 * q + k))
-                                    << (16 * (k % 2));
+        for (int k = 0; k < 4; ++k) {
+            const int64_t i = 4 * q0 + k;
+            x[k] = 0u;
+            if (i < e.n) {
+                if (wide)
+                    x[k] = gload(reinterpret_cast<const uint32_t*>(grad) + i);
+                else
+                    x[k] = gload(reinterpret_cast<const uint16_t*>(grad) + i);
             }
-            r.g[u].x = __uint_as_float(w.x);   // widened by list_widen, once every load is on its way
-            r.g[u].y = __uint_as_float(w.y);
         }
+        r.g[0] = wide ? u32x2{x[0], x[1]} : u32x2{x[0] | x[1] << 16, x[2] | x[3] << 16};
+        r.g2[0] = u32x2{x[2], x[3]};
     }
 }
 
-template <bool E8, int U>
-__device__ __forceinline__ void list_widen(int gf, ListRegs<E8>& r)
+__device__ __forceinline__ f32x4 list_widen(int gf, const u32x2& a, const u32x2& b)
 {
     if (gf == kF32)
-        return;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const u32x2 w = {__float_as_uint(r.g[u].x), __float_as_uint(r.g[u].y)};
-        r.g[u] = gf == kBF16 ? widen4<kBF16>(w) : widen4<kF16>(w);
-    }
+        return f32x4{__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(b.x), __uint_as_float(b.y)};
+    return gf == kBF16 ? widen4<kBF16>(a) : widen4<kF16>(a);
 }
 
 // Update and stores of the U quads loaded by list_load.
@@ -498,7 +537,12 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
                                             uint32_t key)
 {
     const int64_t q0 = base / 4 + threadIdx.x;
-    list_widen<E8, U>(e.gf, r);
+    f32x4 g[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const u32x2 lo = r.g[u], hi = r.g2[u];
+        g[u] = list_widen(e.gf, lo, hi);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t q = q0 + u * kListBlock, blk = list_block(base, u);
@@ -518,11 +562,11 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float pk = p[k], mk = m[k], vk = v[k];
-                adam1_fp8(r.g[u][k], pk, mk, vk, c);
+                adam1_fp8(g[u][k], pk, mk, vk, c);
                 p[k] = pk, m[k] = mk, v[k] = vk;
             }
         } else {
-            list_update(r.g[u], p, m, v, c.lrwd != 0.0f, c);
+            list_update(g[u], p, m, v, c.lrwd != 0.0f, c);
         }
         if constexpr (E8) {
             float sm, sv;
@@ -569,35 +613,46 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
     }
 }
 
-// The tile of one block in flight.  A whole aligned one is loaded at once; any
-// other goes one quad per lane after another when its turn comes (its code
-// once, not four times: a short list's time is in part the fetching of code
-// that no block has run before).
-template <bool E8, bool DITHER, bool NT>
+// What one block has in flight: a tile, or with U = 1 a quarter of one (a quad
+// per lane).  A whole aligned tile is loaded at once; any other goes one quad
+// per lane after another when its turn comes (its code once, not four times: a
+// short list's time is in part the fetching of code that no block has run
+// before).
+template <bool E8, bool DITHER, bool NT, int U>
 struct ListTile {
+    static_assert(U == 1 || U == kListQuads, "a quarter or a whole tile");
     ListEntry e;
     int64_t base;
     bool full;
-    uint32_t index;
+    int index;
     ListRegs<E8> r;
 
-    __device__ __forceinline__ void load(const int32_t* tile0, const ListEntry* entries, int count, int tile)
+    // `part` of kListQuads / U of the tile
+    __device__ __forceinline__ void set(const ListEntry* entries, int tile, int part)
     {
-        const int j = list_find(tile0, count, tile);
-        e = entries[j];
-        index = static_cast<uint32_t>(j);
-        base = static_cast<int64_t>(tile - e.tile0) * kListTile;
-        full = e.vec && e.n - base >= kListTile;
-        if (full)
-            list_load<E8, NT, true, kListQuads>(e, base, r);
+        e = entries[index];
+        base = static_cast<int64_t>(tile - e.tile0) * kListTile + part * (U * 4 * kListBlock);
+        full = U == kListQuads && e.vec && e.n - base >= kListTile;
+    }
+
+    __device__ __forceinline__ void load()
+    {
+        if constexpr (U == 1)
+            list_load<E8, false, false, 1>(e, base, r);
+        else if (full)
+            list_load<E8, NT, true, U>(e, base, r);
     }
 
     __device__ __forceinline__ void finish(ListStep& q)
     {
         list_tensor_consts(e, q);
-        const uint32_t key = DITHER ? dither_mix(q.key + index * kGold) : 0u;
+        const uint32_t key = DITHER ? dither_mix(q.key + static_cast<uint32_t>(index) * kGold) : 0u;
+        if constexpr (U == 1) {
+            list_finish<E8, DITHER, false, false, 1>(e, base, r, q.c, key);
+            return;
+        }
         if (full) {
-            list_finish<E8, DITHER, NT, true, kListQuads>(e, base, r, q.c, key);
+            list_finish<E8, DITHER, NT, true, U>(e, base, r, q.c, key);
             return;
         }
         const int64_t end = e.n - base < kListTile ? e.n : base + kListTile;
@@ -633,29 +688,38 @@ __device__ __forceinline__ ds_scaler list_scaler(const ds_scaler* st)
     return s;
 }
 
-// Takes this block's ticket; the last block advances the scaler from `now`,
-// the state as it was when the kernel started.  Up to kTicketLines blocks take
-// it from the scaler's counter at once.
-__device__ __forceinline__ void list_end_step(ds_scaler* st, const ds_scaler& now, uint32_t* tickets)
+// A block's ticket: taken by thread 0 once all of the block has read the scaler
+// (and found the step's flag and norm), so early that the update hides the
+// atomic; the last block then advances the scaler from `now`, what it has read.
+// Up to kTicketLines blocks take theirs from the scaler's counter at once.
+__device__ __forceinline__ unsigned list_lines() { return gridDim.x <= 1024 ? 16 : kTicketLines; }
+
+__device__ __forceinline__ uint32_t list_ticket(ds_scaler* st, uint32_t* tickets)
 {
-    const unsigned lines = gridDim.x < kTicketLines ? gridDim.x : kTicketLines;
+    if (gridDim.x <= kTicketLines)
+        return atomicAdd(&st->blocks_done, 1u);
+    return atomicAdd(tickets + blockIdx.x % list_lines() * (kTicketBytes / 4), 1u);
+}
+
+__device__ __forceinline__ void list_end_step(ds_scaler* st, const ds_scaler& now, uint32_t* tickets, uint32_t before)
+{
     if (gridDim.x > kTicketLines) {
-        const unsigned line = blockIdx.x % kTicketLines;
-        const unsigned of_line = (gridDim.x - line + kTicketLines - 1) / kTicketLines;
-        uint32_t* ticket = tickets + line * (kTicketBytes / 4);
-        if (atomicAdd(ticket, 1u) != of_line - 1u)
+        const unsigned lines = list_lines(), line = blockIdx.x % lines;
+        if (before != (gridDim.x - line + lines - 1) / lines - 1u)
             return;
-        *ticket = 0u;
+        tickets[line * (kTicketBytes / 4)] = 0u;
+        if (atomicAdd(&st->blocks_done, 1u) != lines - 1u)
+            return;
+    } else if (before != gridDim.x - 1u) {
+        return;
     }
-    if (atomicAdd(&st->blocks_done, 1u) == lines - 1u) {
-        const ds_scaler s = advanced(now, now.overflow);
-        u32x4 x[kScalerWords / 4];
-        __builtin_memcpy(x, &s, sizeof(x));
+    const ds_scaler s = advanced(now, now.overflow);
+    u32x4 x[kScalerWords / 4];
+    __builtin_memcpy(x, &s, sizeof(x));
 #pragma unroll
-        for (int i = 0; i < kScalerWords / 4; ++i)
-            reinterpret_cast<u32x4*>(st)[i] = x[i];
-        st->blocks_done = 0u;
-    }
+    for (int i = 0; i < kScalerWords / 4; ++i)
+        reinterpret_cast<u32x4*>(st)[i] = x[i];
+    st->blocks_done = 0u;
 }
 
 // One tile per block and loop turn.  The step's constants (fp64 powers and
@@ -669,161 +733,178 @@ __global__ __launch_bounds__(kListBlock, 4) void list_adam_kernel(ds_scaler* __r
     const int32_t* tile0 = reinterpret_cast<const int32_t*>(table + kTile0At);
     const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
     const ds_scaler now = list_scaler(st);
+    uint32_t before = 0u;
+    if constexpr (FUSE) {
+        __syncthreads();   // every wave of this block has read the scaler
+        if (threadIdx.x == 0)
+            before = list_ticket(st, tickets);
+    }
     if (now.overflow == 0u) {
         ListStep q;
         bool first = true;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            ListTile<E8, DITHER, NT> t;
-            t.load(tile0, entries, count, tile);
+            ListTile<E8, DITHER, NT, kListQuads> t;
+            t.index = list_find(tile0, count, tile);
+            t.set(entries, tile, 0);
+            t.load();
             if (first)
                 q = list_step(&now, hp);
             first = false;
             t.finish(q);
         }
     }
-    if constexpr (FUSE) {
-        __syncthreads();   // every lane of this block has read the scaler state
+    if constexpr (FUSE)
         if (threadIdx.x == 0)
-            list_end_step(st, now, tickets);
-    }
+            list_end_step(st, now, tickets, before);
 }
 
 // ---- a whole step over a short list ----
 
 // Up to kStepParts tiles every block adds the check's partial sums itself,
-// instead of a kernel between the check and the update; up to kStepCheck tiles
-// every block also checks the whole list itself, instead of a kernel before.
-constexpr int kStepParts = 2048, kStepCheck = 8;
+// instead of a kernel between the check and the update (363 tiles: 14.0 us a
+// step, 17.3); up to kStepCheck tiles every block also checks the whole list
+// itself, instead of a kernel before (four tiles: 5.3 us, 8.8; eight with the
+// norm: 8.7, 9.1).  Up to kStepQuarter tiles a block does a quarter of one:
+// the code that a block runs for the first time is then a third as long, and
+// fetching it is most of so short a kernel's time (64 tiles with the norm:
+// 9.1 us, 10.6 with a tile a block; 256: 13.0, 12.6).
+constexpr int kStepParts = 2048, kStepQuarter = 128, kStepCheck = 8;
 static_assert(kStepParts <= kCheckFew && kStepParts <= kGroup && kFinishBlock == kListBlock,
               "one group of one tile's sums each: the order of sumsq_finish_kernel");
-enum ListFront { kFrontParts, kFrontCheck, kFrontCheckSum };
+enum ListFront { kFrontNone, kFrontParts, kFrontCheck, kFrontCheckSum };
+constexpr bool list_checks(int front) { return front == kFrontCheck || front == kFrontCheckSum; }
 
-// The sum over part[0 .. parts): sumsq_finish_kernel's, in its order.  In every thread.
-__device__ __forceinline__ double list_sum_parts(const double* part, int parts, double* lds)
-{
+// This lane's share of the sum over part[0 .. parts), in sumsq_finish_kernel's order.
+struct ListParts {
     double x[kStepParts / kListBlock];
+
+    __device__ __forceinline__ void load(const double* part, int parts)
+    {
 #pragma unroll
-    for (int j = 0; j < kStepParts / kListBlock; ++j) {
-        const int i = j * kListBlock + static_cast<int>(threadIdx.x);
-        x[j] = i < parts ? part[i] : 0.0;
+        for (int j = 0; j < kStepParts / kListBlock; ++j) {
+            const int i = j * kListBlock + static_cast<int>(threadIdx.x);
+            x[j] = part[i < parts ? i : 0];     // past the end: left out below (no branch between the loads)
+        }
     }
-    double s = 0.0;
+
+    __device__ __forceinline__ double lane_sum(int parts) const
+    {
+        double s = 0.0;
 #pragma unroll
-    for (int j = 0; j < kStepParts / kListBlock; ++j)
-        s = s + x[j];
-    s = block_sum_fixed<kListBlock>(s, lds, 0);
-    if (threadIdx.x == 0)
-        lds[kListBlock / 64] = s;
-    __syncthreads();
-    return lds[kListBlock / 64];
-}
+        for (int j = 0; j < kStepParts / kListBlock; ++j)
+            s = s + (j * kListBlock + static_cast<int>(threadIdx.x) < parts ? x[j] : 0.0);
+        return s;
+    }
+};
 
 // One tile checked by one wave, lane by lane as the four waves of
-// list_check_kernel's block do it: s[w] is what lane `lane` of its wave w sums.
-template <int GF, bool SUMSQ>
-__device__ __forceinline__ void list_wave_tile(const void* grad, int lane, uint32_t& bad, double (&s)[kListBlock / 64])
-{
-    constexpr int kPer = GF == kF32 ? 4 : 8, kWaves = kListBlock / 64;
-    constexpr int kVecs = static_cast<int>(kListTile) / (kListBlock * kPer);
-    const u32x4* G = static_cast<const u32x4*>(grad) + lane;
-#pragma unroll 1
-    for (int i = 0; i < kVecs; i += 2) {   // 8 vectors at once: the block's own tile is in registers meanwhile
-        u32x4 x[2][kWaves];
+// list_check_kernel's block do it (list_check_tile): s[w] is what lane `lane`
+// of its wave w sums.  512 vectors are in registers at a time, half an fp32
+// tile or a whole one of 16 bits.
+template <bool SUMSQ>
+struct ListWaveCheck {
+    static constexpr int kWaves = kListBlock / 64;
+    const unsigned char* g;
+    int gf, n;
+    bool fast;
+    u32x4 x[2][kWaves];
+
+    __device__ __forceinline__ void set(const ListEntry& e, int tile)
+    {
+        const int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile, left = e.n - base;
+        gf = e.gf;
+        g = static_cast<const unsigned char*>(e.grad) + base * (gf == kF32 ? 4 : 2);
+        n = static_cast<int>(left < kListTile ? left : kListTile);
+        fast = (reinterpret_cast<uintptr_t>(g) & 15) == 0;
+    }
+
+    __device__ __forceinline__ void load(int first)
+    {
+        const int vecs = fast ? n / (gf == kF32 ? 4 : 8) : 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                x[j][w] = gload(G + (i + j) * kListBlock + w * 64);
+            for (int w = 0; w < kWaves; ++w) {
+                const int v = first + j * kListBlock + w * 64 + static_cast<int>(__lane_id());
+                x[j][w] = u32x4{0u, 0u, 0u, 0u};     // adds nothing
+                if (v < vecs)
+                    x[j][w] = gload(reinterpret_cast<const u32x4*>(g) + v);
+            }
+    }
+
+    template <int GF>
+    __device__ __forceinline__ void add(uint32_t& bad, double (&s)[kWaves]) const
+    {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
                 list_check_vec<GF, SUMSQ>(x[j][w], bad, s[w]);
     }
-}
 
-// The sum of squares of one tile (in every lane of the wave), and its check.
-template <bool SUMSQ>
-__device__ __forceinline__ double list_wave_check(const int32_t* tile0, const ListEntry* entries, int count, int tile,
-                                                  uint32_t& bad)
-{
-    constexpr int kWaves = kListBlock / 64;
-    const ListEntry e = entries[list_find(tile0, count, tile)];
-    const int64_t base = static_cast<int64_t>(tile - e.tile0) * kListTile, left = e.n - base;
-    const unsigned char* g = static_cast<const unsigned char*>(e.grad) + base * (e.gf == kF32 ? 4 : 2);
-    const int lane = static_cast<int>(__lane_id());
-    double s[kWaves] = {};
-    if (left >= kListTile && (reinterpret_cast<uintptr_t>(g) & 15) == 0) {
-        if (e.gf == kF32)
-            list_wave_tile<kF32, SUMSQ>(g, lane, bad, s);
-        else if (e.gf == kBF16)
-            list_wave_tile<kBF16, SUMSQ>(g, lane, bad, s);
-        else
-            list_wave_tile<kF16, SUMSQ>(g, lane, bad, s);
-    } else {
-        const int n = static_cast<int>(left < kListTile ? left : kListTile);
+    // The check of the tile whose first 512 vectors are loaded; its sum, in every lane.
+    __device__ __forceinline__ double finish(uint32_t& bad)
+    {
+        const int lane = static_cast<int>(__lane_id());
+        double s[kWaves] = {};
+        if (fast) {
+            if (gf == kBF16) {
+                add<kBF16>(bad, s);
+            } else if (gf == kF16) {
+                add<kF16>(bad, s);
+            } else {
+                add<kF32>(bad, s);
+                if (n > static_cast<int>(kListTile) / 2) {
+                    load(2 * kListBlock);
+                    add<kF32>(bad, s);
+                }
+            }
+            const int left = n % (gf == kF32 ? 4 : 8);
+            if (left != 0 && lane < left)
+                list_check1<SUMSQ>(list_grad1(gf, g, n - left + lane), bad, s[0]);
+        } else {
 #pragma unroll 1
-        for (int at = 0; at < n; at += 2 * kListBlock) {
-            float x[2][kWaves];
+            for (int at = 0; at < n; at += 2 * kListBlock) {
+                float y[2][kWaves];
+                if (gf == kF32) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                    for (int i = 0; i < 2 * kWaves; ++i) {
+                        const int e = at + i * 64 + lane;
+                        y[i / kWaves][i % kWaves] = e < n ? gload(reinterpret_cast<const float*>(g) + e) : 0.0f;
+                    }
+                } else {
+                    uint32_t h[2 * kWaves];
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    const int i = at + j * kListBlock + w * 64 + lane;
-                    x[j][w] = i < n ? list_grad1(e.gf, g, i) : 0.0f;
+                    for (int i = 0; i < 2 * kWaves; ++i) {
+                        const int e = at + i * 64 + lane;
+                        h[i] = e < n ? gload(reinterpret_cast<const uint16_t*>(g) + e) : 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2 * kWaves; ++i)
+                        y[i / kWaves][i % kWaves] = gf == kBF16 ? dec1<kBF16>(h[i]) : dec1<kF16>(h[i]);
                 }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    bad |= nonfinite_f32(__float_as_uint(x[j][w]));
-                    if constexpr (SUMSQ)
-                        s[w] = s[w] + sq(x[j][w]);
-                }
+                for (int i = 0; i < 2 * kWaves; ++i)
+                    list_check1<SUMSQ>(y[i / kWaves][i % kWaves], bad, s[i % kWaves]);
+            }
         }
-    }
-    if constexpr (!SUMSQ)
-        return 0.0;
-    static_assert(kWaves == 4, "the butterfly of block_sum_fixed over the waves");
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1)
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            s[w] = s[w] + __shfl_xor(s[w], off);
-    return (s[0] + s[2]) + (s[1] + s[3]);
-}
-
-// The check of all (at most kStepCheck) tiles by one block, a tile per wave in
-// turn.  The flag and the sum of squares are in every thread.
-template <bool SUMSQ>
-__device__ __forceinline__ uint32_t list_check_all(const int32_t* tile0, const ListEntry* entries, int count, int tiles,
-                                                   double* lds, double& sum)
-{
-    static_assert(kStepCheck <= 64, "one lane per tile below");
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = static_cast<int>(__lane_id());
-    uint32_t bad = 0u;
-#pragma unroll 1
-    for (int tile = wave; tile < tiles; tile += kListBlock / 64) {
-        const double s = list_wave_check<SUMSQ>(tile0, entries, count, tile, bad);
-        if (SUMSQ && lane == 0)
-            lds[tile] = s;
-    }
-    bad = static_cast<uint32_t>(__syncthreads_or(static_cast<int>(bad)));
-    if constexpr (SUMSQ) {
-        double s = lane < tiles ? lds[lane] : 0.0;
+        if constexpr (!SUMSQ)
+            return 0.0;
+        static_assert(kWaves == 4, "the butterfly of block_sum_fixed over the waves");
 #pragma unroll
         for (int off = 32; off > 0; off >>= 1)
-            s = s + __shfl_xor(s, off);
-        sum = s;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                s[w] = s[w] + __shfl_xor(s[w], off);
+        return (s[0] + s[2]) + (s[1] + s[3]);
     }
-    return bad;
-}
+};
 
-// A block per tile: the step's end (and, but for kFrontParts, its check) in
-// one kernel.  The gradients are only read, so the blocks need not meet: each
-// comes to the same flag and sum.
-template <bool E8, bool DITHER, int FRONT>
-__global__ __launch_bounds__(kListBlock, FRONT == kFrontParts ? 4 : 2) void list_step_kernel(ds_scaler* __restrict__ st,
+// A block per tile, or four: the step's end (and with kFrontCheck and
+// kFrontCheckSum its check) in one kernel.  The gradients are only read, so
+// the blocks need not meet: each comes to the same flag and sum.
+template <bool E8, bool DITHER, int FRONT, int U>
+__global__ __launch_bounds__(kListBlock, list_checks(FRONT) ? 2 : 4) void list_step_kernel(ds_scaler* __restrict__ st,
                                                                const unsigned char* __restrict__ table,
                                                                uint32_t* __restrict__ tickets, int32_t count,
                                                                int32_t tiles, ListHyper hp,
@@ -833,23 +914,74 @@ __global__ __launch_bounds__(kListBlock, FRONT == kFrontParts ? 4 : 2) void list
     const int32_t* tile0 = reinterpret_cast<const int32_t*>(table + kTile0At);
     const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
     ds_scaler now = list_scaler(st);
-    ListTile<E8, DITHER, false> t;
-    t.load(tile0, entries, count, blockIdx.x);
+    constexpr int kSplit = kListQuads / U;
+    const int own = blockIdx.x / kSplit, part_of = blockIdx.x % kSplit;
+    ListTile<E8, DITHER, false, U> t;
+    double mine = 0.0;
     if constexpr (FRONT == kFrontParts) {
-        now.grad_sumsq = now.grad_sumsq + list_sum_parts(part, tiles, lds);
-    } else {
-        double sum = 0.0;
-        now.overflow |= list_check_all<FRONT == kFrontCheckSum>(tile0, entries, count, tiles, lds, sum);
-        if constexpr (FRONT == kFrontCheckSum)
-            now.grad_sumsq = now.grad_sumsq + sum;
+        // beside the table's loads; what adds them later would wait for the tile's
+        ListParts parts;
+        parts.load(part, tiles);
+        t.index = list_find(tile0, count, own);
+        t.set(entries, own, part_of);
+        mine = parts.lane_sum(tiles);
+    } else if constexpr (FRONT == kFrontNone) {
+        t.index = list_find(tile0, count, own);
+        t.set(entries, own, part_of);
     }
+    // the whole list's check: a tile per wave in turn, the first one's loads before the block's own
+    constexpr int kWaves = kListBlock / 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = static_cast<int>(__lane_id());
+    ListWaveCheck<FRONT == kFrontCheckSum> check;
+    if constexpr (list_checks(FRONT)) {
+        int other;
+        list_find2(tile0, count, own, wave < tiles ? wave : 0, t.index, other);
+        t.set(entries, own, part_of);
+        check.set(entries[other], wave < tiles ? wave : 0);
+        check.load(0);
+    }
+    t.load();
+    ListStep q = list_step(&now, hp);      // while the loads are on their way
+    if constexpr (FRONT == kFrontParts) {
+        mine = block_sum_fixed<kListBlock>(mine, lds, 0);
+        if (threadIdx.x == 0)
+            lds[kListBlock / 64] = mine;
+        __syncthreads();
+        now.grad_sumsq = now.grad_sumsq + lds[kListBlock / 64];
+    } else if constexpr (FRONT == kFrontNone) {
+        __syncthreads();
+    } else {
+        uint32_t bad = 0u;
+        static_assert(kStepCheck <= 64, "one lane per tile below");
+#pragma unroll 1
+        for (int tile = wave; tile < tiles; tile += kWaves) {
+            if (tile != wave) {
+                check.set(entries[list_find(tile0, count, tile)], tile);
+                check.load(0);
+            }
+            const double sum = check.finish(bad);
+            if (FRONT == kFrontCheckSum && lane == 0)
+                lds[tile] = sum;
+        }
+        now.overflow |= static_cast<uint32_t>(__syncthreads_or(static_cast<int>(bad)));
+        if constexpr (FRONT == kFrontCheckSum) {
+            double sum = lane < tiles ? lds[lane] : 0.0;
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1)
+                sum = sum + __shfl_xor(sum, off);
+            now.grad_sumsq = now.grad_sumsq + sum;
+        }
+    }
+    uint32_t before = 0u;
+    if (threadIdx.x == 0)                  // behind a barrier that every wave reached with the scaler read
+        before = list_ticket(st, tickets);
     if (now.overflow == 0u) {
-        ListStep q = list_step(&now, hp);
+        if constexpr (FRONT == kFrontParts || FRONT == kFrontCheckSum)
+            q.c.inv = make_consts(&now, hp.h).inv;   // by the norm
         t.finish(q);
     }
-    __syncthreads();   // every lane of this block has read the scaler state
     if (threadIdx.x == 0)
-        list_end_step(st, now, tickets);
+        list_end_step(st, now, tickets, before);
 }
 
 // ---- host side ----
@@ -1020,23 +1152,26 @@ ds_status list_check_args(const ds_scaler* st, const ds_tensor_list* l, const vo
     return DS_OK;
 }
 
+// The check's first kernel: the flag, and the partial sums where `part` is given.
+ds_status launch_list_check(ds_scaler* st, const ds_tensor_list* l, double* part, hipStream_t s)
+{
+    const unsigned blocks = grid_blocks(list_parts(l->tiles), kListBlock);
+    const unsigned char* table = static_cast<const unsigned char*>(l->table);
+    const int32_t tiles = static_cast<int32_t>(l->tiles);
+    if (part == nullptr) list_check_kernel<false><<<blocks, kListBlock, 0, s>>>(st, table, l->count, tiles, nullptr);
+    else                 list_check_kernel<true><<<blocks, kListBlock, 0, s>>>(st, table, l->count, tiles, part);
+    return launched();
+}
+
 ds_status list_check(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws_bytes, hipStream_t s)
 {
     if (const ds_status rc = list_check_args(st, l, ws, ws_bytes); rc != DS_OK)
         return rc;
     if (l->tiles == 0)
         return DS_OK;
-    const unsigned blocks = grid_blocks(list_parts(l->tiles), kListBlock);
-    const unsigned char* table = static_cast<const unsigned char*>(l->table);
-    const int32_t tiles = static_cast<int32_t>(l->tiles);
     double* part = static_cast<double*>(ws);
-    if (part == nullptr) {
-        list_check_kernel<false><<<blocks, kListBlock, 0, s>>>(st, table, l->count, tiles, nullptr);
-        return launched();
-    }
-    list_check_kernel<true><<<blocks, kListBlock, 0, s>>>(st, table, l->count, tiles, part);
-    if (launched() != DS_OK)
-        return DS_ERR_HIP;
+    if (const ds_status rc = launch_list_check(st, l, part, s); rc != DS_OK || part == nullptr)
+        return rc;
     return launch_finish(st, part, list_parts(l->tiles), s);
 }
 
@@ -1126,17 +1261,17 @@ ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, 
     return launched();
 }
 
-template <int FRONT>
+template <int FRONT, int U>
 void launch_list_step(hipStream_t s, ds_scaler* st, const ds_tensor_list* l, bool dither, const ListHyper& hp,
                       const double* part)
 {
     const unsigned char* table = static_cast<const unsigned char*>(l->table);
     uint32_t* tickets = static_cast<uint32_t*>(l->table);
     const int32_t tiles = static_cast<int32_t>(l->tiles), count = l->count;
-    const unsigned b = static_cast<unsigned>(tiles);
-    if (l->sdt == DS_FP32) list_step_kernel<false, false, FRONT><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
-    else if (dither)       list_step_kernel<true, true, FRONT><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
-    else                   list_step_kernel<true, false, FRONT><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
+    const unsigned b = static_cast<unsigned>(tiles * (kListQuads / U));
+    if (l->sdt == DS_FP32) list_step_kernel<false, false, FRONT, U><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
+    else if (dither)       list_step_kernel<true, true, FRONT, U><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
+    else                   list_step_kernel<true, false, FRONT, U><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
 }
 
 ds_status list_step_all(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws_bytes, const AdamHyper& h,
@@ -1147,7 +1282,7 @@ ds_status list_step_all(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t
     if (!list_hyper_ok(h, beta1, beta2, rounding))
         return DS_ERR_HPARAM;
     // a pinned grid (DSZERO_GRID) is for the kernels that loop over their tiles
-    if (l->tiles < 1 || l->tiles > (ws != nullptr ? kStepParts : kStepCheck) || env_long("DSZERO_GRID", 0) > 0) {
+    if (l->tiles < 1 || l->tiles > (ws != nullptr ? kStepParts : kStepQuarter) || env_long("DSZERO_GRID", 0) > 0) {
         if (const ds_status rc = list_check(st, l, ws, ws_bytes, s); rc != DS_OK)
             return rc;
         return list_adam(st, l, h, beta1, beta2, rounding, seed, true, s);
@@ -1159,16 +1294,18 @@ ds_status list_step_all(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t
     const bool dither = rounding == DS_ROUND_DITHER;
     double* part = static_cast<double*>(ws);
     if (alone && ws == nullptr) {
-        launch_list_step<kFrontCheck>(s, st, l, dither, hp, nullptr);
+        launch_list_step<kFrontCheck, 1>(s, st, l, dither, hp, nullptr);
     } else if (alone) {
-        launch_list_step<kFrontCheckSum>(s, st, l, dither, hp, nullptr);
+        launch_list_step<kFrontCheckSum, 1>(s, st, l, dither, hp, nullptr);
     } else {
-        const int32_t tiles = static_cast<int32_t>(l->tiles);
-        list_check_kernel<true><<<static_cast<unsigned>(list_parts(tiles)), kListBlock, 0, s>>>(
-            st, static_cast<const unsigned char*>(l->table), l->count, tiles, part);
-        if (launched() != DS_OK)
-            return DS_ERR_HIP;
-        launch_list_step<kFrontParts>(s, st, l, dither, hp, part);
+        if (const ds_status rc = launch_list_check(st, l, part, s); rc != DS_OK)
+            return rc;
+        if (part == nullptr)
+            launch_list_step<kFrontNone, 1>(s, st, l, dither, hp, nullptr);
+        else if (l->tiles <= kStepQuarter)
+            launch_list_step<kFrontParts, 1>(s, st, l, dither, hp, part);
+        else
+            launch_list_step<kFrontParts, kListQuads>(s, st, l, dither, hp, part);
     }
     return launched();
 }
