@@ -36,8 +36,9 @@ class ExpertBalance:
             self.used = torch.zeros((), dtype=torch.int32, device=device)
             # enough for any number of tokens (2.1 MB for 512 experts)
             need = _lib.ds_balance_workspace_bytes(1 << 30, self.E)
-            self._ws = torch.empty((need + 7) // 8, dtype=torch.float64, device=device)
+            self._ws = torch.zeros((need + 7) // 8, dtype=torch.float64, device=device)
         self._device = self.counts.device.index
+        self._mask_types = (torch.bool, torch.uint8)
         self._at = (self.counts.data_ptr(), self.mean_prob.data_ptr(), self.value.data_ptr(), self.used.data_ptr(),
                     self._ws.data_ptr(), self._ws.numel() * 8)
 
@@ -46,7 +47,7 @@ class ExpertBalance:
         shape = x.shape
         if len(shape) != 2 or shape[1] != self.E:
             raise ValueError(f"{what}: expected [tokens, {self.E}], got {tuple(shape)}")
-        if x.device != self.counts.device:
+        if not x.is_cuda or x.get_device() != self._device:
             raise ValueError(f"{what}: expected a tensor on {self.counts.device}, got one on {x.device}")
         T = shape[0]
         stride, inner = x.stride()
@@ -61,10 +62,9 @@ class ExpertBalance:
     def _mask(self, mask, tokens):
         if mask is None:
             return None
-        torch = self.torch
-        if mask.dtype not in (torch.bool, torch.uint8) or mask.dim() != 1 or mask.shape[0] != tokens:
+        if mask.dtype not in self._mask_types or mask.shape != (tokens,):
             raise ValueError(f"mask: expected {tokens} bool or uint8 values")
-        if mask.device != self.counts.device or not mask.is_contiguous():
+        if not mask.is_cuda or mask.get_device() != self._device or not mask.is_contiguous():
             raise ValueError(f"mask: expected a contiguous tensor on {self.counts.device}")
         return mask.data_ptr() if tokens else None
 

@@ -11,6 +11,7 @@
 constexpr int kBalBlock = 256;
 constexpr int kBalMaxBlocks = 1024;        // rows of partial sums: four blocks per CU
 constexpr int kBalFinishBlock = 1024, kBalFinishCols = 16;   // finishing kernel: lanes, experts per block
+constexpr unsigned kBalMeet = 128;
 constexpr int64_t kBalGradBlocks = 2048;   // gradient: eight blocks per CU
 constexpr int64_t kBalMaxTokens = int64_t(1) << 30;
 static_assert(DS_MAX_EXPERTS == 512 && DS_MAX_EXPERT_CHOICES == 16, "the instances below");
@@ -336,10 +337,74 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
         part = block_sum_fixed<kBalBlock>(part, lds_loss, 0);
         if (threadIdx.x == 0)
             bal_end(o, s.experts, rows, part);
-    } else if (threadIdx.x == 0) {
+        return;
+    }
+    if (threadIdx.x == 0)
         w.used[blockIdx.x] = rows;
-        if (blockIdx.x == 0)
-            *w.ticket = 0u;                // of the finishing kernel, which runs after this one
+    if constexpr (G * V <= 64) {
+        if (gridDim.x > kBalMeet)
+            return;
+        // the last block to come here ends the call
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            lds_used[0] = atomicAdd(w.ticket, 1u) == gridDim.x - 1u ? 1 : 0;
+        }
+        __syncthreads();
+        if (lds_used[0] == 0)
+            return;
+        __threadfence();
+        const int parts = static_cast<int>(gridDim.x), col = lane, e = col < s.experts ? col : 0;
+        int n = 0;
+        double p = 0.0;
+        for (int i0 = wave; i0 < parts; i0 += 16 * kWaves) {
+            int32_t c[16];
+            float q[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int i = i0 + u * kWaves < parts ? i0 + u * kWaves : 0;
+                c[u] = w.count[i * s.experts + e];
+                q[u] = w.prob[i * s.experts + e];
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const bool in = i0 + u * kWaves < parts;
+                n += in ? c[u] : 0;
+                p = p + static_cast<double>(in ? q[u] : 0.0f);
+            }
+        }
+        rows = 0;
+        for (int i = threadIdx.x; i < parts; i += kBalBlock)
+            rows += w.used[i];
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            rows += __shfl_xor(rows, off);
+        __shared__ double sum[kWaves][64];
+        __shared__ int32_t count[kWaves][64], some[kWaves];
+        sum[wave][col] = p;
+        count[wave][col] = n;
+        if (lane == 0)
+            some[wave] = rows;
+        __syncthreads();
+        if (wave != 0)
+            return;
+        rows = 0;
+        n = 0;
+        p = 0.0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            rows += some[i];
+            n += count[i][col];
+            p = p + sum[i][col];
+        }
+        part = col < s.experts ? bal_expert(o, s.k, rows, col, n, p) : 0.0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            part = part + __shfl_xor(part, off);
+        if (lane == 0) {
+            bal_end(o, s.experts, rows, part);
+            *w.ticket = 0u;
+        }
     }
 }
 
@@ -420,6 +485,8 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
         }
         if (__builtin_amdgcn_readfirstlane(before) != gridDim.x - 1u)
             return;
+        if (lane == 0)
+            *w.ticket = 0u;
         __threadfence();
         part = lane < static_cast<int>(gridDim.x) ? __builtin_nontemporal_load(w.loss + lane) : 0.0;
 #pragma unroll
@@ -657,7 +724,7 @@ ds_status balance_loss(const void* logits, ds_dtype dt, int64_t tokens, int32_t 
     else                    launch_balance2<kF32>(blocks, s, logits, shape, mask, w, o);
     if (launched() != DS_OK)
         return DS_ERR_HIP;
-    if (blocks == 1)
+    if (blocks == 1 || (experts <= 64 && blocks <= kBalMeet))
         return DS_OK;
     const int32_t parts = static_cast<int32_t>(blocks);
     if (experts <= 64) {

@@ -354,6 +354,19 @@ __device__ __forceinline__ void list_tensor_consts(const ListEntry& e, ListStep&
     q.c.lrwd = lr * e.weight_decay;
 }
 
+// The constants in scalar registers (they are the same in every lane, which
+// the compiler cannot know of a value that it formed in vector registers).
+__device__ __forceinline__ float list_scalar(float x)
+{
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+
+__device__ __forceinline__ AdamConsts list_scalars(const AdamConsts& c)
+{
+    return AdamConsts{list_scalar(c.inv),  c.b1, c.b2, list_scalar(c.omb1), list_scalar(c.omb2), list_scalar(c.lrwd),
+                      list_scalar(c.step_size), list_scalar(c.rbc2), c.eps};
+}
+
 __device__ __forceinline__ void list_update(const f32x4& g, f32x4& p, f32x4& m, f32x4& v, bool wd, const AdamConsts& c)
 {
     if (wd)
@@ -441,6 +454,13 @@ __device__ __forceinline__ int64_t list_block(int64_t base, int u)
     return base / DS_STATE_BLOCK + u * (kListBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 }
 
+// A state's scale, uniform over the wave, by a scalar load.  The wave that reads
+// it is the one that writes it, afterwards.
+__device__ __forceinline__ float list_scale(const float* p)
+{
+    return *(const __attribute__((address_space(4))) float*)p;
+}
+
 // Loads of U quads per lane, into the first U, from element `base` on.  FULL: whole and aligned,
 // vectors of four throughout.  Else a vector where the tensor is aligned and
 // the quad whole, single elements otherwise, zeros past the end (so that a
@@ -455,8 +475,8 @@ __device__ __forceinline__ void list_load(const ListEntry& e, int64_t base, List
         if constexpr (E8) {
             const int64_t blk = list_block(base, u);
             const bool in = FULL || blk * DS_STATE_BLOCK < e.n;
-            r.m_scale[u] = in ? gload(e.m_scale + blk) : 0.0f;
-            r.v_scale[u] = in ? gload(e.v_scale + blk) : 0.0f;
+            r.m_scale[u] = in ? list_scale(e.m_scale + blk) : 0.0f;
+            r.v_scale[u] = in ? list_scale(e.v_scale + blk) : 0.0f;
         }
         if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
             r.p[u] = gload<NT>(reinterpret_cast<const f32x4*>(e.master) + q);
@@ -537,6 +557,7 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
                                             uint32_t key)
 {
     const int64_t q0 = base / 4 + threadIdx.x;
+    float scale_m = 0.0f, scale_v = 0.0f;
     f32x4 g[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -572,9 +593,16 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
             float sm, sv;
             list_encode<DITHER>(m, v, DITHER ? dither_mix(key + static_cast<uint32_t>(blk) * kGold) : 0u, sm, sv, cm,
                                 cv);
-            if (__lane_id() == 0u) {
-                gstore(e.m_scale + blk, sm);
-                gstore(e.v_scale + blk, sv);
+            if (__lane_id() == static_cast<unsigned>(u)) {
+                scale_m = sm;
+                scale_v = sv;
+            }
+            if (u == U - 1) {                      // the wave's scales together, one a lane
+                const int64_t mine = list_block(base, 0) + __lane_id() * (kListBlock / 64);
+                if (__lane_id() < U) {
+                    gstore(e.m_scale + mine, scale_m);
+                    gstore(e.v_scale + mine, scale_v);
+                }
             }
         }
         if (FULL || (e.vec && 4 * q + 4 <= e.n)) {
@@ -646,20 +674,21 @@ struct ListTile {
     __device__ __forceinline__ void finish(ListStep& q)
     {
         list_tensor_consts(e, q);
+        const AdamConsts c = list_scalars(q.c);
         const uint32_t key = DITHER ? dither_mix(q.key + static_cast<uint32_t>(index) * kGold) : 0u;
         if constexpr (U == 1) {
-            list_finish<E8, DITHER, false, false, 1>(e, base, r, q.c, key);
+            list_finish<E8, DITHER, false, false, 1>(e, base, r, c, key);
             return;
         }
         if (full) {
-            list_finish<E8, DITHER, NT, true, U>(e, base, r, q.c, key);
+            list_finish<E8, DITHER, NT, true, U>(e, base, r, c, key);
             return;
         }
         const int64_t end = e.n - base < kListTile ? e.n : base + kListTile;
 #pragma unroll 1
         for (int64_t at = base; at < end; at += 4 * kListBlock) {
             list_load<E8, false, false, 1>(e, at, r);
-            list_finish<E8, DITHER, false, false, 1>(e, at, r, q.c, key);
+            list_finish<E8, DITHER, false, false, 1>(e, at, r, c, key);
         }
     }
 };
@@ -722,9 +751,9 @@ __device__ __forceinline__ void list_end_step(ds_scaler* st, const ds_scaler& no
     st->blocks_done = 0u;
 }
 
-// One tile per block and loop turn.  The step's constants (fp64 powers and
-// divisions) are formed while the first tile's loads are on their way.
-template <bool E8, bool DITHER, bool NT, bool FUSE>
+// A tile per block and loop turn: for a pinned grid (DSZERO_GRID), and past the
+// largest one.
+template <bool E8, bool DITHER, bool FUSE>
 __global__ __launch_bounds__(kListBlock, 4) void list_adam_kernel(ds_scaler* __restrict__ st,
                                                                const unsigned char* __restrict__ table,
                                                                uint32_t* __restrict__ tickets, int32_t count,
@@ -740,16 +769,12 @@ __global__ __launch_bounds__(kListBlock, 4) void list_adam_kernel(ds_scaler* __r
             before = list_ticket(st, tickets);
     }
     if (now.overflow == 0u) {
-        ListStep q;
-        bool first = true;
+        ListStep q = list_step(&now, hp);
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            ListTile<E8, DITHER, NT, kListQuads> t;
+            ListTile<E8, DITHER, false, kListQuads> t;
             t.index = list_find(tile0, count, tile);
             t.set(entries, tile, 0);
             t.load();
-            if (first)
-                q = list_step(&now, hp);
-            first = false;
             t.finish(q);
         }
     }
@@ -758,7 +783,7 @@ __global__ __launch_bounds__(kListBlock, 4) void list_adam_kernel(ds_scaler* __r
             list_end_step(st, now, tickets, before);
 }
 
-// ---- a whole step over a short list ----
+// ---- a block per tile; a whole step over a short list ----
 
 // Up to kStepParts tiles every block adds the check's partial sums itself,
 // instead of a kernel between the check and the update (363 tiles: 14.0 us a
@@ -900,23 +925,31 @@ struct ListWaveCheck {
     }
 };
 
-// A block per tile, or four: the step's end (and with kFrontCheck and
-// kFrontCheckSum its check) in one kernel.  The gradients are only read, so
-// the blocks need not meet: each comes to the same flag and sum.
-template <bool E8, bool DITHER, int FRONT, int U>
-__global__ __launch_bounds__(kListBlock, list_checks(FRONT) ? 2 : 4) void list_step_kernel(ds_scaler* __restrict__ st,
-                                                               const unsigned char* __restrict__ table,
-                                                               uint32_t* __restrict__ tickets, int32_t count,
-                                                               int32_t tiles, ListHyper hp,
-                                                               const double* __restrict__ part)
+// A block per tile, or four: the update, with FUSE the step's end, and with
+// kFrontCheck and kFrontCheckSum its check.  The gradients are only read, so
+// the blocks need not meet: each comes to the same flag and sum.  The step's
+// constants (fp64 powers and divisions) are formed while the loads are on
+// their way.
+template <bool E8, bool DITHER, bool NT, bool FUSE, int FRONT, int U>
+__global__ __launch_bounds__(kListBlock, list_checks(FRONT) ? 2 : 4) void list_step_kernel(
+    ds_scaler* __restrict__ st, const unsigned char* __restrict__ table, uint32_t* __restrict__ tickets, int32_t count,
+    int32_t tiles, ListHyper hp, const double* __restrict__ part)
 {
     __shared__ double lds[FRONT == kFrontParts ? kListBlock / 64 + 1 : kStepCheck];
     const int32_t* tile0 = reinterpret_cast<const int32_t*>(table + kTile0At);
     const ListEntry* entries = reinterpret_cast<const ListEntry*>(table + list_entries_at(count));
     ds_scaler now = list_scaler(st);
+    if constexpr (FRONT == kFrontNone) {
+        if (now.overflow != 0u) {              // nothing to update
+            __syncthreads();
+            if (FUSE && threadIdx.x == 0)
+                list_end_step(st, now, tickets, list_ticket(st, tickets));
+            return;
+        }
+    }
     constexpr int kSplit = kListQuads / U;
     const int own = blockIdx.x / kSplit, part_of = blockIdx.x % kSplit;
-    ListTile<E8, DITHER, false, U> t;
+    ListTile<E8, DITHER, NT, U> t;
     double mine = 0.0;
     if constexpr (FRONT == kFrontParts) {
         // beside the table's loads; what adds them later would wait for the tile's
@@ -949,7 +982,8 @@ __global__ __launch_bounds__(kListBlock, list_checks(FRONT) ? 2 : 4) void list_s
         __syncthreads();
         now.grad_sumsq = now.grad_sumsq + lds[kListBlock / 64];
     } else if constexpr (FRONT == kFrontNone) {
-        __syncthreads();
+        if constexpr (FUSE)
+            __syncthreads();
     } else {
         uint32_t bad = 0u;
         static_assert(kStepCheck <= 64, "one lane per tile below");
@@ -973,14 +1007,14 @@ __global__ __launch_bounds__(kListBlock, list_checks(FRONT) ? 2 : 4) void list_s
         }
     }
     uint32_t before = 0u;
-    if (threadIdx.x == 0)                  // behind a barrier that every wave reached with the scaler read
+    if (FUSE && threadIdx.x == 0)          // behind a barrier that every wave reached with the scaler read
         before = list_ticket(st, tickets);
     if (now.overflow == 0u) {
         if constexpr (FRONT == kFrontParts || FRONT == kFrontCheckSum)
             q.c.inv = make_consts(&now, hp.h).inv;   // by the norm
         t.finish(q);
     }
-    if (threadIdx.x == 0)
+    if (FUSE && threadIdx.x == 0)
         list_end_step(st, now, tickets, before);
 }
 
@@ -1175,23 +1209,41 @@ ds_status list_check(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws
     return launch_finish(st, part, list_parts(l->tiles), s);
 }
 
-template <bool E8, bool DITHER, bool NT>
-void launch_list_adam2(bool fuse, unsigned blocks, hipStream_t s, ds_scaler* st, const ds_tensor_list* l,
-                       const ListHyper& hp)
+// What the kernels of one step take.
+struct ListLaunch {
+    ds_scaler* st;
+    const ds_tensor_list* l;
+    ListHyper hp;
+    const double* part;
+    hipStream_t s;
+};
+
+template <bool E8, bool DITHER, bool NT, bool FUSE, int FRONT, int U>
+void launch_list_step2(const ListLaunch& a)
 {
-    const unsigned char* table = static_cast<const unsigned char*>(l->table);
-    uint32_t* tickets = static_cast<uint32_t*>(l->table);
-    const int32_t tiles = static_cast<int32_t>(l->tiles), count = l->count;
-    if (fuse) list_adam_kernel<E8, DITHER, NT, true><<<blocks, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp);
-    else      list_adam_kernel<E8, DITHER, NT, false><<<blocks, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp);
+    const unsigned char* table = static_cast<const unsigned char*>(a.l->table);
+    uint32_t* tickets = static_cast<uint32_t*>(a.l->table);
+    const int32_t tiles = static_cast<int32_t>(a.l->tiles), count = a.l->count;
+    const unsigned b = static_cast<unsigned>(tiles) * (kListQuads / U);
+    list_step_kernel<E8, DITHER, NT, FUSE, FRONT, U><<<b, kListBlock, 0, a.s>>>(a.st, table, tickets, count, tiles, a.hp, a.part);
+}
+
+template <bool NT, bool FUSE, int FRONT, int U>
+void launch_list_step(const ListLaunch& a, bool dither)
+{
+    if (a.l->sdt == DS_FP32) launch_list_step2<false, false, NT, FUSE, FRONT, U>(a);
+    else if (dither)         launch_list_step2<true, true, NT, FUSE, FRONT, U>(a);
+    else                     launch_list_step2<true, false, NT, FUSE, FRONT, U>(a);
 }
 
 template <bool E8, bool DITHER>
-void launch_list_adam(bool nt, bool fuse, unsigned blocks, hipStream_t s, ds_scaler* st, const ds_tensor_list* l,
-                      const ListHyper& hp)
+void launch_list_adam(const ListLaunch& a, bool fuse, unsigned blocks)
 {
-    if (nt) launch_list_adam2<E8, DITHER, true>(fuse, blocks, s, st, l, hp);
-    else    launch_list_adam2<E8, DITHER, false>(fuse, blocks, s, st, l, hp);
+    const unsigned char* table = static_cast<const unsigned char*>(a.l->table);
+    uint32_t* tickets = static_cast<uint32_t*>(a.l->table);
+    const int32_t tiles = static_cast<int32_t>(a.l->tiles), count = a.l->count;
+    if (fuse) list_adam_kernel<E8, DITHER, true><<<blocks, kListBlock, 0, a.s>>>(a.st, table, tickets, count, tiles, a.hp);
+    else      list_adam_kernel<E8, DITHER, false><<<blocks, kListBlock, 0, a.s>>>(a.st, table, tickets, count, tiles, a.hp);
 }
 
 // The kernels' hyperparameters from a call's; false: a schedule that is not one.
@@ -1243,35 +1295,27 @@ ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, 
     }
     if (overlap(st, sizeof(ds_scaler), l->table, list_bytes(l->count)))
         return DS_ERR_ALIAS;
-    const ListHyper hp = list_hyper(h, beta1, beta2, seed);
-    const bool nt = variant_nt(l->elems);
+    const ListLaunch a{st, l, list_hyper(h, beta1, beta2, seed), nullptr, s};
     const unsigned blocks = grid_blocks(l->tiles, kListBlock);
-    const bool e8 = l->sdt != DS_FP32, fuse = end_step && (!e8 || blocks <= kFuseBlocks);
-    if (!e8)
-        launch_list_adam<false, false>(nt, fuse, blocks, s, st, l, hp);
-    else if (rounding == DS_ROUND_DITHER)
-        launch_list_adam<true, true>(nt, fuse, blocks, s, st, l, hp);
-    else
-        launch_list_adam<true, false>(nt, fuse, blocks, s, st, l, hp);
+    const bool e8 = l->sdt != DS_FP32, dither = rounding == DS_ROUND_DITHER;
+    const bool fuse = end_step && (!e8 || blocks <= kFuseBlocks);
+    if (blocks != l->tiles) {
+        if (!e8)         launch_list_adam<false, false>(a, fuse, blocks);
+        else if (dither) launch_list_adam<true, true>(a, fuse, blocks);
+        else             launch_list_adam<true, false>(a, fuse, blocks);
+    } else if (variant_nt(l->elems)) {
+        if (fuse) launch_list_step<true, true, kFrontNone, kListQuads>(a, dither);
+        else      launch_list_step<true, false, kFrontNone, kListQuads>(a, dither);
+    } else {
+        if (fuse) launch_list_step<false, true, kFrontNone, kListQuads>(a, dither);
+        else      launch_list_step<false, false, kFrontNone, kListQuads>(a, dither);
+    }
     if (end_step && !fuse) {
         if (launched() != DS_OK)
             return DS_ERR_HIP;
         update_scale_kernel<<<1, 1, 0, s>>>(st);
     }
     return launched();
-}
-
-template <int FRONT, int U>
-void launch_list_step(hipStream_t s, ds_scaler* st, const ds_tensor_list* l, bool dither, const ListHyper& hp,
-                      const double* part)
-{
-    const unsigned char* table = static_cast<const unsigned char*>(l->table);
-    uint32_t* tickets = static_cast<uint32_t*>(l->table);
-    const int32_t tiles = static_cast<int32_t>(l->tiles), count = l->count;
-    const unsigned b = static_cast<unsigned>(tiles * (kListQuads / U));
-    if (l->sdt == DS_FP32) list_step_kernel<false, false, FRONT, U><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
-    else if (dither)       list_step_kernel<true, true, FRONT, U><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
-    else                   list_step_kernel<true, false, FRONT, U><<<b, kListBlock, 0, s>>>(st, table, tickets, count, tiles, hp, part);
 }
 
 ds_status list_step_all(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t ws_bytes, const AdamHyper& h,
@@ -1288,24 +1332,19 @@ ds_status list_step_all(ds_scaler* st, const ds_tensor_list* l, void* ws, size_t
         return list_adam(st, l, h, beta1, beta2, rounding, seed, true, s);
     }
     const bool alone = l->tiles <= kStepCheck;
-    const ListHyper hp = list_hyper(h, beta1, beta2, seed);
     if (const ds_status rc = list_check_args(st, l, ws, ws_bytes); rc != DS_OK)
         return rc;
     const bool dither = rounding == DS_ROUND_DITHER;
-    double* part = static_cast<double*>(ws);
-    if (alone && ws == nullptr) {
-        launch_list_step<kFrontCheck, 1>(s, st, l, dither, hp, nullptr);
-    } else if (alone) {
-        launch_list_step<kFrontCheckSum, 1>(s, st, l, dither, hp, nullptr);
-    } else {
-        if (const ds_status rc = launch_list_check(st, l, part, s); rc != DS_OK)
-            return rc;
-        if (part == nullptr)
-            launch_list_step<kFrontNone, 1>(s, st, l, dither, hp, nullptr);
-        else if (l->tiles <= kStepQuarter)
-            launch_list_step<kFrontParts, 1>(s, st, l, dither, hp, part);
-        else
-            launch_list_step<kFrontParts, kListQuads>(s, st, l, dither, hp, part);
+    const ListLaunch a{st, l, list_hyper(h, beta1, beta2, seed), static_cast<double*>(ws), s};
+    if (alone) {
+        if (ws == nullptr) launch_list_step<false, true, kFrontCheck, 1>(a, dither);
+        else               launch_list_step<false, true, kFrontCheckSum, 1>(a, dither);
+        return launched();
     }
+    if (const ds_status rc = launch_list_check(st, l, static_cast<double*>(ws), s); rc != DS_OK)
+        return rc;
+    if (ws == nullptr)                     launch_list_step<false, true, kFrontNone, 1>(a, dither);
+    else if (l->tiles <= kStepQuarter)     launch_list_step<false, true, kFrontParts, 1>(a, dither);
+    else                                   launch_list_step<false, true, kFrontParts, kListQuads>(a, dither);
     return launched();
 }
