@@ -661,8 +661,10 @@ size_t ds_balance_workspace_bytes(int64_t tokens, int32_t experts);
 
 /*
  * counts: int32[experts], mean_prob: fp32[experts], loss: fp32[1], used:
- * int32[1], all device, all written.  workspace: device, 8-byte aligned, no
- * initial contents.  tokens may be 0 (logits may be NULL then).
+ * int32[1], all device, all written.  workspace: device, 8-byte aligned,
+ * cleared to zero once before its first call (it holds a count of finished
+ * blocks that every call leaves at zero; later calls may have other sizes, but
+ * not run at the same time).  tokens may be 0 (logits may be NULL then).
  * Errors: tokens outside [0, 2^30], experts outside 1..512, k outside
  * 1..min(experts, 16), row_stride < experts, a short workspace -> DS_ERR_SIZE;
  * coef not finite or negative -> DS_ERR_HPARAM; else as in the conventions

@@ -34,7 +34,7 @@ class ExpertBalance:
             self.mean_prob = torch.zeros(self.E, dtype=torch.float32, device=device)
             self.value = torch.zeros((), dtype=torch.float32, device=device)
             self.used = torch.zeros((), dtype=torch.int32, device=device)
-            # enough for any number of tokens (2.1 MB for 512 experts)
+            # enough for any number of tokens (2.1 MB for 512 experts); its count of finished blocks starts at zero
             need = _lib.ds_balance_workspace_bytes(1 << 30, self.E)
             self._ws = torch.zeros((need + 7) // 8, dtype=torch.float64, device=device)
         self._device = self.counts.device.index

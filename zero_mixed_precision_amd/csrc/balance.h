@@ -11,7 +11,12 @@
 constexpr int kBalBlock = 256;
 constexpr int kBalMaxBlocks = 1024;        // rows of partial sums: four blocks per CU
 constexpr int kBalFinishBlock = 1024, kBalFinishCols = 16;   // finishing kernel: lanes, experts per block
-constexpr unsigned kBalMeet = 128;
+// Up to so many blocks (and 64 experts) the last block of the forward kernel
+// ends the call, instead of a second kernel: with the gradient 64 x 64 takes
+// 10.4 us and 4096 x 64 13.6 (128 blocks; 15.2 with the second kernel).  A
+// block's ticket and fence cost more as they become many (313 blocks: 19.5 us,
+// 15.1 with the second kernel).
+constexpr int64_t kBalMeet = 128;
 constexpr int64_t kBalGradBlocks = 2048;   // gradient: eight blocks per CU
 constexpr int64_t kBalMaxTokens = int64_t(1) << 30;
 static_assert(DS_MAX_EXPERTS == 512 && DS_MAX_EXPERT_CHOICES == 16, "the instances below");
@@ -200,7 +205,7 @@ __device__ __forceinline__ void bal_end(const BalOut& o, int32_t experts, int ro
 
 // Forward: counts and probability sums of this block's rows into row
 // blockIdx.x of the partial arrays, used rows into used[blockIdx.x].  A grid
-// of one block ends the call itself.
+// of one block ends the call itself, and of up to kBalMeet the last block.
 template <int GF, int G, int V, int KK>
 __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restrict__ logits, BalShape s,
                                                             const uint8_t* __restrict__ mask, BalWork w, BalOut o)

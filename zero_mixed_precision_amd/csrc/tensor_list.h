@@ -18,13 +18,13 @@ constexpr int kCheckTiles = 4;
 constexpr int32_t kCheckFew = 2048;                // tiles: up to here one by one
 // Tickets of the blocks of one step: taken from one address they cost about
 // 13 ns each, one after another (2.5 ms for four layers' 197,636 blocks, more
-// than the 8-bit step itself), so block b takes one from counter b % 64, each
-// counter on a line of its own, and the last of each from the scaler's.
+// than the 8-bit step itself), so block b takes one from counter b % 64 (of 16
+// up to 1024 blocks), each counter on a line of its own, and the last of each
+// from the scaler's.  Taken before the update they cost it little even where a
+// block's time is short (8-bit states, one layer: 570 us a step, 576 with a
+// kernel of its own that advances the scaler; taken at the end they made the
+// update alone 561 us instead of 522).
 constexpr unsigned kTicketLines = 64, kTicketBytes = 128;
-// With 8-bit states a block's short time is the longer for its ticket: past
-// this many blocks the scaler is advanced by a kernel of its own (one layer:
-// 522 + 2 us, 561 us with tickets; with 32-bit states 936 + 2 and 934 us).
-constexpr unsigned kFuseBlocks = 4096;
 constexpr int32_t kMaxTensors = 1 << 20;
 
 // One tensor in the device table.
@@ -1237,13 +1237,13 @@ void launch_list_step(const ListLaunch& a, bool dither)
 }
 
 template <bool E8, bool DITHER>
-void launch_list_adam(const ListLaunch& a, bool fuse, unsigned blocks)
+void launch_list_adam(const ListLaunch& a, bool end_step, unsigned blocks)
 {
     const unsigned char* table = static_cast<const unsigned char*>(a.l->table);
     uint32_t* tickets = static_cast<uint32_t*>(a.l->table);
     const int32_t tiles = static_cast<int32_t>(a.l->tiles), count = a.l->count;
-    if (fuse) list_adam_kernel<E8, DITHER, true><<<blocks, kListBlock, 0, a.s>>>(a.st, table, tickets, count, tiles, a.hp);
-    else      list_adam_kernel<E8, DITHER, false><<<blocks, kListBlock, 0, a.s>>>(a.st, table, tickets, count, tiles, a.hp);
+    if (end_step) list_adam_kernel<E8, DITHER, true><<<blocks, kListBlock, 0, a.s>>>(a.st, table, tickets, count, tiles, a.hp);
+    else          list_adam_kernel<E8, DITHER, false><<<blocks, kListBlock, 0, a.s>>>(a.st, table, tickets, count, tiles, a.hp);
 }
 
 // The kernels' hyperparameters from a call's; false: a schedule that is not one.
@@ -1298,22 +1298,16 @@ ds_status list_adam(ds_scaler* st, const ds_tensor_list* l, const AdamHyper& h, 
     const ListLaunch a{st, l, list_hyper(h, beta1, beta2, seed), nullptr, s};
     const unsigned blocks = grid_blocks(l->tiles, kListBlock);
     const bool e8 = l->sdt != DS_FP32, dither = rounding == DS_ROUND_DITHER;
-    const bool fuse = end_step && (!e8 || blocks <= kFuseBlocks);
     if (blocks != l->tiles) {
-        if (!e8)         launch_list_adam<false, false>(a, fuse, blocks);
-        else if (dither) launch_list_adam<true, true>(a, fuse, blocks);
-        else             launch_list_adam<true, false>(a, fuse, blocks);
+        if (!e8)         launch_list_adam<false, false>(a, end_step, blocks);
+        else if (dither) launch_list_adam<true, true>(a, end_step, blocks);
+        else             launch_list_adam<true, false>(a, end_step, blocks);
     } else if (variant_nt(l->elems)) {
-        if (fuse) launch_list_step<true, true, kFrontNone, kListQuads>(a, dither);
-        else      launch_list_step<true, false, kFrontNone, kListQuads>(a, dither);
+        if (end_step) launch_list_step<true, true, kFrontNone, kListQuads>(a, dither);
+        else          launch_list_step<true, false, kFrontNone, kListQuads>(a, dither);
     } else {
-        if (fuse) launch_list_step<false, true, kFrontNone, kListQuads>(a, dither);
-        else      launch_list_step<false, false, kFrontNone, kListQuads>(a, dither);
-    }
-    if (end_step && !fuse) {
-        if (launched() != DS_OK)
-            return DS_ERR_HIP;
-        update_scale_kernel<<<1, 1, 0, s>>>(st);
+        if (end_step) launch_list_step<false, true, kFrontNone, kListQuads>(a, dither);
+        else          launch_list_step<false, false, kFrontNone, kListQuads>(a, dither);
     }
     return launched();
 }
