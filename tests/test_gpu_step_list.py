@@ -120,8 +120,7 @@ def test_steps_that_share_a_scaler_clip_by_one_norm():
         for half in (first, second):
             half.update()
     torch.cuda.synchronize()
-    # the sums are fp64 of the same squares in another order: a factor that differs by 1e-12 at most, fp32 results by
-    # a rounding of it
+    # fp64 sums of the same squares in another order: below 1e-12 apart, which no rounding to fp32 and bf16 here shows
     a, b = whole.scaler().last_grad_sumsq, first.scaler().last_grad_sumsq
     assert abs(a - b) <= 1e-12 * a and a > 0.01
     for p, q in zip(whole.params, params):
@@ -157,3 +156,26 @@ def test_a_scaler_elsewhere_is_refused():
     for call in (op.step, op.check, op.update):
         with pytest.raises(RuntimeError, match="set_gradients"):
             call()
+
+
+def test_replaced_gradients_are_not_reused_while_a_step_reads_them():
+    """A gradient that set_gradients() has replaced goes back to torch's pool; on a stream of its own a step may still be
+    to read it, so its memory must not come back before."""
+    side = torch.cuda.Stream()
+    n = 3_000_017
+    op, grads = build([n], "bf16", "bf16", "fp32", 0.0, 0, stream=side)
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    new = torch.ones_like(grads[0])
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)           # about a tenth of a second
+    op.step()
+    op.set_gradients([new])
+    old = grads.pop()
+    at = old.data_ptr()
+    del old
+    again = torch.empty(n, dtype=torch.bfloat16, device=DEV)
+    assert not side.query(), "the stream was to be busy here"
+    assert again.data_ptr() != at
+    torch.cuda.synchronize()
+    assert op.scaler().step == 1

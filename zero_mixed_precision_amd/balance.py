@@ -43,25 +43,27 @@ class ExpertBalance:
                     self._ws.data_ptr(), self._ws.numel() * 8)
 
     def _rows(self, x, what):
-        """(address, row stride) of a [tokens, experts] matrix."""
+        """(type, address, tokens, row stride) of a [tokens, experts] matrix.  A small call's time is the host's, half of
+        it spent here and in marshalling: each property of a tensor is asked for once."""
+        dt = _dtype_of(x, self.torch, what)
         shape = x.shape
         if len(shape) != 2 or shape[1] != self.E:
             raise ValueError(f"{what}: expected [tokens, {self.E}], got {tuple(shape)}")
         if not x.is_cuda or x.get_device() != self._device:
             raise ValueError(f"{what}: expected a tensor on {self.counts.device}, got one on {x.device}")
         T = shape[0]
+        if T == 0:
+            return dt, None, 0, self.E
         stride, inner = x.stride()
-        if inner != 1 and self.E > 1 and T > 0:
+        if inner != 1 and self.E > 1:
             raise ValueError(f"{what}: the experts of a row must be adjacent")
-        if T <= 1:
+        if T == 1:
             stride = self.E
         elif stride < self.E:
             raise ValueError(f"{what}: rows overlap")
-        return (x.data_ptr() if T else None), stride
+        return dt, x.data_ptr(), T, stride
 
     def _mask(self, mask, tokens):
-        if mask is None:
-            return None
         if mask.dtype not in self._mask_types or mask.shape != (tokens,):
             raise ValueError(f"mask: expected {tokens} bool or uint8 values")
         if not mask.is_cuda or mask.get_device() != self._device or not mask.is_contiguous():
@@ -71,24 +73,26 @@ class ExpertBalance:
     def loss(self, logits, mask=None):
         """Counts and loss of ``logits`` (fp16, bf16 or fp32 [tokens, experts], rows any distance apart); ``mask``:
         bool or uint8 per token, 0 leaves it out.  Returns ``value``."""
-        dt = _dtype_of(logits, self.torch, "logits")
-        z, stride = self._rows(logits, "logits")
-        T = logits.shape[0]
+        dt, z, T, stride = self._rows(logits, "logits")
         counts, mean, value, used, ws, ws_bytes = self._at
-        _lib._ok(_lib.lib.ds_balance_loss(z, dt, T, self.E, stride, self._mask(mask, T), self.k, self.coef, counts, mean,
-                                          value, used, ws, ws_bytes, _lib._stream_on(self.stream, self._device)), "ds_balance_loss")
+        rc = _lib.lib.ds_balance_loss(z, dt, T, self.E, stride, None if mask is None else self._mask(mask, T), self.k,
+                                      self.coef, counts, mean, value, used, ws, ws_bytes,
+                                      _lib._stream_on(self.stream, self._device))
+        if rc:
+            _lib._ok(rc, "ds_balance_loss")
         return self.value
 
     def gradient(self, logits, out, mask=None, scaler=None, accumulate=False):
         """The gradient by ``logits`` of the loss() just taken of them, into ``out`` (their type and shape), times the
         scale of ``scaler`` (a ds_scaler state on the device; None: 1).  accumulate: add to ``out``."""
-        if out.dtype != logits.dtype or out.shape != logits.shape:
+        dt, z, T, stride = self._rows(logits, "logits")
+        of, d, rows, gstride = self._rows(out, "out")
+        if of != dt or rows != T:
             raise ValueError("out: expected the logits' type and shape")
-        dt = _dtype_of(logits, self.torch, "logits")
-        z, stride = self._rows(logits, "logits")
-        d, gstride = self._rows(out, "out")
-        T = logits.shape[0]
-        _lib._ok(_lib.lib.ds_balance_loss_grad(_lib._scaler(scaler), z, dt, T, self.E, stride, self._mask(mask, T),
-                                               self.k, self.coef, self._at[0], self._at[3], d, gstride, accumulate,
-                                               _lib._stream_on(self.stream, self._device)), "ds_balance_loss_grad")
+        rc = _lib.lib.ds_balance_loss_grad(None if scaler is None else _lib._scaler(scaler), z, dt, T, self.E, stride,
+                                           None if mask is None else self._mask(mask, T), self.k, self.coef,
+                                           self._at[0], self._at[3], d, gstride, accumulate,
+                                           _lib._stream_on(self.stream, self._device))
+        if rc:
+            _lib._ok(rc, "ds_balance_loss_grad")
         return out

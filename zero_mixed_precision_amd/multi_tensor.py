@@ -160,7 +160,8 @@ class MultiTensorStep:
 
     def set_gradients(self, grads) -> None:
         """The gradient tensors of the following steps, one per parameter (16-bit in the configuration's format, or
-        fp32).  They are read where they lie, so they stay allocated; call it again when one has moved."""
+        fp32).  They are read where they lie, so they stay allocated; call it again when one has moved.  On a stream of
+        its own the step is ordered after what writes them by the caller."""
         torch = self.torch
         grads = list(grads)
         if len(grads) != len(self.params):
@@ -177,6 +178,10 @@ class MultiTensorStep:
         tensors = self._tensors if grads else []
         self._list = _lib.ds_tensor_list_write(self._table, tensors, self._sdt, self.stream)
         self._list_at = ctypes.byref(self._list)
+        if self.stream is not None:              # not handed out again while steps on that stream still read them
+            there = self._torch_stream()
+            for g in grads:
+                g.record_stream(there)
         self._grads = grads
 
     def step(self) -> None:
