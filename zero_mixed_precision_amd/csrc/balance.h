@@ -7,6 +7,13 @@
 // maximum and sum and the k largest are reductions over G lanes, and since a
 // lane meets the same experts in every row, the counts and the probability
 // sums stay in its registers until the block has done all its rows.
+//
+// 131072 x 256 in bf16, the 8 largest: forward 40.6 us, bound by vector
+// instructions (95 % of the busy cycles; about a third of them keep and merge the
+// lists of the largest), the sums of its partial rows 9.0 us, bound by the
+// latency of reading them, gradient 29.5 us (134 MB, 4.6 TB/s).  Loads that do
+// not wait for the mask, or 512 blocks instead of 1024, made the forward
+// kernel 44 and 45 us.
 
 constexpr int kBalBlock = 256;
 constexpr int kBalMaxBlocks = 1024;        // rows of partial sums: four blocks per CU
