@@ -930,11 +930,11 @@ struct ListWaveCheck {
 // the blocks need not meet: each comes to the same flag and sum.  The step's
 // constants (fp64 powers and divisions) are formed while the loads are on
 // their way.  One layer of 202,383,360 parameters in bf16: 937 us with 32-bit
-// states (6.05 TB/s of 28 bytes an element), which memory bounds, and 511 us
-// with 8-bit ones (5.57 TB/s of 14.06), where memory and the vector units are
-// busy alike (78 instructions an element; forming the constants in one wave
-// alone took 8 % of them and no time).  Blocks that loop over tiles are slower
-// (1024 to 16384 of them: 10 to 14 % in 32 bits, 20 to 30 % in 8).
+// states (6.05 TB/s of 28 bytes an element), 511 us with 8-bit ones (6.36 TB/s
+// of 16.06; a plain copy reaches 6.65): memory bounds both, and in 8 bits the
+// vector units are as busy (78 instructions an element; forming the constants
+// in one wave alone took 8 % of them and no time).  Blocks that loop over tiles
+// are slower (1024 to 16384 of them: 10 to 14 % in 32 bits, 20 to 30 % in 8).
 template <bool E8, bool DITHER, bool NT, bool FUSE, int FRONT, int U>
 __global__ __launch_bounds__(kListBlock, list_checks(FRONT) ? 2 : 4) void list_step_kernel(
     ds_scaler* __restrict__ st, const unsigned char* __restrict__ table, uint32_t* __restrict__ tickets, int32_t count,
