@@ -19,7 +19,10 @@ from .multi_tensor import _dtype_of
 
 class ExpertBalance:
     """``loss()`` leaves, on the device: ``value`` (fp32 scalar), ``counts`` (int32 per expert), ``mean_prob`` (fp32 per
-    expert) and ``used`` (int32 scalar: rows that counted).  They are overwritten by the next call."""
+    expert) and ``used`` (int32 scalar: rows that counted).  They are overwritten by the next call.
+
+    ``stream``: a stream of its own (default: torch's current one).  The caller orders it after what writes the inputs,
+    and what reads the results after it; the inputs may be freed as soon as a call returns."""
 
     def __init__(self, num_experts: int, k: int, coef: float, device="cuda", stream=None):
         import torch
@@ -70,6 +73,14 @@ class ExpertBalance:
             raise ValueError(f"mask: expected a contiguous tensor on {self.counts.device}")
         return mask.data_ptr() if tokens else None
 
+    def _keep(self, *tensors):
+        """On a stream of its own: torch does not hand the tensors' memory out again before that stream has used it."""
+        from .checkpoint import torch_stream
+        there = torch_stream(self.stream, self.torch)
+        for x in tensors:
+            if x is not None and not isinstance(x, int):
+                x.record_stream(there)
+
     def loss(self, logits, mask=None):
         """Counts and loss of ``logits`` (fp16, bf16 or fp32 [tokens, experts], rows any distance apart); ``mask``:
         bool or uint8 per token, 0 leaves it out.  Returns ``value``."""
@@ -80,6 +91,8 @@ class ExpertBalance:
                                       _lib._stream_on(self.stream, self._device))
         if rc:
             _lib._ok(rc, "ds_balance_loss")
+        if self.stream is not None:
+            self._keep(logits, mask)
         return self.value
 
     def gradient(self, logits, out, mask=None, scaler=None, accumulate=False):
@@ -95,4 +108,6 @@ class ExpertBalance:
                                            _lib._stream_on(self.stream, self._device))
         if rc:
             _lib._ok(rc, "ds_balance_loss_grad")
+        if self.stream is not None:
+            self._keep(logits, out, mask, scaler)
         return out
