@@ -126,6 +126,9 @@ class MultiTensorStep:
                                           count=count, sdt=self._sdt)
                 need = _lib.ds_tensor_list_workspace_bytes(shape)
                 self.ws = torch.empty(max(need // 8, 1), dtype=torch.float64, device=device)
+        if stream is not None:                  # not handed out again while steps on that stream still use them
+            for x in (*self.params, *(() if state is None else (state,))):
+                x.record_stream(there)
         if state is None:
             _lib.ds_state_init(self.state, cfg.init_scale, cfg.min_loss_scale, cfg.loss_scale_window, cfg.hysteresis,
                                int(cfg.consecutive_hysteresis), int(cfg.dynamic), self.stream)
