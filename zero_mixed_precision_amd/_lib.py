@@ -9,6 +9,7 @@ built, importing the binding raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -267,6 +268,18 @@ def _stream_on(stream, device_index: int) -> int:
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
     return _raw_stream(device_index)
+
+
+def on_its_device(method):
+    """A method that runs with the GPU of its object (``_device``) current, as launches have to: kernels go to the current
+    GPU, and a default stream's handle is the same on each.  ``_many``: the process sees more than one."""
+    @functools.wraps(method)
+    def call(self, *args, **kw):
+        if self._many and self.torch.cuda.current_device() != self._device:
+            with self.torch.cuda.device(self._device):
+                return method(self, *args, **kw)
+        return method(self, *args, **kw)
+    return call
 
 
 def _ok(rc: int, where: str) -> None:

@@ -14,7 +14,7 @@ loss-scaled backward pass without a host synchronisation.
 from __future__ import annotations
 
 from . import _lib
-from .multi_tensor import _dtype_of
+from .multi_tensor import _dtype_of, check_stream
 
 
 class ExpertBalance:
@@ -40,7 +40,8 @@ class ExpertBalance:
             # enough for any number of tokens (2.1 MB for 512 experts); its count of finished blocks starts at zero
             need = _lib.ds_balance_workspace_bytes(1 << 30, self.E)
             self._ws = torch.zeros((need + 7) // 8, dtype=torch.float64, device=device)
-        self._device = self.counts.device.index
+        check_stream(stream, self.counts.device)
+        self._device, self._many = self.counts.device.index, torch.cuda.device_count() > 1
         self._mask_types = (torch.bool, torch.uint8)
         self._at = (self.counts.data_ptr(), self.mean_prob.data_ptr(), self.value.data_ptr(), self.used.data_ptr(),
                     self._ws.data_ptr(), self._ws.numel() * 8)
@@ -84,6 +85,9 @@ class ExpertBalance:
     def loss(self, logits, mask=None):
         """Counts and loss of ``logits`` (fp16, bf16 or fp32 [tokens, experts], rows any distance apart); ``mask``:
         bool or uint8 per token, 0 leaves it out.  Returns ``value``."""
+        if self._many and self.torch.cuda.current_device() != self._device:     # launches go to the current GPU
+            with self.torch.cuda.device(self._device):
+                return self.loss(logits, mask)
         dt, z, T, stride = self._rows(logits, "logits")
         counts, mean, value, used, ws, ws_bytes = self._at
         rc = _lib.lib.ds_balance_loss(z, dt, T, self.E, stride, None if mask is None else self._mask(mask, T), self.k,
@@ -98,6 +102,12 @@ class ExpertBalance:
     def gradient(self, logits, out, mask=None, scaler=None, accumulate=False):
         """The gradient by ``logits`` of the loss() just taken of them, into ``out`` (their type and shape), times the
         scale of ``scaler`` (a ds_scaler state on the device; None: 1).  accumulate: add to ``out``."""
+        if self._many:
+            if self.torch.cuda.current_device() != self._device:
+                with self.torch.cuda.device(self._device):
+                    return self.gradient(logits, out, mask, scaler, accumulate)
+            if scaler is not None and not isinstance(scaler, int) and scaler.device != self.counts.device:
+                raise ValueError(f"scaler: expected a state on {self.counts.device}, got one on {scaler.device}")
         dt, z, T, stride = self._rows(logits, "logits")
         of, d, rows, gstride = self._rows(out, "out")
         if of != dt or rows != T:

@@ -48,6 +48,13 @@ def per_tensor(value, default, count, what):
     return value
 
 
+def check_stream(stream, device):
+    """Refuses a torch stream of another GPU than ``device`` (a raw handle does not say which it belongs to)."""
+    there = getattr(stream, "device", None)
+    if there is not None and there != device:
+        raise ValueError(f"stream: expected one of {device}, got one of {there}")
+
+
 class MultiTensorStep:
     """``params``: fp16 or bf16 tensors (the step keeps an fp32 master of each and writes the parameter), or fp32 ones
     (their own master); contiguous, on one GPU, any alignment of their type.
@@ -88,7 +95,9 @@ class MultiTensorStep:
                 raise ValueError(f"parameter {i}: expected a tensor in the memory of one GPU, got one on {p.device}")
         device = self.params[0].device if count else torch.device("cuda", torch.cuda.current_device())
 
-        self._device = device.index
+        check_stream(stream, device)
+        # what is called once per step looks at these itself, the rest through on_its_device
+        self._device, self._many = device.index, torch.cuda.device_count() > 1
         self.numels = [p.numel() for p in self.params]
         self.offsets, total = [], 0
         for n in self.numels:
@@ -130,8 +139,9 @@ class MultiTensorStep:
             for x in (*self.params, *(() if state is None else (state,))):
                 x.record_stream(there)
         if state is None:
-            _lib.ds_state_init(self.state, cfg.init_scale, cfg.min_loss_scale, cfg.loss_scale_window, cfg.hysteresis,
-                               int(cfg.consecutive_hysteresis), int(cfg.dynamic), self.stream)
+            with torch.cuda.device(device):
+                _lib.ds_state_init(self.state, cfg.init_scale, cfg.min_loss_scale, cfg.loss_scale_window,
+                                   cfg.hysteresis, int(cfg.consecutive_hysteresis), int(cfg.dynamic), self.stream)
         self.sched = cfg.lr_schedule()
         self._tensors = (_lib.DsTensor * max(count, 1))()
         for i, p in enumerate(self.params):
@@ -161,6 +171,7 @@ class MultiTensorStep:
         """Tensor i as a view of one of the flat arrays."""
         return flat[self.offsets[i]:self.offsets[i] + self.numels[i]]
 
+    @_lib.on_its_device
     def set_gradients(self, grads) -> None:
         """The gradient tensors of the following steps, one per parameter (16-bit in the configuration's format, or
         fp32).  They are read where they lie, so they stay allocated; call it again when one has moved.  On a stream of
@@ -189,6 +200,9 @@ class MultiTensorStep:
 
     def step(self) -> None:
         """One step on the gradients set: overflow check (with the joint norm if clipped), gated Adam, scaler."""
+        if self._many and self.torch.cuda.current_device() != self._device:
+            with self.torch.cuda.device(self._device):
+                return self.step()
         if not self.end_step:
             self.check()
             self.update()
@@ -204,6 +218,9 @@ class MultiTensorStep:
     def check(self) -> None:
         """The first half of step(): the overflow check, with the sum of squares if clipped.  Where several steps share
         a scaler, every check() comes before the first update(), so that all of them see one flag and one norm."""
+        if self._many and self.torch.cuda.current_device() != self._device:
+            with self.torch.cuda.device(self._device):
+                return self.check()
         if self._list is None:
             raise RuntimeError("set_gradients() before check()")
         _lib._ok(_lib.lib.ds_check_overflow_list(self._state_at, self._list_at, self._ws_at, self._ws_bytes,
@@ -211,6 +228,9 @@ class MultiTensorStep:
 
     def update(self) -> None:
         """The second half of step(): gated Adam and, with ``end_step``, the scaler."""
+        if self._many and self.torch.cuda.current_device() != self._device:
+            with self.torch.cuda.device(self._device):
+                return self.update()
         if self._list is None:
             raise RuntimeError("set_gradients() before update()")
         c = self.cfg
@@ -224,15 +244,18 @@ class MultiTensorStep:
         """The loss scale S as an fp32 scalar on the device (a view of the scaler state: no synchronisation)."""
         return self.state[:4].view(self.torch.float32)[0]
 
+    @_lib.on_its_device
     def scaler(self) -> _lib.DsScaler:
         return _lib.ds_state_read(self.state, self.stream)
 
+    @_lib.on_its_device
     def set_applied_steps(self, t: int) -> None:
         """Resume at ``t`` applied steps (the bias corrections, a schedule and the dither go by it)."""
         sc = self.scaler()
         sc.step, sc.iter, sc.skipped = int(t), int(t), 0
         _lib.ds_state_write(self.state, sc, self.stream)
 
+    @_lib.on_its_device
     def moments(self, i: int):
         """(m, v) of tensor i in fp32."""
         m, v = self.view(self.m, i), self.view(self.v, i)
@@ -250,6 +273,7 @@ class MultiTensorStep:
             out.update(m_scale=self.m_scale, v_scale=self.v_scale)
         return out
 
+    @_lib.on_its_device
     def state_dict(self) -> dict:
         """Host copies of the states, masters and scaler (the parameters themselves are the caller's)."""
         sc = self.scaler()                      # synchronises the step's stream
@@ -259,6 +283,7 @@ class MultiTensorStep:
                 "scaler": torch.frombuffer(bytearray(raw), dtype=torch.uint8).clone(),
                 **{k: a.detach().cpu() for k, a in self._arrays().items()}}
 
+    @_lib.on_its_device
     def load_state_dict(self, d: dict) -> None:
         """Restore what state_dict() returned; 16-bit parameters are rewritten from their masters."""
         from .checkpoint import validate_scaler
