@@ -35,3 +35,44 @@ def test_parameters_and_a_shared_scaler_outlive_the_steps_that_use_them(dtype):
     assert not side.query(), "the stream was to be busy here"
     assert not places & {x.data_ptr() for x in again}
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("states", ["fp32", "fp8"])
+def test_what_the_current_stream_reads_is_after_the_steps(states):
+    """Moments, loss scale and a loaded state, while the step's own stream is busy, against a step without one."""
+    side = torch.cuda.Stream()
+    cfg = ZeroMPConfig(initial_scale_power=10, hysteresis=1, lr=1e-3)
+    n = 70_001
+
+    def fresh(stream):
+        gen = torch.Generator(device=DEV)
+        gen.manual_seed(2)
+        params = [(torch.randn(n, generator=gen, device=DEV) * 0.02).half()]
+        op = MultiTensorStep(params, cfg, states=states, stream=stream)
+        op.set_gradients([torch.randn(n, generator=gen, device=DEV).half()])
+        return op
+
+    plain, own = fresh(None), fresh(side)
+    busy(side)
+    for op in (plain, own):
+        op.step()
+    m, v = own.moments(0)
+    for op in (plain, own):
+        op.step()                                # must not reach the moments being read
+    assert not side.query(), "the stream was to be busy here"
+    again = fresh(None)
+    again.step()
+    for got, want in zip((m, v), again.moments(0)):
+        assert torch.equal(got, want)
+    for op in (plain, own):
+        op._grads[0][n - 1] = float("inf")
+    busy(side)
+    own.step()
+    assert float(own.loss_scale) == 512.0        # halved by that step
+    plain.step()
+    saved = again.state_dict()
+    busy(side)
+    own.load_state_dict(saved)
+    got = own.params[0].clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, again.params[0]) and torch.equal(own.m.view(torch.uint8), again.m.view(torch.uint8))

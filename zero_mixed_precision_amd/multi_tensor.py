@@ -167,6 +167,17 @@ class MultiTensorStep:
         from .checkpoint import torch_stream
         return torch_stream(self.stream, self.torch)
 
+    def _after_steps(self):
+        """Torch's current stream goes on after the steps enqueued so far.  (Inside a capture the caller orders a stream
+        of the step's own: a wait for one that is not captured would end it.)"""
+        if self.stream is not None and not self.torch.cuda.is_current_stream_capturing():
+            self.torch.cuda.current_stream().wait_stream(self._torch_stream())
+
+    def _before_steps(self):
+        """The steps to come go on after what torch's current stream has been given so far."""
+        if self.stream is not None and not self.torch.cuda.is_current_stream_capturing():
+            self._torch_stream().wait_stream(self.torch.cuda.current_stream())
+
     def view(self, flat, i: int):
         """Tensor i as a view of one of the flat arrays."""
         return flat[self.offsets[i]:self.offsets[i] + self.numels[i]]
@@ -240,8 +251,11 @@ class MultiTensorStep:
                  "ds_adam_step_list")
 
     @property
+    @_lib.on_its_device
     def loss_scale(self):
-        """The loss scale S as an fp32 scalar on the device (a view of the scaler state: no synchronisation)."""
+        """The loss scale S as an fp32 scalar on the device (a view of the scaler state: no host synchronisation; torch's
+        current stream reads it after the steps enqueued so far)."""
+        self._after_steps()
         return self.state[:4].view(self.torch.float32)[0]
 
     @_lib.on_its_device
@@ -257,13 +271,17 @@ class MultiTensorStep:
 
     @_lib.on_its_device
     def moments(self, i: int):
-        """(m, v) of tensor i in fp32."""
+        """(m, v) of tensor i in fp32, after the steps enqueued so far."""
         m, v = self.view(self.m, i), self.view(self.v, i)
+        self._after_steps()
         if self.states == "fp32":
-            return m.clone(), v.clone()
-        n, blk = self.numels[i], self.offsets[i] // ALIGN
-        scale = lambda s: s[blk:blk + (n + ALIGN - 1) // ALIGN].repeat_interleave(ALIGN)[:n]  # noqa: E731
-        return m.float() * scale(self.m_scale), v.float() * scale(self.v_scale)
+            m, v = m.clone(), v.clone()
+        else:
+            n, blk = self.numels[i], self.offsets[i] // ALIGN
+            scale = lambda s: s[blk:blk + (n + ALIGN - 1) // ALIGN].repeat_interleave(ALIGN)[:n]  # noqa: E731
+            m, v = m.float() * scale(self.m_scale), v.float() * scale(self.v_scale)
+        self._before_steps()
+        return m, v
 
     def _arrays(self):
         out = {"m": self.m, "v": self.v}
@@ -300,6 +318,7 @@ class MultiTensorStep:
             raise ValueError(f"scaler state of {len(raw)} bytes")
         sc = _lib.DsScaler.from_buffer_copy(raw)
         validate_scaler(sc)
+        self._before_steps()                    # parameters and states may still be being read
         with torch.no_grad(), torch.cuda.stream(self._torch_stream()):
             for k, a in arrays.items():
                 a.copy_(d[k])
@@ -307,3 +326,4 @@ class MultiTensorStep:
                 if p.dtype != torch.float32:
                     p.copy_(self.view(self.master, i).view(p.shape))
         _lib.ds_state_write(self.state, sc, self.stream)
+        self._after_steps()
