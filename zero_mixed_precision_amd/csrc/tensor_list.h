@@ -415,22 +415,48 @@ __device__ __forceinline__ void list_encode(const f32x4& m, const f32x4& v, uint
     cm |= (lo | hi) & 0x80808080u;
 }
 
-// One element with 8-bit states: adam1 with the hardware's square root and
+// The root of a subnormal v, which the hardware's instruction takes for zero.
+__device__ __forceinline__ float list_small_root(float v, float root)
+{
+    return v < 0x1p-126f ? __builtin_amdgcn_sqrtf(v * 0x1p64f) * 0x1p-32f : root;
+}
+
+// Four elements with 8-bit states: adam1 with the hardware's square root and
 // reciprocal (each within 1 unit) and fused multiply-adds in the parameter's
 // part.  Its states' arithmetic is adam1's, rounding by rounding.  The IEEE
-// forms take about 20 of some 70 instructions per element here, where they,
-// not the memory, would set the pace.
-__device__ __forceinline__ void adam1_fp8(float graw, float& p, float& m, float& v, const AdamConsts& c)
+// forms are 24 more vector instructions an element beside 78 (one layer: 606 us
+// a step, 573 with these; 363 odd tiles 17.1 and 15.9; four tiles 6.0 and 5.8).
+// A subnormal v has a root below 2^-63:
+// where rbc2 times that is below 2^-26 of eps, as at any usual eps, it is lost
+// in the denominator's rounding, else (`tiny`, the same for a whole block) such
+// a v is scaled first.
+__device__ __forceinline__ bool list_tiny(const AdamConsts& c) { return c.rbc2 * 0x1p-37f > c.eps; }
+
+__device__ __forceinline__ void adam4_fp8(const f32x4& graw, f32x4& p, f32x4& m, f32x4& v, const AdamConsts& c,
+                                          bool tiny)
 {
-    const float g = graw * c.inv;
-    const float m1 = c.b1 * m, m2 = c.omb1 * g;
-    m = m1 + m2;
-    const float gg = g * g, v1 = c.b2 * v, v2 = c.omb2 * gg;
-    v = v1 + v2;
-    // at least the smallest normal number: the reciprocal of a smaller one is infinite
-    const float den = fmaxf(__builtin_fmaf(__builtin_amdgcn_sqrtf(v), c.rbc2, c.eps), 0x1p-126f);
-    p = __builtin_fmaf(-c.lrwd, p, p);
-    p = __builtin_fmaf(-c.step_size, m * __builtin_amdgcn_rcpf(den), p);
+    float root[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float g = graw[k] * c.inv;
+        const float m1 = c.b1 * m[k], m2 = c.omb1 * g;
+        m[k] = m1 + m2;
+        const float gg = g * g, v1 = c.b2 * v[k], v2 = c.omb2 * gg;
+        v[k] = v1 + v2;
+        root[k] = __builtin_amdgcn_sqrtf(v[k]);
+    }
+    if (__builtin_expect(tiny, 0)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            root[k] = list_small_root(v[k], root[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        // at least the smallest normal number: the reciprocal of a smaller one is infinite
+        const float den = fmaxf(__builtin_fmaf(root[k], c.rbc2, c.eps), 0x1p-126f);
+        const float q = __builtin_fmaf(-c.lrwd, p[k], p[k]);
+        p[k] = __builtin_fmaf(-c.step_size, m[k] * __builtin_amdgcn_rcpf(den), q);
+    }
 }
 
 // A tile's quads in registers, four per lane.
@@ -558,6 +584,7 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
 {
     const int64_t q0 = base / 4 + threadIdx.x;
     float scale_m = 0.0f, scale_v = 0.0f;
+    const bool tiny = E8 && list_tiny(c);
     f32x4 g[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -580,12 +607,7 @@ __device__ __forceinline__ void list_finish(const ListEntry& e, int64_t base, Li
         f32x4 p = r.p[u];
         uint32_t cm = 0u, cv = 0u;
         if constexpr (E8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float pk = p[k], mk = m[k], vk = v[k];
-                adam1_fp8(g[u][k], pk, mk, vk, c);
-                p[k] = pk, m[k] = mk, v[k] = vk;
-            }
+            adam4_fp8(g[u], p, m, v, c, tiny);
         } else {
             list_update(g[u], p, m, v, c.lrwd != 0.0f, c);
         }
