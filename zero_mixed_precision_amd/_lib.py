@@ -100,7 +100,9 @@ class DsTensor(ctypes.Structure):
 
 
 class DsTensorList(ctypes.Structure):
-    """Mirror of ``ds_tensor_list`` (32 bytes, host memory)."""
+    """Mirror of ``ds_tensor_list`` (32 bytes, host memory).  ``checked``, for the binding alone: the scaler
+    (its address) under which the gradients of the step at hand have been checked."""
+    checked = None
     _fields_ = [
         ("table", ctypes.c_void_p),
         ("tiles", ctypes.c_int64),
@@ -476,8 +478,9 @@ def ds_check_overflow_list(st, tensors: DsTensorList, workspace=None, workspace_
     """ds_check_overflow over a list; with a workspace also the gradients' sum of squares."""
     ws_bytes = 0 if workspace is None else _nbytes(workspace, workspace_bytes)
     ws = None if workspace is None else _p(workspace, ds_tensor_list_workspace_bytes(tensors), "workspace")
-    _ok(lib.ds_check_overflow_list(_scaler(st), ctypes.byref(tensors), ws, ws_bytes, _s(stream)),
-        "ds_check_overflow_list")
+    at = _scaler(st)
+    _ok(lib.ds_check_overflow_list(at, ctypes.byref(tensors), ws, ws_bytes, _s(stream)), "ds_check_overflow_list")
+    tensors.checked = at
 
 
 def ds_adam_step_list(st, tensors: DsTensorList, lr, sched, beta1, beta2, eps, max_grad_norm, accum_steps,

@@ -65,7 +65,7 @@ class MultiTensorStep:
     ``dither_seed`` (8-bit states): None rounds to nearest, a number rounds with the dither of that seed.
     ``weight_decay`` and ``lr_scale``: one number, or one per tensor (default: the configuration's decay, and 1).
     ``state``: share another step's scaler.  Then check() is called on every step that shares it before update() on
-    the first, and only the last has ``end_step``."""
+    the first, and only the last has ``end_step``; step() without a check() is for a list that is alone."""
 
     def __init__(self, params, cfg: ZeroMPConfig, states="fp32", weight_decay=None, lr_scale=None, dither_seed=None,
                  stream=None, state=None, end_step=True):
@@ -210,21 +210,26 @@ class MultiTensorStep:
         self._grads = grads
 
     def step(self) -> None:
-        """One step on the gradients set: overflow check (with the joint norm if clipped), gated Adam, scaler."""
+        """One step on the gradients set: overflow check (with the joint norm if clipped), gated Adam, scaler.  Where
+        it does not end the step (``end_step``) it comes after check() and is update()."""
         if self._many and self.torch.cuda.current_device() != self._device:
             with self.torch.cuda.device(self._device):
                 return self.step()
-        if not self.end_step:
-            self.check()
-            self.update()
-            return
         if self._list is None:
             raise RuntimeError("set_gradients() before step()")
         c = self.cfg
+        if not self.end_step:
+            if self._list.checked != self._state_at:
+                raise RuntimeError("check() on every step that shares the scaler before this one moves its tensors")
+            self.update()
+            return
+        if c.gradient_clipping > 0 and self._list.checked == self._state_at:
+            raise RuntimeError("check() has summed these gradients' squares already: update() is the other half")
         _lib._ok(_lib.lib.ds_step_list(self._state_at, self._list_at, self._ws_at, self._ws_bytes, c.lr, self._sched_at,
                                        c.betas[0], c.betas[1], c.eps, c.gradient_clipping, c.gradient_accumulation_steps,
                                        self._rounding, self._seed, _lib._stream_on(self.stream, self._device)),
                  "ds_step_list")
+        self._list.checked = None
 
     def check(self) -> None:
         """The first half of step(): the overflow check, with the sum of squares if clipped.  Where several steps share
@@ -236,6 +241,7 @@ class MultiTensorStep:
             raise RuntimeError("set_gradients() before check()")
         _lib._ok(_lib.lib.ds_check_overflow_list(self._state_at, self._list_at, self._ws_at, self._ws_bytes,
                                                  _lib._stream_on(self.stream, self._device)), "ds_check_overflow_list")
+        self._list.checked = self._state_at
 
     def update(self) -> None:
         """The second half of step(): gated Adam and, with ``end_step``, the scaler."""
@@ -249,6 +255,7 @@ class MultiTensorStep:
                                             c.eps, c.gradient_clipping, c.gradient_accumulation_steps, self._rounding,
                                             self._seed, self.end_step, _lib._stream_on(self.stream, self._device)),
                  "ds_adam_step_list")
+        self._list.checked = None
 
     @property
     @_lib.on_its_device
