@@ -626,8 +626,10 @@ ds_status ds_adam_step_list(ds_scaler* st, const ds_tensor_list* list, float lr,
  * 8 tiles, where every block of the update checks the whole list itself, and
  * with a workspace two up to 2048 tiles, where every block adds the check's
  * partial sums itself.  What was checked before in the same step (a flat partition,
- * another list) counts here as for ds_adam_step_list.  Errors as for the two
- * calls; refused as a whole.
+ * another list) counts here as for ds_adam_step_list.  Without a workspace this
+ * list's squares are not summed: max_grad_norm > 0 then clips by what other calls
+ * of the step have summed (by nothing, if none has).  Errors as for the two calls;
+ * refused as a whole.
  */
 ds_status ds_step_list(ds_scaler* st, const ds_tensor_list* list, void* workspace_or_null, size_t workspace_bytes,
                        float lr, const ds_lr_schedule* sched_or_null, double beta1, double beta2, float eps,

@@ -63,6 +63,8 @@ class MultiTensorStep:
     values between tensors are zero and unused.  ``master`` is None if every parameter is fp32.  With states="fp8",
     ``m`` is float8_e4m3fn and ``v`` float8_e5m2, and ``m_scale``, ``v_scale`` hold one scale per 256 elements.
     ``dither_seed`` (8-bit states): None rounds to nearest, a number rounds with the dither of that seed.
+    ``cfg``: rate, betas, eps, clipping and accumulation are read at each step; the schedule, the scaler's settings and
+    the default decay once, here.
     ``weight_decay`` and ``lr_scale``: one number, or one per tensor (default: the configuration's decay, and 1).
     ``state``: share another step's scaler.  Then check() is called on every step that shares it before update() on
     the first, and only the last has ``end_step``; step() without a check() is for a list that is alone."""
@@ -106,7 +108,6 @@ class MultiTensorStep:
         with torch.cuda.device(device):
             here, there = torch.cuda.current_stream(), self._torch_stream()
         there.wait_stream(here)                 # the parameters may still be being written
-        self.clip = float(cfg.gradient_clipping)
         with torch.cuda.device(device), torch.cuda.stream(there):
             f32 = dict(dtype=torch.float32, device=device)
             copies = any(p.dtype != torch.float32 for p in self.params)
@@ -128,13 +129,6 @@ class MultiTensorStep:
             if state is None:
                 self.state = torch.zeros(_lib.ds_scaler_size(), dtype=torch.uint8, device=device)
             self._table = torch.zeros(max(_lib.ds_tensor_list_bytes(count), 16), dtype=torch.uint8, device=device)
-            self.ws = None
-            if self.clip > 0:                   # of the list that set_gradients() writes; no initial contents
-                tiles = sum((n + 4095) // 4096 for n in self.numels)
-                shape = _lib.DsTensorList(table=self._table.data_ptr(), tiles=tiles, elems=sum(self.numels),
-                                          count=count, sdt=self._sdt)
-                need = _lib.ds_tensor_list_workspace_bytes(shape)
-                self.ws = torch.empty(max(need // 8, 1), dtype=torch.float64, device=device)
         if stream is not None:                  # not handed out again while steps on that stream still use them
             for x in (*self.params, *(() if state is None else (state,))):
                 x.record_stream(there)
@@ -159,13 +153,25 @@ class MultiTensorStep:
         self._grads, self._list, self._list_at = None, None, None
         # what every step passes: this object's own arrays, sized and placed here
         self._state_at = _lib._scaler(self.state)
-        self._ws_at = None if self.ws is None else self.ws.data_ptr()
-        self._ws_bytes = 0 if self.ws is None else self.ws.numel() * 8
+        self.ws, self._ws_at, self._ws_bytes = None, None, 0
+        if cfg.gradient_clipping > 0:
+            self._make_workspace()
         self._sched_at = None if self.sched is None else ctypes.byref(self.sched)
 
     def _torch_stream(self):
         from .checkpoint import torch_stream
         return torch_stream(self.stream, self.torch)
+
+    @_lib.on_its_device
+    def _make_workspace(self):
+        """Room for the partial sums of squares of the list that set_gradients() writes; no initial contents."""
+        torch = self.torch
+        shape = _lib.DsTensorList(table=self._table.data_ptr(), tiles=sum((n + 4095) // 4096 for n in self.numels),
+                                  elems=sum(self.numels), count=len(self.numels), sdt=self._sdt)
+        need = _lib.ds_tensor_list_workspace_bytes(shape)
+        with torch.cuda.stream(self._torch_stream()):
+            self.ws = torch.empty(max(need // 8, 1), dtype=torch.float64, device=self._table.device)
+        self._ws_at, self._ws_bytes = self.ws.data_ptr(), self.ws.numel() * 8
 
     def _after_steps(self):
         """Torch's current stream goes on after the steps enqueued so far.  (Inside a capture the caller orders a stream
@@ -225,6 +231,8 @@ class MultiTensorStep:
             return
         if c.gradient_clipping > 0 and self._list.checked == self._state_at:
             raise RuntimeError("check() has summed these gradients' squares already: update() is the other half")
+        if c.gradient_clipping > 0 and self.ws is None:
+            self._make_workspace()
         _lib._ok(_lib.lib.ds_step_list(self._state_at, self._list_at, self._ws_at, self._ws_bytes, c.lr, self._sched_at,
                                        c.betas[0], c.betas[1], c.eps, c.gradient_clipping, c.gradient_accumulation_steps,
                                        self._rounding, self._seed, _lib._stream_on(self.stream, self._device)),
@@ -239,6 +247,8 @@ class MultiTensorStep:
                 return self.check()
         if self._list is None:
             raise RuntimeError("set_gradients() before check()")
+        if self.cfg.gradient_clipping > 0 and self.ws is None:
+            self._make_workspace()
         _lib._ok(_lib.lib.ds_check_overflow_list(self._state_at, self._list_at, self._ws_at, self._ws_bytes,
                                                  _lib._stream_on(self.stream, self._device)), "ds_check_overflow_list")
         self._list.checked = self._state_at
