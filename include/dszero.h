@@ -596,7 +596,10 @@ size_t ds_tensor_list_workspace_bytes(const ds_tensor_list* list);
  * ds_check_overflow_sumsq: per four tiles in a fixed order, then per 4096 of
  * those sums, so the result depends on the list alone.  It adds to st->grad_sumsq, so a flat
  * partition checked in the same step is clipped by the joint norm.  An empty
- * list launches nothing.  Errors as for ds_check_overflow_sumsq; a list that
+ * list launches nothing.  Errors as for ds_check_overflow_sumsq, but that the
+ * scaler and the workspace are compared with the table and with one another
+ * only: the addresses of the list's arrays are on the device, and the caller
+ * keeps both apart from them (so too in the two calls below).  A list that
  * ds_tensor_list_write has not filled -> DS_ERR_NULL / DS_ERR_SIZE.
  */
 ds_status ds_check_overflow_list(ds_scaler* st, const ds_tensor_list* list, void* workspace_or_null,

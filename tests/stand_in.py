@@ -1,6 +1,7 @@
 """Stand-ins for GPU tensors, torch's device and stream functions and the library, for tests of host code without a GPU:
 they hold addresses that nothing reads, and record what is asked of them."""
 import contextlib
+import itertools
 from types import SimpleNamespace
 
 import torch
@@ -12,9 +13,11 @@ class Tensor:
     """A matrix or vector that says it lies on GPU ``index``."""
 
     is_cuda = True
+    places = itertools.count(0x10000000, 0x1000000)
 
-    def __init__(self, *shape, dtype=torch.bfloat16, index=0, at=0x10000000):
-        self.shape, self.dtype, self.index, self.at = torch.Size(shape), dtype, index, at
+    def __init__(self, *shape, dtype=torch.bfloat16, index=0, at=None):
+        self.shape, self.dtype, self.index = torch.Size(shape), dtype, index
+        self.at = next(Tensor.places) if at is None else at
         self.device = torch.device("cuda", index)
         self.recorded = []
 

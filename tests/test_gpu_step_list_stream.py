@@ -76,3 +76,9 @@ def test_what_the_current_stream_reads_is_after_the_steps(states):
     got = own.params[0].clone()
     torch.cuda.synchronize()
     assert torch.equal(got, again.params[0]) and torch.equal(own.m.view(torch.uint8), again.m.view(torch.uint8))
+
+
+def test_a_scaler_inside_a_parameter_is_refused():
+    p = torch.zeros(4096, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="parameter 0 shares"):
+        MultiTensorStep([p], ZeroMPConfig(bf16=True), state=p.view(torch.uint8)[4096:4224])

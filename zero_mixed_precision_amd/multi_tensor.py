@@ -55,6 +55,13 @@ def check_stream(stream, device):
         raise ValueError(f"stream: expected one of {device}, got one of {there}")
 
 
+def check_apart(state, x, what):
+    """Refuses a tensor that shares memory with the scaler's state (steps would overwrite the one with the other)."""
+    a, b = state.data_ptr(), x.data_ptr()
+    if b < a + ctypes.sizeof(_lib.DsScaler) and a < b + x.numel() * x.element_size():
+        raise ValueError(f"{what} shares memory with the scaler's state")
+
+
 class MultiTensorStep:
     """``params``: fp16 or bf16 tensors (the step keeps an fp32 master of each and writes the parameter), or fp32 ones
     (their own master); contiguous, on one GPU, any alignment of their type.
@@ -107,6 +114,10 @@ class MultiTensorStep:
             total += (n + ALIGN - 1) // ALIGN * ALIGN
         with torch.cuda.device(device):
             here, there = torch.cuda.current_stream(), self._torch_stream()
+        self._shares = state is not None        # a state of its own lies apart from all that the caller has
+        if self._shares:
+            for i, p in enumerate(self.params):
+                check_apart(state, p, f"parameter {i}")
         there.wait_stream(here)                 # the parameters may still be being written
         with torch.cuda.device(device), torch.cuda.stream(there):
             f32 = dict(dtype=torch.float32, device=device)
@@ -203,6 +214,8 @@ class MultiTensorStep:
                 raise ValueError(f"gradient {i}: expected a contiguous tensor of {p.numel()} elements on {p.device}")
             if g.dtype == wrong:
                 raise ValueError(f"gradient {i}: {g.dtype} in a {'bf16' if self.cfg.bf16 else 'fp16'} configuration")
+            if self._shares:
+                check_apart(self.state, g, f"gradient {i}")
             self._tensors[i].gdt = _dtype_of(g, torch, f"gradient {i}")
             self._tensors[i].grad = g.data_ptr() or None
         self._list = None
