@@ -655,8 +655,8 @@ ds_status ds_step_list(ds_scaler* st, const ds_tensor_list* list, void* workspac
  * T' = 0: mean_prob, loss and the gradient are 0.  Rows that are not used have
  * gradient 0, whatever they hold.  A used row with a NaN or +infinity makes
  * mean_prob, the loss and its own gradient NaN and counts nothing.  fp32
- * arithmetic per row, sums over rows in fp32 per block and fp64 across blocks
- * in a fixed order (the same bits every call).
+ * arithmetic per row; sums over rows in fp32 for some thousand rows at most,
+ * over these in fp64, in a fixed order (the same bits every call).
  */
 #define DS_MAX_EXPERTS 512
 #define DS_MAX_EXPERT_CHOICES 16

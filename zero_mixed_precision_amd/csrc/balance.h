@@ -24,6 +24,10 @@ constexpr int kBalFinishBlock = 1024, kBalFinishCols = 16;   // finishing kernel
 // block's ticket and fence cost more as they become many (313 blocks: 19.5 us,
 // 15.1 with the second kernel).
 constexpr int64_t kBalMeet = 128;
+// A lane sums the probabilities of so many turns in fp32, the block then in
+// fp64: however many tokens there are, a partial sum has some 80 roundings (one
+// fp32 sum over all turns is off by 1e-4 of itself at 2^28 tokens).
+constexpr int kBalTurns = 64;
 constexpr int64_t kBalGradBlocks = 2048;   // gradient: eight blocks per CU
 constexpr int64_t kBalMaxTokens = int64_t(1) << 30;
 static_assert(DS_MAX_EXPERTS == 512 && DS_MAX_EXPERT_CHOICES == 16, "the instances below");
@@ -210,6 +214,35 @@ __device__ __forceinline__ void bal_end(const BalOut& o, int32_t experts, int ro
     *o.used = rows;
 }
 
+// Lanes whose sums share a row of the block's shared arrays.
+constexpr int bal_span_lanes(int G) { return G > 16 ? G : 16; }
+
+// The lanes' sums x by expert into the shared array: lanes of the same experts
+// in a row of 16 by a rotation, the others a row each.
+template <int G, int V, typename T>
+__device__ __forceinline__ void bal_rows(T (&lds)[kBalBlock / bal_span_lanes(G)][G * V], T (&x)[V])
+{
+    const int lane = static_cast<int>(__lane_id()), g = lane % G;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if constexpr (G == 8)
+            x[v] = x[v] + row_half(x[v]);
+        if (G > 8 || lane % 16 < 8)
+            lds[threadIdx.x / bal_span_lanes(G)][4 * ((v / 4) * G + g) + v % 4] = x[v];
+    }
+}
+
+// Expert e over the shared array's rows, in their order.
+template <int G, int V, typename T>
+__device__ __forceinline__ T bal_row_sum(const T (&lds)[kBalBlock / bal_span_lanes(G)][G * V], int e)
+{
+    T x = 0;
+#pragma unroll
+    for (int i = 0; i < kBalBlock / bal_span_lanes(G); ++i)
+        x = x + lds[i][e];
+    return x;
+}
+
 // Forward: counts and probability sums of this block's rows into row
 // blockIdx.x of the partial arrays, used rows into used[blockIdx.x].  A grid
 // of one block ends the call itself, and of up to kBalMeet the last block.
@@ -219,9 +252,9 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
 {
     constexpr int kRows = 64 / G;          // rows of a wave
     constexpr int kWaves = kBalBlock / 64;
-    constexpr int kSpan = G > 16 ? G : 16; // lanes whose sums share a row of the shared arrays
-    __shared__ int32_t lds_count[kBalBlock / kSpan][G * V];
-    __shared__ float lds_prob[kBalBlock / kSpan][G * V];
+    __shared__ int32_t lds_count[kBalBlock / bal_span_lanes(G)][G * V];
+    __shared__ float lds_prob[kBalBlock / bal_span_lanes(G)][G * V];
+    __shared__ double lds_sum[G * V];
     __shared__ int32_t lds_used[kWaves];
     __shared__ double lds_loss[2 * kWaves];
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64, g = lane % G;
@@ -235,8 +268,23 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
     int used = 0;
     constexpr int es = GF == kF32 ? 4 : 2;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWaves * kRows;
-    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kRows; t0 < s.tokens; t0 += step) {
-        const int64_t t = t0 + lane / G;
+    int turns = 0;
+    bool folded = false;
+    for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * kWaves * kRows; b0 < s.tokens; b0 += step) {
+        if (turns == kBalTurns) {          // the same for all of the block
+            bal_rows<G, V>(lds_prob, prob);
+            __syncthreads();
+            for (int e = threadIdx.x; e < s.experts; e += kBalBlock)
+                lds_sum[e] = (folded ? lds_sum[e] : 0.0) + static_cast<double>(bal_row_sum<G, V>(lds_prob, e));
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                prob[v] = 0.0f;
+            turns = 0;
+            folded = true;
+        }
+        ++turns;
+        const int64_t t = b0 + wave * kRows + lane / G;
         bool on = t < s.tokens;
         if (on && mask != nullptr)
             on = mask[t] != 0;
@@ -305,20 +353,8 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
             cnt[v] += static_cast<int>((chosen >> (V - 1 - v)) & 1u);
         }
     }
-    // lanes of the same experts: in a row of 16 lanes by a rotation, then the
-    // block's rows and waves through shared memory, in a fixed order
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if constexpr (G == 8) {
-            cnt[v] += static_cast<int>(row_half(static_cast<uint32_t>(cnt[v])));
-            prob[v] = prob[v] + row_half(prob[v]);
-        }
-        if (G > 8 || lane % 16 < 8) {
-            const int e = 4 * ((v / 4) * G + g) + v % 4;
-            lds_count[threadIdx.x / kSpan][e] = cnt[v];
-            lds_prob[threadIdx.x / kSpan][e] = prob[v];
-        }
-    }
+    bal_rows<G, V>(lds_count, cnt);
+    bal_rows<G, V>(lds_prob, prob);
 #pragma unroll
     for (int off = G; off < 64; off <<= 1)
         used += __shfl_xor(used, off);
@@ -331,18 +367,13 @@ __global__ __launch_bounds__(kBalBlock) void balance_kernel(const void* __restri
         rows += lds_used[i];
     double part = 0.0;
     for (int e = threadIdx.x; e < s.experts; e += kBalBlock) {
-        int n = 0;
-        float p = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kBalBlock / kSpan; ++i) {
-            n += lds_count[i][e];
-            p = p + lds_prob[i][e];
-        }
+        const int n = bal_row_sum<G, V>(lds_count, e);
+        const double p = (folded ? lds_sum[e] : 0.0) + static_cast<double>(bal_row_sum<G, V>(lds_prob, e));
         if (gridDim.x > 1) {
             w.count[blockIdx.x * s.experts + e] = n;
-            w.prob[blockIdx.x * s.experts + e] = p;
+            w.prob[blockIdx.x * s.experts + e] = static_cast<float>(p);
         } else {
-            part = part + bal_expert(o, s.k, rows, e, n, static_cast<double>(p));
+            part = part + bal_expert(o, s.k, rows, e, n, p);
         }
     }
     if (gridDim.x == 1) {

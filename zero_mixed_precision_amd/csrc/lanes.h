@@ -81,3 +81,5 @@ __device__ __forceinline__ uint32_t row_half(uint32_t x)
 }
 
 __device__ __forceinline__ float row_half(float x) { return __uint_as_float(row_half(__float_as_uint(x))); }
+
+__device__ __forceinline__ int row_half(int x) { return static_cast<int>(row_half(static_cast<uint32_t>(x))); }
