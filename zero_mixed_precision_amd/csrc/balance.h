@@ -635,9 +635,10 @@ __global__ __launch_bounds__(kBalBlock) void balance_grad_kernel(const ds_scaler
             dot = __builtin_fmaf(z[v], f[v], dot);
         }
         dot = row_sum<G>(dot);
+        const float by = on ? factor : 0.0f;       // the factor itself may be infinite
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            z[v] = factor * (z[v] * (f[v] - dot));
+            z[v] = by * (z[v] * (f[v] - dot));
         if (ACC ? on : in)
             bal_store<GF, G, V, ACC>(static_cast<unsigned char*>(dlogits) + t * dstride * es, s.experts, dvec, g, z);
     }
