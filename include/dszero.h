@@ -497,26 +497,32 @@ ds_status ds_partition_range(int64_t total, int32_t world, int32_t rank, int64_t
  * ---------------------------------------------------------------------------
  * For parameters that are not one flat partition: expert groups, norms and
  * biases with a decay of their own, fp32 parameters beside 16-bit ones.  One
- * call covers every tensor of the list with the arithmetic of ds_adam_step,
- * gated by the same ds_scaler; the two Adam states are held in 32 bits
- * (DS_FP32) or in 8 (DS_FP8).
+ * call covers every tensor of the list, gated by the same ds_scaler; the two
+ * Adam states are held in 32 bits (DS_FP32: the arithmetic of ds_adam_step) or
+ * in 8 (DS_FP8: as below).
  *
  * 8-bit states.  Element i of a tensor belongs to block i / 256 of that tensor
  * (the last block may be short).  m is stored as e4m3 codes (sign, 4 exponent
  * bits with bias 7, 3 mantissa bits; no infinity, 0x7F is NaN, the largest
  * value 448), v as e5m2 codes (5 exponent bits with bias 15, 2 mantissa bits;
  * the largest finite value 57344, 0x7F is NaN), with one fp32 scale per block
- * and state; a code of value c stands for c * scale.  A step decodes m and v,
- * updates in fp32 as ds_adam_step does (the parameter moves by the new m and v
- * before they are rounded), and encodes x = m, v, with max = 448, 57344:
+ * and state; a code of value c stands for c * scale.  A step decodes m and v
+ * and updates them in fp32 as ds_adam_step does.  The parameter moves by the new
+ * m and v before they are rounded, in fp32, but with the hardware's square root
+ * and reciprocal (each within 1 unit in the last place) and fused multiply-adds:
+ *   p = p - lr_j weight_decay p
+ *   p = p - step_size (m (1 / max(sqrt(v) rbc2 + eps, 2^-126)))
+ * so it is within a few units of ds_adam_step's, not its bits.  Then x = m, v
+ * are encoded, with max = 448, 57344:
  *   top   = max |x| over the block, at most 2^126
  *   scale = top / max,  a = min(|x| * (max * (1 / top)), max)
- *           (top < 2^-110: scale 0 and codes 0)
+ *           (top < 2^-110: scale 0 and a = 0)
  *   code  = floor(a / ulp + u) steps of ulp: 2^(max(floor(log2 a), -6) - 3)
  *           for m, 2^(max(floor(log2 a), -14) - 2) for v
  * with u = 1/2 (DS_ROUND_NEAREST) or a dither in [0, 1) (DS_ROUND_DITHER).
- * A positive v never becomes code 0, which would leave a zero denominator
- * under a moment that is not zero.  A NaN is kept as a NaN code.  Why a
+ * A positive v never becomes code 0 but code 1, since 0 would leave a zero
+ * denominator under a moment that is not zero (under a scale of 0 code 1 stands
+ * for 0 too).  A NaN is kept as a NaN code.  Why a
  * dither: v moves by (1 - beta2) of itself or less per step, far below half a
  * step of its code, so rounding to nearest would hold it where it is; with
  * the dither the expected value of the stored state is the fp32 one (a
@@ -593,8 +599,9 @@ size_t ds_tensor_list_workspace_bytes(const ds_tensor_list* list);
 /*
  * ds_check_overflow over every gradient of the list, and with a workspace
  * (device, 8-byte aligned, no initial contents) also the sum of squares as
- * ds_check_overflow_sumsq: per four tiles in a fixed order, then per 4096 of
- * those sums, so the result depends on the list alone.  It adds to st->grad_sumsq, so a flat
+ * ds_check_overflow_sumsq: per tile (per four of a list of more than 2048) in a
+ * fixed order, then per 4096 of those sums, so the result depends on the list
+ * alone.  It adds to st->grad_sumsq, so a flat
  * partition checked in the same step is clipped by the joint norm.  An empty
  * list launches nothing.  Errors as for ds_check_overflow_sumsq, but that the
  * scaler and the workspace are compared with the table and with one another
@@ -607,11 +614,11 @@ ds_status ds_check_overflow_list(ds_scaler* st, const ds_tensor_list* list, void
 
 /*
  * The gated Adam step over every tensor of the list in one kernel, with the
- * arithmetic of ds_adam_step (lr / sched_or_null, eps, max_grad_norm and
- * accum_steps as there) and lr_j = lr * lr_scale (fp32) and weight_decay of
+ * arithmetic above (lr / sched_or_null, eps, max_grad_norm and accum_steps as
+ * in ds_adam_step) and lr_j = lr * lr_scale (fp32) and weight_decay of
  * each tensor.  The betas come in 64 bits: 1 - beta is formed there and then
  * rounded (1 - 0.999f in fp32 is 4.7e-5 off 0.001, as much as 8-bit codes can
- * see); betas that fp32 holds give the bits of ds_adam_step.  end_step != 0 also advances the scaler, as
+ * see); with 32-bit states, betas that fp32 holds give the bits of ds_adam_step.  end_step != 0 also advances the scaler, as
  * ds_adam_step_fused does; 0 leaves that to a later call of the same step
  * (another list, or a flat partition's ds_adam_step_fused).  rounding and seed:
  * of 8-bit states (ignored with 32-bit ones).  An empty list only advances the
