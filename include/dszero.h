@@ -512,7 +512,8 @@ ds_status ds_partition_range(int64_t total, int32_t world, int32_t rank, int64_t
  * and reciprocal (each within 1 unit in the last place) and fused multiply-adds:
  *   p = p - lr_j weight_decay p
  *   p = p - step_size (m (1 / max(sqrt(v) rbc2 + eps, 2^-126)))
- * so it is within a few units of ds_adam_step's, not its bits.  Then x = m, v
+ * (step_size = lr_j / (1 - beta1^t), rbc2 = 1 / sqrt(1 - beta2^t)), so it is
+ * within a few units of ds_adam_step's, not its bits.  Then x = m, v
  * are encoded, with max = 448, 57344:
  *   top   = max |x| over the block, at most 2^126
  *   scale = top / max,  a = min(|x| * (max * (1 / top)), max)
