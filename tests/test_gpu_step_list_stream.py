@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from zero_mixed_precision_amd import MultiTensorStep, ZeroMPConfig
+from zero_mixed_precision_amd import ExpertBalance, MultiTensorStep, ZeroMPConfig
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -82,3 +82,20 @@ def test_a_scaler_inside_a_parameter_is_refused():
     p = torch.zeros(4096, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError, match="parameter 0 shares"):
         MultiTensorStep([p], ZeroMPConfig(bf16=True), state=p.view(torch.uint8)[4096:4224])
+
+
+def test_leaves_of_autograd_on_a_stream_of_its_own():
+    """Parameters and logits that require gradients."""
+    side = torch.cuda.Stream()
+    p = torch.zeros(100, 8, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    p.grad = torch.ones_like(p)
+    op = MultiTensorStep([p], ZeroMPConfig(bf16=True, lr=1e-3), stream=side)
+    op.set_gradients([p.grad])
+    balance = ExpertBalance(8, 2, 0.1, stream=side)
+    side.wait_stream(torch.cuda.current_stream())
+    op.step()
+    balance.loss(p)
+    balance.gradient(p, torch.empty_like(p), scaler=op.state)
+    balance.loss(p * 2)
+    torch.cuda.synchronize()
+    assert int(balance.used) == 100 and op.scaler().step == 1
