@@ -602,9 +602,8 @@ size_t ds_tensor_list_workspace_bytes(const ds_tensor_list* list);
  * (device, 8-byte aligned, no initial contents) also the sum of squares as
  * ds_check_overflow_sumsq: per tile (per four of a list of more than 2048) in a
  * fixed order, then per 4096 of those sums, so the result depends on the list
- * alone.  It adds to st->grad_sumsq, so a flat
- * partition checked in the same step is clipped by the joint norm.  An empty
- * list launches nothing.  Errors as for ds_check_overflow_sumsq, but that the
+ * alone.  It adds to st->grad_sumsq, so a flat partition checked in the same
+ * step is clipped by the joint norm.  An empty list launches nothing.  Errors as for ds_check_overflow_sumsq, but that the
  * scaler and the workspace are compared with the table and with one another
  * only: the addresses of the list's arrays are on the device, and the caller
  * keeps both apart from them (so too in the two calls below).  A list that
@@ -619,7 +618,8 @@ ds_status ds_check_overflow_list(ds_scaler* st, const ds_tensor_list* list, void
  * in ds_adam_step) and lr_j = lr * lr_scale (fp32) and weight_decay of
  * each tensor.  The betas come in 64 bits: 1 - beta is formed there and then
  * rounded (1 - 0.999f in fp32 is 4.7e-5 off 0.001, as much as 8-bit codes can
- * see); with 32-bit states, betas that fp32 holds give the bits of ds_adam_step.  end_step != 0 also advances the scaler, as
+ * see); with 32-bit states, betas that fp32 holds give the bits of
+ * ds_adam_step.  end_step != 0 also advances the scaler, as
  * ds_adam_step_fused does; 0 leaves that to a later call of the same step
  * (another list, or a flat partition's ds_adam_step_fused).  rounding and seed:
  * of 8-bit states (ignored with 32-bit ones).  An empty list only advances the

@@ -10,19 +10,25 @@
 //
 // 131072 x 256 in bf16, the 8 largest: forward 40.6 us, bound by vector
 // instructions (95 % of the busy cycles; about a third of them keep and merge the
-// lists of the largest), the sums of its partial rows 9.0 us, bound by the
-// latency of reading them, gradient 29.5 us (134 MB, 4.6 TB/s).  Loads that do
-// not wait for the mask, or 512 blocks instead of 1024, made the forward
-// kernel 44 and 45 us.
+// lists of the largest), the sums of its partial rows 9.7 us, bound by the
+// latency of reading them, gradient 29.6 us (134 MB): neither memory (4.5 TB/s,
+// two thirds of a copy's rate) nor the vector units (77 % of the busy cycles)
+// bound it alone, since a wave loads its next row when it has done with one.
+// Loads that do not wait for the mask, or 512 blocks instead of 1024, made the
+// forward kernel 44 and 45 us.
 
 constexpr int kBalBlock = 256;
 constexpr int kBalMaxBlocks = 1024;        // rows of partial sums: four blocks per CU
 constexpr int kBalFinishBlock = 1024, kBalFinishCols = 16;   // finishing kernel: lanes, experts per block
 // Up to so many blocks (and 64 experts) the last block of the forward kernel
-// ends the call, instead of a second kernel: with the gradient 64 x 64 takes
-// 10.4 us and 4096 x 64 13.6 (128 blocks; 15.2 with the second kernel).  A
-// block's ticket and fence cost more as they become many (313 blocks: 19.5 us,
-// 15.1 with the second kernel).
+// ends the call, instead of a second kernel.  That saves a launch, which is what
+// a call from a program costs, and takes the GPU longer, a ticket and a fence
+// for each block.  Loss and gradient of 64 experts, called one after another,
+// with the meeting and with the second kernel: 32 blocks 11.4 and 14.6 us, 64
+// 12.4 and 14.6, 128 14.1 and 14.5, 160 15.4 and 14.5, 256 18.2 and 14.7 (8
+// experts: 128 12.8 and 14.6, 192 14.6 and 14.6, 256 16.6 and 14.6).  Inside a
+// graph, where launches are cheap, the second kernel is ahead from 32 blocks on
+// (the loss alone at 128 blocks: 10.1 and 7.0).
 constexpr int64_t kBalMeet = 128;
 // A lane sums the probabilities of so many turns in fp32, the block then in
 // fp64: however many tokens there are, a partial sum has some 80 roundings (one
@@ -94,7 +100,10 @@ __device__ __forceinline__ void bal_load(const void* row, const BalShape& s, int
     }
 }
 
-// z becomes exp(z - max); returns 1 / sum.  `top` is the row's maximum (NaN
+// z becomes exp(z - max); returns 1 / sum.  The exponential is the hardware's, of
+// 2, of z - max times log2 e: off by some 2 units and 2 |z - max| 2^-24 of itself,
+// as the tests count it (the accurate one: 131072 x 256 with its gradient 91.6 us,
+// 78.2 with this).  `top` is the row's maximum (NaN
 // left out); a NaN or +infinity in the row makes the sum, so 1 / sum, NaN.
 // A row that is not used passes top 0 and comes back as zeros.
 template <int G, int V>
@@ -460,7 +469,7 @@ __global__ __launch_bounds__(kBalFinishBlock) void balance_finish_kernel(int32_t
                                                                          BalWork w, BalOut o)
 {
     constexpr int kGroups = kBalFinishBlock / COLS, kWaves = kBalFinishBlock / 64;
-    constexpr int kDeep = 10;
+    constexpr int kDeep = 10;              // rows on their way a lane: 131072 x 256 takes the same with 4, 6 or 16 (1 %)
     __shared__ double lds_prob[kWaves][COLS];
     __shared__ int32_t lds_count[kWaves][COLS];
     __shared__ int32_t lds_used[kWaves];

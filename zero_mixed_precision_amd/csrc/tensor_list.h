@@ -12,10 +12,14 @@ constexpr int kListQuads = 4;
 static_assert(kListTile == 4 * kListBlock * kListQuads, "one tile per block");
 static_assert(DS_STATE_BLOCK == 4 * 64, "one quad per lane of a wave is one block of an 8-bit state");
 // Tiles that share one partial sum of squares, and a block's turn: four keep
-// enough loads on their way on a long list (four layers: 254 us, 369 us one by
-// one); a short one is over sooner one by one (363 tiles: 3.9 us, 6.4 us).
+// enough loads on their way on a long list, a short one is over as soon one by
+// one.  Check and sum of a bf16 list, one by one and by fours: 256 tiles 6.4 and
+// 6.6 us, 512 6.7 and 6.9, 1024 7.4 and 6.9, 2048 8.9 and 7.4, 4096 12.9 and
+// 9.6, four layers (197,636) 433 and 272.  Up to kCheckFew one by one, though
+// fours are ahead from some 700 on: ds_step_list's update adds up these sums,
+// one per tile, up to as many tiles (kStepParts).
 constexpr int kCheckTiles = 4;
-constexpr int32_t kCheckFew = 2048;                // tiles: up to here one by one
+constexpr int32_t kCheckFew = 2048;                // tiles
 // Tickets of the blocks of one step: taken from one address they cost about
 // 13 ns each, one after another (2.5 ms for four layers' 197,636 blocks, more
 // than the 8-bit step itself), so block b takes one from counter b % 64 (of 16
@@ -415,7 +419,12 @@ __device__ __forceinline__ void list_encode(const f32x4& m, const f32x4& v, uint
     cm |= (lo | hi) & 0x80808080u;
 }
 
-// The root of a subnormal v, which the hardware's instruction takes for zero.
+// The hardware's square root takes a subnormal v for zero.  Its true root is
+// below 2^-63: where rbc2 times that is below 2^-26 of eps, as at any usual eps,
+// it is lost in the denominator's rounding; else (the same for a whole block)
+// such a v is scaled first.
+__device__ __forceinline__ bool list_tiny(const AdamConsts& c) { return c.rbc2 * 0x1p-37f > c.eps; }
+
 __device__ __forceinline__ float list_small_root(float v, float root)
 {
     return v < 0x1p-126f ? __builtin_amdgcn_sqrtf(v * 0x1p64f) * 0x1p-32f : root;
@@ -424,14 +433,8 @@ __device__ __forceinline__ float list_small_root(float v, float root)
 // Four elements with 8-bit states: adam1 with the hardware's square root and
 // reciprocal (each within 1 unit) and fused multiply-adds in the parameter's
 // part.  Its states' arithmetic is adam1's, rounding by rounding.  The IEEE
-// forms are 24 more vector instructions an element beside 78 (one layer: 606 us
+// forms are 24 more vector instructions an element beside 79 (one layer: 606 us
 // a step, 573 with these; 363 odd tiles 17.1 and 15.9; four tiles 6.0 and 5.8).
-// A subnormal v has a root below 2^-63:
-// where rbc2 times that is below 2^-26 of eps, as at any usual eps, it is lost
-// in the denominator's rounding, else (`tiny`, the same for a whole block) such
-// a v is scaled first.
-__device__ __forceinline__ bool list_tiny(const AdamConsts& c) { return c.rbc2 * 0x1p-37f > c.eps; }
-
 __device__ __forceinline__ void adam4_fp8(const f32x4& graw, f32x4& p, f32x4& m, f32x4& v, const AdamConsts& c,
                                           bool tiny)
 {
@@ -951,10 +954,10 @@ struct ListWaveCheck {
 // kFrontCheck and kFrontCheckSum its check.  The gradients are only read, so
 // the blocks need not meet: each comes to the same flag and sum.  The step's
 // constants (fp64 powers and divisions) are formed while the loads are on
-// their way.  One layer of 202,383,360 parameters in bf16: 937 us with 32-bit
-// states (6.05 TB/s of 28 bytes an element), 511 us with 8-bit ones (6.36 TB/s
+// their way.  One layer of 202,383,360 parameters in bf16: 938 us with 32-bit
+// states (6.04 TB/s of 28 bytes an element), 508 us with 8-bit ones (6.40 TB/s
 // of 16.06; a plain copy reaches 6.65): memory bounds both, and in 8 bits the
-// vector units are as busy (78 instructions an element; forming the constants
+// vector units are as busy (79 instructions an element; forming the constants
 // in one wave alone took 8 % of them and no time).  Blocks that loop over tiles
 // are slower (1024 to 16384 of them: 10 to 14 % in 32 bits, 20 to 30 % in 8).
 template <bool E8, bool DITHER, bool NT, bool FUSE, int FRONT, int U>
