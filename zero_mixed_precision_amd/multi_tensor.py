@@ -214,10 +214,11 @@ class MultiTensorStep:
                 raise ValueError(f"gradient {i}: expected a contiguous tensor of {p.numel()} elements on {p.device}")
             if g.dtype == wrong:
                 raise ValueError(f"gradient {i}: {g.dtype} in a {'bf16' if self.cfg.bf16 else 'fp16'} configuration")
-            if self._shares:
-                check_apart(self.state, g, f"gradient {i}")
             self._tensors[i].gdt = _dtype_of(g, torch, f"gradient {i}")
             self._tensors[i].grad = g.data_ptr() or None
+        if self._shares:
+            for i, g in enumerate(grads):
+                check_apart(self.state, g, f"gradient {i}")
         self._list = None
         tensors = self._tensors if grads else []
         self._list = _lib.ds_tensor_list_write(self._table, tensors, self._sdt, self.stream)
