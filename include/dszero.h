@@ -702,6 +702,148 @@ ds_status ds_balance_loss_grad(const ds_scaler* st_or_null, const void* logits, 
                                float coef, const int32_t* counts, const int32_t* used, void* dlogits,
                                int64_t grad_stride, int32_t accumulate, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Tokens sorted by expert, moved there and back, with the gradients
+ * ---------------------------------------------------------------------------
+ * chosen: [tokens] rows of k expert numbers (int32 or int64: index_bytes 4 or
+ * 8), rows row_stride elements apart.  A number outside 0..experts-1 drops its
+ * choice (a token over an expert's capacity).  The pairs p = t k + j that are
+ * not dropped are sorted by expert, and by p inside an expert: pair p has slot
+ * place[p] (dropped: -1), slot q holds pair source[q] (behind the last one: -1),
+ * and expert e has the slots offsets[e] .. offsets[e + 1] - 1.  The same expert
+ * twice in a row is two pairs.
+ *
+ * The moves take rows of `width` values of type dt (DS_FP16, DS_BF16, DS_FP32):
+ *   gather        out[place[t k + j]] = x[t]
+ *   gather_grad   dx[t] = sum_j dout[place[t k + j]]
+ *   combine       out[t] = sum_j gate_tj rows[place[t k + j]]
+ *   combine_grad  drows[place[t k + j]] = gate_tj dout[t],
+ *                 dgate_tj = sum_d dout[t]_d rows[place[t k + j]]_d
+ * over the choices that are not dropped (a token without any: 0; a dropped
+ * choice's gate is not read, its dgate is 0).  Sums in fp32 in a fixed order (j
+ * ascending), rounded once.  Rows of the sorted side behind the last slot are
+ * left as they are, and a slot of place at or past the sorted side's row count
+ * is passed over.  Gates and their gradients have the type gdt, any of the
+ * three.  Every array needs the alignment of its type only.
+ * Limits: experts 1..512, k 1..16, tokens k < 2^31, width 1..2^24.  Errors:
+ * sizes, strides smaller than a row or a short workspace -> DS_ERR_SIZE;
+ * an unknown dt, gdt or index_bytes -> DS_ERR_DTYPE; else as in the conventions.
+ */
+
+/* Device scratch of ds_dispatch_sort (0 for sizes out of range). */
+size_t ds_dispatch_workspace_bytes(int64_t tokens, int32_t experts, int32_t k);
+
+/* offsets: int32[experts + 1], place and source: int32[tokens k], all written.
+ * workspace: device, 4-byte aligned, no initial contents. */
+ds_status ds_dispatch_sort(const void* chosen, int32_t index_bytes, int64_t tokens, int32_t experts, int32_t k,
+                           int64_t row_stride, int32_t* offsets, int32_t* place, int32_t* source, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+ds_status ds_dispatch_gather(const void* x, ds_dtype dt, int64_t tokens, int32_t k, int64_t width, int64_t x_stride,
+                             const int32_t* place, void* out, int64_t out_stride, int64_t out_rows, void* stream);
+
+ds_status ds_dispatch_gather_grad(const void* dout, ds_dtype dt, int64_t tokens, int32_t k, int64_t width,
+                                  int64_t dout_stride, int64_t dout_rows, const int32_t* place, void* dx,
+                                  int64_t dx_stride, void* stream);
+
+ds_status ds_dispatch_combine(const void* rows, ds_dtype dt, int64_t tokens, int32_t k, int64_t width, int64_t rows_stride,
+                              int64_t rows_count, const int32_t* place, const void* gates, ds_dtype gdt,
+                              int64_t gates_stride, void* out, int64_t out_stride, void* stream);
+
+ds_status ds_dispatch_combine_grad(const void* dout, ds_dtype dt, int64_t tokens, int32_t k, int64_t width,
+                                   int64_t dout_stride, const void* rows, int64_t rows_stride, int64_t rows_count,
+                                   const int32_t* place, const void* gates, ds_dtype gdt, int64_t gates_stride, void* drows,
+                                   int64_t drows_stride, void* dgates, int64_t dgates_stride, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Distillation from a teacher's top logits, with the gradient
+ * ---------------------------------------------------------------------------
+ * logits: the student's, [tokens] rows of `vocab` values of type dt, row_stride
+ * apart.  teacher, index: [tokens] rows of k of the teacher's logits (type tdt)
+ * and their places in the vocabulary (int32 or int64: index_bytes 4 or 8), in
+ * any order; a negative place is an absent entry, so that rows may have
+ * different numbers of them; the same place twice adds up.  A row is used if
+ * mask is NULL or mask[t] != 0, it has an entry above -infinity, and some logit
+ * is above -infinity; T' is the number of used rows (*used).  With q the softmax
+ * of the row's entries / temperature and p that of its logits / temperature:
+ *   token_loss[t] = temperature^2 sum_j q_j (log q_j - log p_place(j))
+ *   loss = coef / T' sum over used rows of token_loss[t]
+ *   dlogits_tv = S coef temperature / T' (p_v - sum of q_j with place(j) = v)
+ * with S = st->scale read on the device (st_or_null NULL: 1).  Entries with q_j
+ * = 0 add nothing.  token_loss and the gradient of rows that are not used are 0,
+ * whatever they hold; T' = 0: loss 0.  A used row with a NaN or +infinity, or
+ * with a place at or past vocab, has a NaN loss and a gradient of NaN.  fp32
+ * arithmetic per row, rounded once; the mean over rows in fp64 in a fixed order.
+ * dlogits_or_null (type dt, rows grad_stride apart) may be the logits
+ * themselves, with the same stride; else it overlaps no other array.
+ * accumulate != 0 adds to what it holds (in fp32, rounded once; rows that are
+ * not used stay as they are).  token_loss: fp32[tokens], loss: fp32[1], used:
+ * int32[1].  workspace: device, 8-byte aligned, cleared to zero once before its
+ * first call (every call leaves its count at zero; calls that share it must not
+ * run at the same time).  Arrays need the alignment of their type only.
+ * Errors: tokens outside [0, 2^30], vocab outside [1, 2^30], k outside 1..1024,
+ * a stride smaller than a row, a short workspace -> DS_ERR_SIZE; a temperature
+ * outside [2^-10, 2^10], coef negative or not finite, accumulate without
+ * dlogits -> DS_ERR_HPARAM; an unknown dt, tdt or index_bytes -> DS_ERR_DTYPE;
+ * else as in the conventions.
+ */
+#define DS_MAX_TEACHER_LOGITS 1024
+
+/* Device scratch of ds_distill_loss (0 for sizes out of range). */
+size_t ds_distill_workspace_bytes(int64_t tokens);
+
+ds_status ds_distill_loss(const ds_scaler* st_or_null, const void* logits, ds_dtype dt, int64_t tokens, int64_t vocab,
+                          int64_t row_stride, const void* teacher, ds_dtype tdt, int64_t teacher_stride, const void* index,
+                          int32_t index_bytes, int64_t index_stride, int32_t k, const uint8_t* mask_or_null,
+                          float temperature, float coef, float* token_loss, float* loss, int32_t* used,
+                          void* dlogits_or_null, int64_t grad_stride, int32_t accumulate, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Cross entropy over a large vocabulary from hidden states, with the gradient
+ * ---------------------------------------------------------------------------
+ * hidden: [tokens] rows of `width` values, weight: [vocab] rows of `width`
+ * values, both of type dt (DS_FP16 or DS_BF16), rows hidden_stride and
+ * weight_stride apart; targets: [tokens] (int32 or int64: index_bytes 4 or 8).
+ * A row is used if mask is NULL or mask[t] != 0, and its target is not negative;
+ * T' is the number of used rows (*used).  With z = hidden weight^T (fp32 sums),
+ * never kept:
+ *   token_loss[t] = log sum_v exp(z_tv) - z_t,target
+ *   loss = coef / T' sum over used rows of token_loss[t]
+ *   dz_tv = S coef / T' (exp(z_tv) / sum_u exp(z_tu) - [v = target])
+ *   dhidden = dz weight,  dweight = dz^T hidden
+ * with S = st->scale read on the device (st_or_null NULL: 1).  Rows that are not
+ * used have token_loss and dhidden 0 and reach nothing else, whatever they hold;
+ * T' = 0: loss and gradients are 0.  A target at or past vocab makes its row's
+ * loss and gradient, and with them dweight, NaN.  exp(z) / sum - [v = target] is
+ * rounded to dt (in fp16 times 2^15) before the two products of the gradient,
+ * which sum in fp32 and are rounded once.  dhidden_or_null: type dt;
+ * dweight_or_null: type dwdt, dt or DS_FP32 (without both: the loss alone).
+ * accumulate != 0 adds to dweight (in fp32, rounded once).
+ * workspace: device, 256-byte aligned, no initial contents; calls that share it
+ * must not run at the same time.  It holds a piece of the vocabulary's dz, 512
+ * MiB at most for up to 131072 tokens.  Arrays need the alignment of their type
+ * only; a weight whose rows are 16-byte aligned and a multiple of 64 values
+ * wide is read where it lies, any other copied piece by piece.
+ * Errors: tokens outside [0, 2^24], vocab outside [1, 2^24], width outside
+ * [1, 65536], a stride smaller than a row, a short workspace -> DS_ERR_SIZE;
+ * dt not 16-bit, dwdt another type, an unknown index_bytes -> DS_ERR_DTYPE; coef
+ * negative or not finite, accumulate without dweight -> DS_ERR_HPARAM; else as
+ * in the conventions.
+ */
+
+/* Device scratch of ds_vocab_ce (0 for sizes out of range). */
+size_t ds_vocab_ce_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width);
+
+ds_status ds_vocab_ce(const ds_scaler* st_or_null, const void* hidden, int64_t hidden_stride, const void* weight,
+                      int64_t weight_stride, ds_dtype dt, const void* targets, int32_t index_bytes, int64_t tokens,
+                      int64_t vocab, int64_t width, const uint8_t* mask_or_null, float coef, float* token_loss, float* loss,
+                      int32_t* used, void* dhidden_or_null, int64_t dhidden_stride, void* dweight_or_null, ds_dtype dwdt,
+                      int64_t dweight_stride, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static string naming a status code. */
 const char* ds_status_string(ds_status s);
 

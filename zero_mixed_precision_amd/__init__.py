@@ -13,6 +13,10 @@ from .layout import FlatLayout
 from .step import ShardStep
 from .multi_tensor import MultiTensorStep
 from .balance import ExpertBalance
+from .dispatch import ExpertDispatch
+from .distill import TopLogitDistillation
+from .vocab import VocabCrossEntropy
 
 __all__ = ["_lib", "DS_BF16", "DS_FP16", "DS_FP32", "DsError", "DsScaler", "ZeroMPConfig", "FlatLayout",
-           "ShardStep", "MultiTensorStep", "ExpertBalance"]
+           "ShardStep", "MultiTensorStep", "ExpertBalance", "ExpertDispatch", "TopLogitDistillation",
+           "VocabCrossEntropy"]

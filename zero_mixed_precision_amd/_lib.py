@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libdszero.so")
 DS_OK, DS_ERR_NULL, DS_ERR_SIZE, DS_ERR_ALIGN, DS_ERR_DTYPE, DS_ERR_HPARAM, DS_ERR_ALIAS, DS_ERR_HIP = range(8)
 DS_FP16, DS_FP32, DS_BF16, DS_FP8 = 1, 2, 3, 4
 DS_ROUND_NEAREST, DS_ROUND_DITHER = 0, 1
-DS_STATE_BLOCK, DS_MAX_EXPERTS, DS_MAX_EXPERT_CHOICES = 256, 512, 16
+DS_STATE_BLOCK, DS_MAX_EXPERTS, DS_MAX_EXPERT_CHOICES, DS_MAX_TEACHER_LOGITS = 256, 512, 16, 1024
 
 EXPORTED = (
     "ds_scaler_size", "ds_state_init", "ds_state_read", "ds_state_write", "ds_accumulate",
@@ -29,6 +29,9 @@ EXPORTED = (
     "ds_accumulate_adam_double_buffered", "ds_update_loss_scale_double_buffered",
     "ds_tensor_list_bytes", "ds_tensor_list_write", "ds_tensor_list_workspace_bytes", "ds_check_overflow_list",
     "ds_adam_step_list", "ds_step_list", "ds_balance_workspace_bytes", "ds_balance_loss", "ds_balance_loss_grad",
+    "ds_dispatch_workspace_bytes", "ds_dispatch_sort", "ds_dispatch_gather", "ds_dispatch_gather_grad",
+    "ds_dispatch_combine", "ds_dispatch_combine_grad", "ds_distill_workspace_bytes", "ds_distill_loss",
+    "ds_vocab_ce_workspace_bytes", "ds_vocab_ce",
 )
 DS_NOALLOC_MAX_ELEMS = 17175674880
 DS_LR_WARMUP, DS_LR_WARMUP_DECAY = 1, 2
@@ -192,6 +195,20 @@ def _load():
                             ctypes.c_int),
         "ds_balance_loss_grad": ([vp, vp, ctypes.c_int, i64, i32, i64, vp, i32, f32, vp, vp, vp, i64, i32, vp],
                                  ctypes.c_int),
+        "ds_dispatch_workspace_bytes": ([i64, i32, i32], ctypes.c_size_t),
+        "ds_dispatch_sort": ([vp, i32, i64, i32, i32, i64, vp, vp, vp, vp, ctypes.c_size_t, vp], ctypes.c_int),
+        "ds_dispatch_gather": ([vp, ctypes.c_int, i64, i32, i64, i64, vp, vp, i64, i64, vp], ctypes.c_int),
+        "ds_dispatch_gather_grad": ([vp, ctypes.c_int, i64, i32, i64, i64, i64, vp, vp, i64, vp], ctypes.c_int),
+        "ds_dispatch_combine": ([vp, ctypes.c_int, i64, i32, i64, i64, i64, vp, vp, ctypes.c_int, i64, vp, i64, vp],
+                                ctypes.c_int),
+        "ds_dispatch_combine_grad": ([vp, ctypes.c_int, i64, i32, i64, i64, vp, i64, i64, vp, vp, ctypes.c_int, i64, vp,
+                                      i64, vp, i64, vp], ctypes.c_int),
+        "ds_distill_workspace_bytes": ([i64], ctypes.c_size_t),
+        "ds_distill_loss": ([vp, vp, ctypes.c_int, i64, i64, i64, vp, ctypes.c_int, i64, vp, i32, i64, i32, vp, f32, f32,
+                             vp, vp, vp, vp, i64, i32, vp, ctypes.c_size_t, vp], ctypes.c_int),
+        "ds_vocab_ce_workspace_bytes": ([i64, i64, i64], ctypes.c_size_t),
+        "ds_vocab_ce": ([vp, vp, i64, vp, i64, ctypes.c_int, vp, i32, i64, i64, i64, vp, f32, vp, vp, vp, vp, i64, vp,
+                         ctypes.c_int, i64, i32, vp, ctypes.c_size_t, vp], ctypes.c_int),
         "ds_layout_greedy": ([vp, i32, i64, i64, vp, vp, vp, vp, ctypes.POINTER(i32),
                               ctypes.POINTER(i64)], ctypes.c_int),
         "ds_partition_range": ([i64, i32, i32, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)],
@@ -539,6 +556,18 @@ def ds_balance_loss_grad(st_or_null, logits, dtype, tokens, experts, row_stride,
                                  _p(counts, 4 * E, "counts"), _p(used, 4, "used"),
                                  _rows(dlogits, dtype, T, E, int(grad_stride), "dlogits"), int(grad_stride),
                                  int(bool(accumulate)), _s(stream)), "ds_balance_loss_grad")
+
+
+def ds_dispatch_workspace_bytes(tokens, experts, k) -> int:
+    return lib.ds_dispatch_workspace_bytes(int(tokens), int(experts), int(k))
+
+
+def ds_distill_workspace_bytes(tokens) -> int:
+    return lib.ds_distill_workspace_bytes(int(tokens))
+
+
+def ds_vocab_ce_workspace_bytes(tokens, vocab, width) -> int:
+    return lib.ds_vocab_ce_workspace_bytes(int(tokens), int(vocab), int(width))
 
 
 def ds_layout_greedy(numels, cap, align):

@@ -1515,6 +1515,10 @@ ds_status adam_step(const ds_scaler* st, float* master, float* m, float* v, uint
 #include "lanes.h"
 #include "tensor_list.h"
 #include "balance.h"
+#include "dispatch.h"
+#include "distill.h"
+#include "gemm.h"
+#include "vocab.h"
 
 }  // namespace
 
@@ -2136,6 +2140,87 @@ ds_status ds_balance_loss_grad(const ds_scaler* st_or_null, const void* logits, 
 {
     return balance_grad(st_or_null, logits, dt, tokens, experts, row_stride, mask_or_null, k, coef, counts, used,
                         dlogits, grad_stride, accumulate != 0, static_cast<hipStream_t>(stream));
+}
+
+size_t ds_dispatch_workspace_bytes(int64_t tokens, int32_t experts, int32_t k)
+{
+    return disp_sizes_ok(tokens, experts, k) ? disp_ws_bytes(tokens * k, experts) : 0;
+}
+
+ds_status ds_dispatch_sort(const void* chosen, int32_t index_bytes, int64_t tokens, int32_t experts, int32_t k,
+                           int64_t row_stride, int32_t* offsets, int32_t* place, int32_t* source, void* workspace,
+                           size_t workspace_bytes, void* stream)
+{
+    return dispatch_sort(chosen, index_bytes, tokens, experts, k, row_stride, offsets, place, source, workspace,
+                         workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+ds_status ds_dispatch_gather(const void* x, ds_dtype dt, int64_t tokens, int32_t k, int64_t width, int64_t x_stride,
+                             const int32_t* place, void* out, int64_t out_stride, int64_t out_rows, void* stream)
+{
+    return dispatch_gather(DispMove{tokens, width, out_rows, k, place}, dt, x, x_stride, out, out_stride,
+                           static_cast<hipStream_t>(stream));
+}
+
+ds_status ds_dispatch_gather_grad(const void* dout, ds_dtype dt, int64_t tokens, int32_t k, int64_t width,
+                                  int64_t dout_stride, int64_t dout_rows, const int32_t* place, void* dx,
+                                  int64_t dx_stride, void* stream)
+{
+    return dispatch_combine(DispMove{tokens, width, dout_rows, k, place}, dt, dout, dout_stride, nullptr, dt, 0, false, dx,
+                            dx_stride, static_cast<hipStream_t>(stream));
+}
+
+ds_status ds_dispatch_combine(const void* rows, ds_dtype dt, int64_t tokens, int32_t k, int64_t width, int64_t rows_stride,
+                              int64_t rows_count, const int32_t* place, const void* gates, ds_dtype gdt,
+                              int64_t gates_stride, void* out, int64_t out_stride, void* stream)
+{
+    return dispatch_combine(DispMove{tokens, width, rows_count, k, place}, dt, rows, rows_stride, gates, gdt, gates_stride,
+                            true, out, out_stride, static_cast<hipStream_t>(stream));
+}
+
+ds_status ds_dispatch_combine_grad(const void* dout, ds_dtype dt, int64_t tokens, int32_t k, int64_t width,
+                                   int64_t dout_stride, const void* rows, int64_t rows_stride, int64_t rows_count,
+                                   const int32_t* place, const void* gates, ds_dtype gdt, int64_t gates_stride, void* drows,
+                                   int64_t drows_stride, void* dgates, int64_t dgates_stride, void* stream)
+{
+    return dispatch_combine_grad(DispMove{tokens, width, rows_count, k, place}, dt, dout, dout_stride, rows, rows_stride,
+                                 gates, gdt, gates_stride, drows, drows_stride, dgates, dgates_stride,
+                                 static_cast<hipStream_t>(stream));
+}
+
+size_t ds_distill_workspace_bytes(int64_t tokens)
+{
+    return distill_tokens_ok(tokens) ? distill_ws_bytes(tokens) : 0;
+}
+
+ds_status ds_distill_loss(const ds_scaler* st_or_null, const void* logits, ds_dtype dt, int64_t tokens, int64_t vocab,
+                          int64_t row_stride, const void* teacher, ds_dtype tdt, int64_t teacher_stride, const void* index,
+                          int32_t index_bytes, int64_t index_stride, int32_t k, const uint8_t* mask_or_null,
+                          float temperature, float coef, float* token_loss, float* loss, int32_t* used,
+                          void* dlogits_or_null, int64_t grad_stride, int32_t accumulate, void* workspace,
+                          size_t workspace_bytes, void* stream)
+{
+    return distill_loss(st_or_null, logits, dt, tokens, vocab, row_stride, teacher, tdt, teacher_stride, index, index_bytes,
+                        index_stride, k, mask_or_null, temperature, coef, token_loss, loss, used, dlogits_or_null,
+                        grad_stride, accumulate != 0, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+size_t ds_vocab_ce_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width)
+{
+    VocabSizes s;
+    VocabWork w;
+    return vocab_sizes(tokens, vocab, width, &s) ? vocab_work(s, nullptr, &w) : 0;
+}
+
+ds_status ds_vocab_ce(const ds_scaler* st_or_null, const void* hidden, int64_t hidden_stride, const void* weight,
+                      int64_t weight_stride, ds_dtype dt, const void* targets, int32_t index_bytes, int64_t tokens,
+                      int64_t vocab, int64_t width, const uint8_t* mask_or_null, float coef, float* token_loss, float* loss,
+                      int32_t* used, void* dhidden_or_null, int64_t dhidden_stride, void* dweight_or_null, ds_dtype dwdt,
+                      int64_t dweight_stride, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return vocab_ce(st_or_null, hidden, hidden_stride, weight, weight_stride, dt, targets, index_bytes, tokens, vocab, width,
+                    mask_or_null, coef, token_loss, loss, used, dhidden_or_null, dhidden_stride, dweight_or_null, dwdt,
+                    dweight_stride, accumulate != 0, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 ds_status ds_layout_greedy(const int64_t* numels, int32_t count, int64_t cap, int64_t align,

@@ -1,0 +1,549 @@
+// vocab.h -- softmax cross entropy over a large vocabulary from hidden states
+// and the head's weight, without keeping the logits, with its gradient.
+// Included by dszero.hip inside its namespace.
+//
+//   z = X W^T,  l_t = lse_t - z_t,y,  dz = S coef / T' (softmax(z) - onehot(y))
+//   dX = dz W,  dW = dz^T X
+//
+// The used rows are packed first (compact, padded with zeros to tiles of 64 k),
+// so rows that are left out cost nothing and what they hold reaches nothing.
+// The first product goes over the whole vocabulary and leaves a maximum and a
+// sum per row and tile, joined per row afterwards.  The gradient goes over
+// pieces of the vocabulary: the logits of a piece are formed again and become
+// dz in 16 bits at the product's end, then two products take it to dX (summed
+// over the pieces in fp32) and to the piece's rows of dW.  8 T V D operations
+// instead of the 6 that keeping the logits would take.
+//
+// dz in 16 bits: each value is off by half a unit of its own, as much as the
+// result's own rounding; in fp16 it is held times 2^15, so that probabilities
+// down to 2^-29 have all their bits.
+
+constexpr int kVocabTile = 256;            // rows of packed arrays are a multiple of it
+constexpr int64_t kVocabMaxTokens = int64_t(1) << 24;
+constexpr int64_t kVocabMaxVocab = int64_t(1) << 24;
+constexpr int64_t kVocabMaxWidth = 65536;
+constexpr int64_t kVocabMaxStride = int64_t(1) << 22;   // of W read in place: offsets in a tile have 32 bits
+constexpr uint64_t kVocabPiece = uint64_t(1) << 29;     // bytes of a piece's dz
+
+struct VocabSizes {
+    int64_t tokens, vocab, width;
+    int64_t tp, dp, vc;                    // padded tokens and width, vocabulary of a piece
+    int64_t tiles;                         // partial sums per row
+};
+
+struct VocabWork {
+    int32_t *used, *slot, *list, *target;  // [1], [tokens], [tp], [tp]
+    float* of_target;                      // [tp] the target's logit
+    TopSum* part;                          // [tiles][tp]
+    TopSum* row;                           // [tp] maximum, log2 of the sum
+    uint16_t* x;                           // [tp][dp]
+    uint16_t* w;                           // [vc][dp], where W cannot be read in place
+    uint16_t* dz;                          // [tp][vc]
+    float* dx;                             // [tp][dp], where there are several pieces
+};
+
+// Compact numbers of the used rows (t ascending), by one block.
+constexpr int kVocabListBlock = 1024;
+template <typename I>
+__global__ __launch_bounds__(kVocabListBlock) void vocab_list_kernel(const I* __restrict__ targets,
+                                                                const uint8_t* __restrict__ mask, VocabSizes s,
+                                                                VocabWork w, float* __restrict__ token_loss)
+{
+    __shared__ int32_t part[kVocabListBlock / 64];
+    const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
+    int32_t before = 0;
+    for (int64_t t0 = 0; t0 < s.tokens; t0 += kVocabListBlock) {
+        const int64_t t = t0 + threadIdx.x;
+        int64_t y = -1;
+        if (t < s.tokens && (mask == nullptr || mask[t] != 0))
+            y = targets[t];
+        const uint64_t on = __ballot(y >= 0);
+        if (lane == 0)
+            part[wave] = __popcll(on);
+        __syncthreads();
+        int32_t at = before + __popcll(on & ((1ull << lane) - 1));
+        for (int v = 0; v < kVocabListBlock / 64; ++v) {
+            at += v < wave ? part[v] : 0;
+            before += part[v];
+        }
+        if (t < s.tokens) {
+            w.slot[t] = y >= 0 ? at : -1;
+            if (y >= 0) {
+                w.list[at] = static_cast<int32_t>(t);
+                w.target[at] = y < s.vocab ? static_cast<int32_t>(y) : -1;
+            } else {
+                token_loss[t] = 0.0f;
+            }
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        *w.used = before;
+}
+
+// A row of `width` 16-bit values, padded with zeros to dp, by one wave.
+__device__ __forceinline__ void pack_row(const uint16_t* from, int64_t width, uint16_t* to, int64_t dp, int lane)
+{
+    for (int64_t c = lane; c < dp / 8; c += 64) {
+        u32x4 v = {0, 0, 0, 0};
+        if (from != nullptr) {
+            if (8 * c + 8 <= width) {
+                v = *reinterpret_cast<const u32x4_any*>(from + 8 * c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (8 * c + i < width)
+                        v[i / 2] |= static_cast<uint32_t>(from[8 * c + i]) << (16 * (i % 2));
+            }
+        }
+        reinterpret_cast<u32x4*>(to)[c] = v;
+    }
+}
+
+constexpr int kPackBlock = 256;
+// Wave t < tokens: row t of X to its place, or zeros to its gradient; the waves
+// behind: zero rows up to the next 64.
+__global__ __launch_bounds__(kPackBlock) void vocab_pack_kernel(const uint16_t* __restrict__ hidden, int64_t hs,
+                                                                uint16_t* __restrict__ dhidden, int64_t dhs,
+                                                                VocabSizes s, VocabWork w)
+{
+    const int lane = static_cast<int>(__lane_id());
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPackBlock / 64);
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kPackBlock / 64) + threadIdx.x / 64; t < s.tokens + kBK;
+         t += step) {
+        if (t >= s.tokens) {
+            const int64_t row = *w.used + (t - s.tokens);
+            if (row < (*w.used + kBK - 1) / kBK * kBK)
+                pack_row(nullptr, 0, w.x + row * s.dp, s.dp, lane);
+            continue;
+        }
+        const int slot = w.slot[t];
+        if (slot >= 0) {
+            pack_row(hidden + t * hs, s.width, w.x + slot * s.dp, s.dp, lane);
+        } else if (dhidden != nullptr) {
+            for (int64_t i = lane; i < s.width; i += 64)
+                dhidden[t * dhs + i] = 0;
+        }
+    }
+}
+
+// Rows v0 .. v0 + rows - 1 of W.
+__global__ __launch_bounds__(kPackBlock) void vocab_pack_weight_kernel(const uint16_t* __restrict__ weight, int64_t ws,
+                                                                       int64_t rows, VocabSizes s, uint16_t* __restrict__ to)
+{
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPackBlock / 64);
+    for (int64_t v = static_cast<int64_t>(blockIdx.x) * (kPackBlock / 64) + threadIdx.x / 64; v < rows; v += step)
+        pack_row(weight + v * ws, s.width, to + v * s.dp, s.dp, static_cast<int>(__lane_id()));
+}
+
+// A piece of the vocabulary: W's rows from v0 on.
+struct VocabPiece {
+    const uint16_t* w;
+    int64_t stride, v0, rows;
+};
+
+// Logits of a piece and, at the end, (DZ) dz or else each row's maximum and sum
+// over the tile.  m: vocabulary, n: tokens.
+template <int FMT, bool DZ, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kernel(VocabPiece p, VocabSizes s, VocabWork w)
+{
+    using P = Product<FMT, false, false, BM, BN, WM, WN>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[P::kLds];
+    const int used = *w.used;
+    int tm, tn;
+    tile_of(static_cast<int>(blockIdx.x), static_cast<int>((p.rows + BM - 1) / BM), static_cast<int>((s.tokens + BN - 1) / BN),
+            tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    if (n0 >= used)
+        return;
+    P c;
+    c.run(lds, Operand{p.w + m0 * p.stride, p.stride, static_cast<int32_t>(p.rows) - m0, 0},
+          Operand{w.x + n0 * s.dp, s.dp, static_cast<int32_t>(s.tp) - n0, 0}, static_cast<int>(s.dp / kBK));
+    const int rows = static_cast<int>(p.rows) - m0;            // of the tile that exist
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) {
+        const int n = n0 + c.col(j);
+        const bool on = n < used;
+        const int y = on ? w.target[n] : -1;
+        const int hit = y < 0 ? -1 : static_cast<int>(y - p.v0) - m0;
+        if constexpr (DZ) {
+            const TopSum row = on ? w.row[n] : TopSum{0.0f, 0.0f};
+            constexpr float unit = FMT == kF16 ? 32768.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f32x4 d;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int m = c.row(i, 4 * q + r);
+                        float z = __builtin_amdgcn_exp2f(
+                            __builtin_fmaf(c.acc[i][j][4 * q + r] - row.top, kLog2e, -row.sum));
+                        z = m == hit ? z - 1.0f : z;
+                        d[r] = on && m < rows ? z * unit : 0.0f;
+                    }
+                    const int m = m0 + c.row(i, 4 * q);
+                    if (m < s.vc && n < s.tp)
+                        *reinterpret_cast<u32x2*>(w.dz + static_cast<int64_t>(n) * s.vc + m) = narrow4<FMT>(d);
+                }
+        } else {
+            float top = kNegInf;
+#pragma unroll
+            for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int m = c.row(i, r);
+                    if (m == hit)
+                        w.of_target[n] = c.acc[i][j][r];
+                    if (m < rows)
+                        top = fmaxf(top, c.acc[i][j][r]);
+                }
+            const float ref = finite_top(top);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (c.row(i, r) < rows)
+                        sum = sum + __builtin_amdgcn_exp2f((c.acc[i][j][r] - ref) * kLog2e);
+            TopSum part = join(TopSum{top, sum}, TopSum{__shfl_xor(top, 32), __shfl_xor(sum, 32)}, kLog2e);
+            if (c.lane < 32)
+                reinterpret_cast<TopSum*>(lds)[c.wm / WM * BN + c.col(j)] = part;
+        }
+    }
+    if constexpr (!DZ) {
+        __syncthreads();
+        for (int n = threadIdx.x; n < BN; n += P::kThreads)
+            if (n0 + n < used) {
+                TopSum part = reinterpret_cast<TopSum*>(lds)[n];
+                for (int i = 1; i < P::kWavesM; ++i)
+                    part = join(part, reinterpret_cast<TopSum*>(lds)[i * BN + n], kLog2e);
+                w.part[(p.v0 / BM + tm) * s.tp + n0 + n] = part;
+            }
+    }
+}
+
+// Joins each row's partial sums: 64 rows a block, its waves share the tiles.
+constexpr int kJoinBlock = 256;
+__global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, VocabWork w, float* __restrict__ token_loss)
+{
+    __shared__ TopSum part[kJoinBlock / 64][64];
+    const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
+    const int used = *w.used;
+    for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * 64; n0 < used; n0 += static_cast<int64_t>(gridDim.x) * 64) {
+        const int64_t n = n0 + lane;
+        TopSum sum{kNegInf, 0.0f};
+        if (n < used)
+            for (int64_t i = wave; i < s.tiles; i += kJoinBlock / 64)
+                sum = join(sum, w.part[i * s.tp + n], kLog2e);
+        part[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0 && n < used) {
+            for (int i = 1; i < kJoinBlock / 64; ++i)
+                sum = join(sum, part[i][lane], kLog2e);
+            const bool known = w.target[n] >= 0;
+            const float log_sum = __builtin_amdgcn_logf(sum.sum);
+            // a target past the vocabulary: NaN for the row
+            w.row[n] = TopSum{known ? sum.top : __builtin_nanf(""), log_sum};
+            token_loss[w.list[n]] = known ? (sum.top - w.of_target[n]) + log_sum * kLn2 : __builtin_nanf("");
+        }
+        __syncthreads();
+    }
+}
+
+struct VocabGrad {
+    const ds_scaler* st;
+    float coef;
+    uint16_t* dhidden;
+    int64_t dhs;
+    void* dweight;
+    int64_t dws;
+    int32_t first, last;                   // of the pieces
+};
+
+template <int FMT>
+__device__ __forceinline__ float vocab_factor(const VocabGrad& g, int used)
+{
+    const double scale = g.st != nullptr ? static_cast<double>(g.st->scale) : 1.0;
+    return used > 0 ? static_cast<float>(scale * static_cast<double>(g.coef) / used * (FMT == kF16 ? 1.0 / 32768.0 : 1.0))
+                    : 0.0f;
+}
+
+// Four values at column d of a row of `width`, the row's last ones one by one.
+template <int FMT>
+__device__ __forceinline__ void store4(void* row, int64_t d, int64_t width, f32x4 x)
+{
+    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+    if (d + 4 <= width) {
+        if constexpr (FMT == kF32)
+            *reinterpret_cast<u32x4_4*>(static_cast<float*>(row) + d) = __builtin_bit_cast(u32x4, x);
+        else
+            *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(row) + d) = narrow4<FMT>(x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (d + i < width)
+                store_elem<FMT>(row, d + i, x[i]);
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ f32x4 load4(const void* row, int64_t d, int64_t width)
+{
+    f32x4 x = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (d + i < width)
+            x[i] = load_elem<FMT>(row, d + i);
+    return x;
+}
+
+// dX of a piece: m: width, n: tokens, k: the piece's vocabulary.
+template <int FMT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_dx_kernel(VocabPiece p, VocabSizes s, VocabWork w,
+                                                                            VocabGrad g)
+{
+    using P = Product<FMT, true, false, BM, BN, WM, WN>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[P::kLds];
+    const int used = *w.used;
+    int tm, tn;
+    tile_of(static_cast<int>(blockIdx.x), static_cast<int>((s.dp + BM - 1) / BM), static_cast<int>((s.tokens + BN - 1) / BN),
+            tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    if (n0 >= used)
+        return;
+    P c;
+    c.run(lds, Operand{p.w + m0, p.stride, static_cast<int32_t>(s.dp) - m0, static_cast<int32_t>(p.rows)},
+          Operand{w.dz + n0 * s.vc, s.vc, static_cast<int32_t>(s.tp) - n0, 0}, static_cast<int>((p.rows + kBK - 1) / kBK));
+    const float factor = vocab_factor<FMT>(g, used);
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) {
+        const int n = n0 + c.col(j);
+        if (n >= used)
+            continue;
+        const int64_t t = g.last ? w.list[n] : 0;
+#pragma unroll
+        for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int d = m0 + c.row(i, 4 * q);
+                if (d >= s.dp)
+                    continue;
+                f32x4 x = {c.acc[i][j][4 * q], c.acc[i][j][4 * q + 1], c.acc[i][j][4 * q + 2], c.acc[i][j][4 * q + 3]};
+                f32x4* sum = reinterpret_cast<f32x4*>(w.dx + static_cast<int64_t>(n) * s.dp + d);
+                if (!g.first)
+                    x = x + *sum;
+                if (g.last)
+                    store4<FMT>(g.dhidden + t * g.dhs, d, s.width, x * factor);
+                else
+                    *sum = x;
+            }
+    }
+}
+
+// dW of a piece: m: width, n: the piece's vocabulary, k: tokens.
+template <int FMT, int OF, bool ACC, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_dw_kernel(VocabPiece p, VocabSizes s, VocabWork w,
+                                                                            VocabGrad g)
+{
+    using P = Product<FMT, true, true, BM, BN, WM, WN>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[P::kLds];
+    const int used = *w.used;
+    int tm, tn;
+    tile_of(static_cast<int>(blockIdx.x), static_cast<int>((s.dp + BM - 1) / BM), static_cast<int>((p.rows + BN - 1) / BN), tm,
+            tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    P c;
+    const int k_rows = static_cast<int>(s.tp);
+    c.run(lds, Operand{w.x + m0, s.dp, static_cast<int32_t>(s.dp) - m0, k_rows},
+          Operand{w.dz + n0, s.vc, static_cast<int32_t>(s.vc) - n0, k_rows}, (used + kBK - 1) / kBK);
+    const float factor = vocab_factor<FMT>(g, used);
+    constexpr int es = OF == kF32 ? 4 : 2;
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) {
+        const int n = n0 + c.col(j);
+        if (n >= p.rows)
+            continue;
+        unsigned char* row = static_cast<unsigned char*>(g.dweight) + (p.v0 + n) * g.dws * es;
+#pragma unroll
+        for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int d = m0 + c.row(i, 4 * q);
+                if (d >= s.width)
+                    continue;
+                f32x4 x = {c.acc[i][j][4 * q], c.acc[i][j][4 * q + 1], c.acc[i][j][4 * q + 2], c.acc[i][j][4 * q + 3]};
+                x = x * factor;
+                if constexpr (ACC)
+                    x = x + load4<OF>(row, d, s.width);
+                store4<OF>(row, d, s.width, x);
+            }
+    }
+}
+
+// ---- host side ----
+
+bool vocab_sizes(int64_t tokens, int64_t vocab, int64_t width, VocabSizes* s)
+{
+    if (tokens < 0 || tokens > kVocabMaxTokens || vocab < 1 || vocab > kVocabMaxVocab || width < 1 || width > kVocabMaxWidth)
+        return false;
+    auto up = [](int64_t x, int64_t a) { return (x + a - 1) / a * a; };
+    s->tokens = tokens;
+    s->vocab = vocab;
+    s->width = width;
+    s->tp = up(tokens > 0 ? tokens : 1, kVocabTile);
+    s->dp = up(width, kBK);
+    const int64_t whole = up(vocab, kVocabTile);
+    int64_t vc = static_cast<int64_t>(kVocabPiece / (2 * static_cast<uint64_t>(s->tp))) / kVocabTile * kVocabTile;
+    vc = vc < 2048 ? 2048 : vc > 65536 ? 65536 : vc;
+    s->vc = vc < whole ? vc : whole;
+    s->tiles = 0;
+    return true;
+}
+
+constexpr int kVocabMinTile = 128;         // of the vocabulary, for the partial sums' space
+
+// The workspace's arrays from `base` on, each 256-byte aligned; returns the bytes.
+uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
+{
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        unsigned char* p = base + at;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    const uint64_t tp = static_cast<uint64_t>(s.tp), dp = static_cast<uint64_t>(s.dp), vc = static_cast<uint64_t>(s.vc);
+    const uint64_t tiles = (static_cast<uint64_t>(s.vocab) + kVocabMinTile - 1) / kVocabMinTile;
+    w->used = reinterpret_cast<int32_t*>(take(4));
+    w->slot = reinterpret_cast<int32_t*>(take(4 * tp));
+    w->list = reinterpret_cast<int32_t*>(take(4 * tp));
+    w->target = reinterpret_cast<int32_t*>(take(4 * tp));
+    w->of_target = reinterpret_cast<float*>(take(4 * tp));
+    w->part = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * tp * tiles));
+    w->row = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * tp));
+    w->x = reinterpret_cast<uint16_t*>(take(2 * tp * dp));
+    w->w = reinterpret_cast<uint16_t*>(take(2 * vc * dp));
+    w->dz = reinterpret_cast<uint16_t*>(take(2 * tp * vc));
+    w->dx = reinterpret_cast<float*>(take(s.vc < s.vocab ? 4 * tp * dp : 0));
+    return at;
+}
+
+struct VocabCall {
+    const uint16_t* weight;
+    int64_t ws;
+    bool in_place;                         // W is read where it lies
+    ds_dtype dwt;
+    bool accumulate;
+};
+
+VocabPiece vocab_piece(const VocabSizes& s, const VocabWork& w, const VocabCall& c, int64_t v0, hipStream_t st)
+{
+    const int64_t rows = s.vocab - v0 < s.vc ? s.vocab - v0 : s.vc;
+    if (c.in_place)
+        return {c.weight + v0 * c.ws, c.ws, v0, rows};
+    vocab_pack_weight_kernel<<<grid_blocks((rows + 3) / 4, kPackBlock), kPackBlock, 0, st>>>(c.weight + v0 * c.ws, c.ws,
+                                                                                           rows, s, w.w);
+    return {w.w, s.dp, v0, rows};
+}
+
+unsigned vocab_tiles(int64_t m, int bm, int64_t n, int bn)
+{
+    return static_cast<unsigned>(((m + bm - 1) / bm) * ((n + bn - 1) / bn));
+}
+
+template <int FMT, int BM, int BN, int WM, int WN>
+ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const VocabGrad& g, float* token_loss, float* loss,
+                    int32_t* used, hipStream_t st)
+{
+    constexpr int threads = (BM / WM) * (BN / WN) * 64;
+    static_assert(BM >= kVocabMinTile, "space of the partial sums");
+    s.tiles = (s.vocab + BM - 1) / BM;
+    if (s.tokens > 0) {
+        for (int64_t v0 = 0; v0 < s.vocab; v0 += s.vc) {
+            const VocabPiece p = vocab_piece(s, w, c, v0, st);
+            vocab_logits_kernel<FMT, false, BM, BN, WM, WN>
+                <<<vocab_tiles(p.rows, BM, s.tokens, BN), threads, 0, st>>>(p, s, w);
+        }
+        vocab_join_kernel<<<grid_blocks((s.tokens + 63) / 64, kJoinBlock), kJoinBlock, 0, st>>>(s, w, token_loss);
+    }
+    rows_mean_kernel<<<1, kMeanBlock, 0, st>>>(token_loss, s.tokens, w.used, g.coef, loss, used, 0);
+    if (launched() != DS_OK)
+        return DS_ERR_HIP;
+    if (g.dhidden == nullptr && g.dweight == nullptr)
+        return DS_OK;
+    for (int64_t v0 = 0; v0 < s.vocab; v0 += s.vc) {
+        const VocabPiece p = vocab_piece(s, w, c, v0, st);
+        VocabGrad h = g;
+        h.first = v0 == 0;
+        h.last = v0 + p.rows == s.vocab;
+        if (s.tokens > 0) {
+            vocab_logits_kernel<FMT, true, BM, BN, WM, WN>
+                <<<vocab_tiles(p.rows, BM, s.tokens, BN), threads, 0, st>>>(p, s, w);
+            if (g.dhidden != nullptr)
+                vocab_dx_kernel<FMT, BM, BN, WM, WN><<<vocab_tiles(s.dp, BM, s.tokens, BN), threads, 0, st>>>(p, s, w, h);
+        }
+        if (g.dweight != nullptr) {
+            const unsigned b = vocab_tiles(s.dp, BM, p.rows, BN);
+            if (c.dwt == DS_FP32) {
+                if (c.accumulate) vocab_dw_kernel<FMT, kF32, true, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
+                else              vocab_dw_kernel<FMT, kF32, false, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
+            } else {
+                if (c.accumulate) vocab_dw_kernel<FMT, FMT, true, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
+                else              vocab_dw_kernel<FMT, FMT, false, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
+            }
+        }
+        if (launched() != DS_OK)
+            return DS_ERR_HIP;
+    }
+    return DS_OK;
+}
+
+ds_status vocab_ce(const ds_scaler* scaler, const void* hidden, int64_t hs, const void* weight, int64_t ws, ds_dtype dt,
+                   const void* targets, int32_t index_bytes, int64_t tokens, int64_t vocab, int64_t width,
+                   const uint8_t* mask, float coef, float* token_loss, float* loss, int32_t* used, void* dhidden, int64_t dhs,
+                   void* dweight, ds_dtype dwt, int64_t dws, bool accumulate, void* workspace, size_t bytes, hipStream_t st)
+{
+    VocabSizes s;
+    if (!vocab_sizes(tokens, vocab, width, &s) || !rows_ok(tokens, width, hs) || !rows_ok(vocab, width, ws) ||
+        (dhidden != nullptr && !rows_ok(tokens, width, dhs)) || (dweight != nullptr && !rows_ok(vocab, width, dws)))
+        return DS_ERR_SIZE;
+    if (!is16(dt) || (index_bytes != 4 && index_bytes != 8) || (dweight != nullptr && dwt != dt && dwt != DS_FP32))
+        return DS_ERR_DTYPE;
+    if (!finite_ge0(coef) || (accumulate && dweight == nullptr))
+        return DS_ERR_HPARAM;
+    if (weight == nullptr || loss == nullptr || used == nullptr || workspace == nullptr ||
+        (tokens > 0 && (hidden == nullptr || targets == nullptr || token_loss == nullptr)))
+        return DS_ERR_NULL;
+    const uint64_t ib = static_cast<uint64_t>(index_bytes);
+    if (!aligned(hidden, 2) || !aligned(weight, 2) || !aligned(targets, ib) || !aligned(token_loss, 4) || !aligned(loss, 4) ||
+        !aligned(used, 4) || !aligned(dhidden, 2) || !aligned(dweight, dwt == DS_FP32 ? 4 : 2) || !aligned(scaler, 8) ||
+        !aligned(workspace, 256))
+        return DS_ERR_ALIGN;
+    VocabWork w;
+    const uint64_t need = vocab_work(s, static_cast<unsigned char*>(workspace), &w);
+    if (bytes < need)
+        return DS_ERR_SIZE;
+    const uint64_t ut = static_cast<uint64_t>(tokens);
+    const void* p[11] = {hidden, weight, targets, mask, scaler, token_loss, loss, used, dhidden, dweight, workspace};
+    const uint64_t span[11] = {disp_span(tokens, width, hs, dt), disp_span(vocab, width, ws, dt), ib * ut, ut,
+                               sizeof(ds_scaler), 4 * ut, 4, 4,
+                               dhidden == nullptr ? 0 : disp_span(tokens, width, dhs, dt),
+                               dweight == nullptr ? 0 : disp_span(vocab, width, dws, dwt), need};
+    if (bal_alias(p, span, 11, 5))
+        return DS_ERR_ALIAS;
+    const VocabCall c{static_cast<const uint16_t*>(weight), ws,
+                      aligned(weight, 16) && ws % 8 == 0 && width % kBK == 0 && ws <= kVocabMaxStride, dwt, accumulate};
+    const VocabGrad g{scaler, coef, static_cast<uint16_t*>(dhidden), dhs, dweight, dws, 0, 0};
+    if (index_bytes == 4)
+        vocab_list_kernel<int32_t><<<1, kVocabListBlock, 0, st>>>(static_cast<const int32_t*>(targets), mask, s, w, token_loss);
+    else
+        vocab_list_kernel<int64_t><<<1, kVocabListBlock, 0, st>>>(static_cast<const int64_t*>(targets), mask, s, w, token_loss);
+    vocab_pack_kernel<<<grid_blocks((tokens + kBK + 3) / 4, kPackBlock), kPackBlock, 0, st>>>(
+        static_cast<const uint16_t*>(hidden), hs, g.dhidden, dhs, s, w);
+    if (launched() != DS_OK)
+        return DS_ERR_HIP;
+    if (dt == DS_FP16)
+        return vocab_run<kF16, 128, 128, 64, 64>(s, w, c, g, token_loss, loss, used, st);
+    return vocab_run<kBF16, 128, 128, 64, 64>(s, w, c, g, token_loss, loss, used, st);
+}
