@@ -14,16 +14,14 @@
 constexpr int kMeanBlock = 1024;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// loss = coef / used * sum of token_loss (fp64, fixed order), *used_out = used.
-// `count` is left at zero for the next call.
-__global__ __launch_bounds__(kMeanBlock) void rows_mean_kernel(const float* __restrict__ token_loss, int64_t tokens,
-                                                              int32_t* __restrict__ count, float coef,
-                                                              float* __restrict__ loss, int32_t* __restrict__ used_out,
-                                                              int32_t clear)
+// coef / used * the sum of the block's rows' losses (fp64, fixed order), for
+// thread 0 of a block of BLOCK lanes.
+template <int BLOCK>
+__device__ __forceinline__ float rows_mean(const float* token_loss, int64_t tokens, int32_t used, float coef)
 {
-    __shared__ double part[kMeanBlock / 64];
+    __shared__ double part[BLOCK / 64];
     double sum = 0.0;
-    for (int64_t t = threadIdx.x; t < tokens; t += kMeanBlock)
+    for (int64_t t = threadIdx.x; t < tokens; t += BLOCK)
         sum += static_cast<double>(token_loss[t]);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
@@ -31,12 +29,22 @@ __global__ __launch_bounds__(kMeanBlock) void rows_mean_kernel(const float* __re
     if (__lane_id() == 0)
         part[threadIdx.x / 64] = sum;
     __syncthreads();
+    sum = 0.0;
+    for (int w = 0; w < BLOCK / 64; ++w)
+        sum += part[w];
+    return used > 0 ? static_cast<float>(static_cast<double>(coef) * sum / used) : 0.0f;
+}
+
+// `count` is left at zero for the next call, if asked.
+__global__ __launch_bounds__(kMeanBlock) void rows_mean_kernel(const float* __restrict__ token_loss, int64_t tokens,
+                                                              int32_t* __restrict__ count, float coef,
+                                                              float* __restrict__ loss, int32_t* __restrict__ used_out,
+                                                              int32_t clear)
+{
+    const int32_t used = *count;
+    const float mean = rows_mean<kMeanBlock>(token_loss, tokens, used, coef);
     if (threadIdx.x == 0) {
-        sum = 0.0;
-        for (int w = 0; w < kMeanBlock / 64; ++w)
-            sum += part[w];
-        const int32_t used = *count;
-        *loss = used > 0 ? static_cast<float>(static_cast<double>(coef) * sum / used) : 0.0f;
+        *loss = mean;
         *used_out = used;
         if (clear)
             *count = 0;
@@ -55,9 +63,11 @@ struct Distill {
     float* token_loss;
     unsigned char* grad;
     int64_t gs;
-    int32_t* count;                        // used rows
+    int32_t* count;                        // used rows; behind it the blocks that are done (zero between calls)
     uint8_t* flag;                         // [tokens]: the row is used
     const ds_scaler* st;
+    float* loss;
+    int32_t* used;
 };
 
 __device__ __forceinline__ int64_t distill_index(const Distill& s, int64_t t, int j)
@@ -66,9 +76,33 @@ __device__ __forceinline__ int64_t distill_index(const Distill& s, int64_t t, in
     return s.wide ? static_cast<const int64_t*>(s.index)[at] : static_cast<const int32_t*>(s.index)[at];
 }
 
-// Which rows are used, and how many: mask, a teacher's entry above -infinity, a
-// logit above -infinity.  A wave has a row and reads on only while it has seen
-// nothing else than -infinity.
+// Whether row t is used (mask, a teacher's entry above -infinity, a logit above
+// -infinity), for the lane's own t (below s.tokens, or the lane has none).  A
+// row's first entry and first logit nearly always say so; the rows where they do
+// not are searched by the wave together.
+template <int ZF>
+__device__ __forceinline__ bool distill_used(const Distill& s, int64_t t, int lane)
+{
+    bool on = t < s.tokens && (s.mask == nullptr || s.mask[t] != 0), open = false;
+    if (on)
+        open = distill_index(s, t, 0) < 0 || load_gate(s.teacher, s.tfmt, t * s.ts) == kNegInf ||
+               load_elem<ZF>(s.logits, t * s.stride) == kNegInf;
+    for (uint64_t left = __ballot(open); left != 0ull; left &= left - 1) {
+        const int of = __ffsll(static_cast<long long>(left)) - 1;
+        const int64_t u = t - lane + of;
+        bool any = false;
+        for (int j = lane; j < s.k; j += 64)
+            any = any || (distill_index(s, u, j) >= 0 && !(load_gate(s.teacher, s.tfmt, u * s.ts + j) == kNegInf));
+        bool found = false;
+        if (__ballot(any) != 0ull)
+            for (int64_t v = lane; v - lane < s.vocab && !found; v += 64)
+                found = __ballot(v < s.vocab && !(load_elem<ZF>(s.logits, u * s.stride + v) == kNegInf)) != 0ull;
+        if (lane == of)
+            on = found;
+    }
+    return on;
+}
+
 constexpr int kUsedBlock = 256;
 template <int ZF>
 __global__ __launch_bounds__(kUsedBlock) void distill_used_kernel(Distill s)
@@ -76,23 +110,13 @@ __global__ __launch_bounds__(kUsedBlock) void distill_used_kernel(Distill s)
     __shared__ int32_t part[kUsedBlock / 64];
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
     int32_t used = 0;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kUsedBlock / 64);
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kUsedBlock / 64) + wave; t < s.tokens; t += step) {
-        bool on = s.mask == nullptr || s.mask[t] != 0;
-        if (on) {
-            bool any = false;
-            for (int j = lane; j < s.k; j += 64)
-                any = any || (distill_index(s, t, j) >= 0 && !(load_gate(s.teacher, s.tfmt, t * s.ts + j) == kNegInf));
-            on = __ballot(any) != 0ull;
-        }
-        if (on) {
-            on = false;
-            for (int64_t v = lane; v - lane < s.vocab && !on; v += 64)
-                on = __ballot(v < s.vocab && !(load_elem<ZF>(s.logits, t * s.stride + v) == kNegInf)) != 0ull;
-        }
-        if (lane == 0)
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kUsedBlock;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kUsedBlock; t0 < s.tokens; t0 += step) {
+        const int64_t t = t0 + threadIdx.x;
+        const bool on = distill_used<ZF>(s, t, lane);
+        if (t < s.tokens)
             s.flag[t] = on;
-        used += on;
+        used += __popcll(__ballot(on));
     }
     if (lane == 0)
         part[wave] = used;
@@ -129,196 +153,337 @@ __device__ __forceinline__ TopSum wave_join(TopSum a, float c)
     return a;
 }
 
-constexpr int kNoVectors = 0;              // NV of the form that reads its row twice
-constexpr int kTwiceUnroll = 4;
+// Sum of exp2((x - top) c) over the vectors and their maximum.  The registers
+// hold the logits as they came; what is widened from them is formed again where
+// it is used, or it would need twice the registers; the scheduler is held to one
+// vector at a time for the same reason.
+template <int ZF, int N>
+__device__ __forceinline__ TopSum distill_vectors(u32x4 (&v)[N], float c)
+{
+    constexpr int kVec = ZF == kF32 ? 4 : 8;
+    float top = kNegInf;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        float x[kVec];
+        widen_vec<ZF>(v[n], x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            top = fmaxf(top, x[i]);
+        asm("" : "+v"(v[n]));
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    const float ref = finite_top(top);
+    float sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        float x[kVec];
+        widen_vec<ZF>(v[n], x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            sum = sum + __builtin_amdgcn_exp2f((x[i] - ref) * c);
+        asm("" : "+v"(v[n]));
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    return {top, sum};
+}
 
-template <int ZF, int BLOCK, int NV, bool GRAD, bool ACC>
+// A row's softmax as the gradient needs it.
+struct DistillRow {
+    float top, log_sum, c, by;             // by: factor of the gradient, NaN where the teacher's entries hold one
+};
+
+__device__ __forceinline__ float distill_p(float x, const DistillRow& r)
+{
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(x - r.top, r.c, -r.log_sum));
+}
+
+// Vector i from `at` on: a base that is the same for the wave and an offset of 32 bits.
+__device__ __forceinline__ u32x4 vector_at(const unsigned char* at, uint32_t i)
+{
+    return reinterpret_cast<const u32x4_any*>(at)[i];
+}
+
+template <int ZF, bool ACC>
+__device__ __forceinline__ void distill_write(unsigned char* out, uint32_t i, u32x4 v, const DistillRow& r, bool on)
+{
+    constexpr int kVec = ZF == kF32 ? 4 : 8;
+    if (!on) {                                                 // a row that is not used
+        reinterpret_cast<u32x4_any*>(out)[i] = u32x4{0, 0, 0, 0};
+        return;
+    }
+    float x[kVec], o[kVec] = {};
+    widen_vec<ZF>(v, x);
+    if constexpr (ACC)
+        widen_vec<ZF>(vector_at(out, i), o);
+#pragma unroll
+    for (int m = 0; m < kVec; ++m)
+        x[m] = ACC ? __builtin_fmaf(r.by, distill_p(x[m], r), o[m]) : r.by * distill_p(x[m], r);
+    reinterpret_cast<u32x4_any*>(out)[i] = narrow_vec<ZF>(x);
+}
+
+constexpr int kTwice = 0;                  // NV of the form that reads its row twice
+constexpr int kTwiceHold = 4;
+
+// Up to so many rows one kernel does the whole call: every block finds all used
+// rows itself, and the last block to end forms the mean.
+constexpr int kFewRows = 256;
+
+// NV vectors a lane hold a row.  A block goes from row to row; while it writes a
+// row's gradient it loads the next row into the registers that this frees, so
+// loads and stores are on their way together.
+template <int ZF, int BLOCK, int NV, bool GRAD, bool ACC, bool FEW>
 __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
 {
     constexpr int ES = ZF == kF32 ? 4 : 2, kVec = 16 / ES, kWaves = BLOCK / 64;
-    constexpr int kTeacher = (DS_MAX_TEACHER_LOGITS + BLOCK - 1) / BLOCK;   // entries per lane, at most
-    constexpr int kHold = NV == kNoVectors ? kTwiceUnroll : NV;
+    constexpr int kHold = NV == kTwice ? kTwiceHold : NV;
+    constexpr uint32_t kNone = ZF == kF32 ? 0xFF800000u : ZF == kBF16 ? 0xFF80FF80u : 0xFC00FC00u;
     __shared__ TopSum of_row[kWaves], of_teacher[kWaves];
     __shared__ float part[kWaves];
-    __shared__ int32_t at[DS_MAX_TEACHER_LOGITS];
-    __shared__ float share[DS_MAX_TEACHER_LOGITS];
-    const int tid = static_cast<int>(threadIdx.x), wave = tid / 64, lane = static_cast<int>(__lane_id());
-    const int64_t vecs = s.vocab / kVec, rest = vecs * kVec;
+    // the entries' places (-1: absent) and their shares, of two rows in turn; a
+    // lane's own: the student's logit there, and what the gradient held there
+    __shared__ __attribute__((aligned(16))) int32_t places[2][DS_MAX_TEACHER_LOGITS];
+    __shared__ float shares[2][DS_MAX_TEACHER_LOGITS];
+    __shared__ float of_logit[DS_MAX_TEACHER_LOGITS];
+    __shared__ float old[ACC ? DS_MAX_TEACHER_LOGITS : 1];
+    __shared__ uint8_t few[FEW ? kFewRows : 1];
+    __shared__ int32_t few_used[FEW ? kWaves : 1];
+    const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(__lane_id());
+    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int vecs = static_cast<int>(s.vocab / kVec);
+    const int64_t rest = static_cast<int64_t>(vecs) * kVec;
+    const int rest_lanes = static_cast<int>(s.vocab - rest);
     const float c = s.c;
-    const int32_t used = *s.count;
+    u32x4 v[kHold];
+    float last = kNegInf;                                      // the lane's one value past the vectors
+    // vector n of row t; `limit`: vecs, or 0 behind the last row
+    auto load_one = [&](int64_t t, int n, int limit) {
+        v[n] = u32x4{kNone, kNone, kNone, kNone};
+        if (n * BLOCK + tid < limit)
+            v[n] = vector_at(s.logits + t * s.stride * ES + n * BLOCK * 16, tid);
+    };
+    // the lane's first entry of row t: its place (past the vocabulary: as it is) and the teacher's logit
+    int64_t place = -1;
+    float theirs_here = kNegInf;
+    auto load_entry = [&](int64_t t) {
+        place = -1;
+        if (tid < s.k && t < s.tokens) {
+            place = distill_index(s, t, tid);
+            theirs_here = load_gate(s.teacher, s.tfmt, t * s.ts + tid);
+        }
+    };
+    load_entry(blockIdx.x);
+    if constexpr (NV != kTwice) {
+        const int limit = blockIdx.x < s.tokens ? vecs : 0;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+            load_one(blockIdx.x, n, limit);
+    }
+    int32_t used = 0;
+    if constexpr (FEW) {
+        int32_t mine = 0;
+        for (int64_t t0 = 0; t0 < s.tokens; t0 += BLOCK) {
+            const bool on = distill_used<ZF>(s, t0 + tid, lane);
+            if (t0 + tid < s.tokens)
+                few[t0 + tid] = on;
+            mine += __popcll(__ballot(on));
+        }
+        if (lane == 0)
+            few_used[wave] = mine;
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w)
+            used += few_used[w];
+    } else {
+        used = *s.count;
+    }
     const float scale = s.st != nullptr ? s.st->scale : 1.0f;
     const float factor = used > 0 ? static_cast<float>(static_cast<double>(scale) * static_cast<double>(s.coef) *
                                                        static_cast<double>(s.tau) / used)
                                   : 0.0f;
-    for (int64_t t = blockIdx.x; t < s.tokens; t += gridDim.x) {
-        const unsigned char* row = s.logits + t * s.stride * ES;
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < s.tokens; t += gridDim.x, turn ^= 1) {
+        const unsigned char* in = s.logits + t * s.stride * ES;
         unsigned char* out = GRAD ? s.grad + t * s.gs * ES : nullptr;
-        const u32x4_any* in = reinterpret_cast<const u32x4_any*>(row);
-        if (s.flag[t] == 0) {                                  // the same for the whole block
-            if (tid == 0)
-                s.token_loss[t] = 0.0f;
-            if constexpr (GRAD && !ACC) {
-                for (int64_t i = tid; i < vecs; i += BLOCK)
-                    reinterpret_cast<u32x4_any*>(out)[i] = u32x4{0, 0, 0, 0};
-                if (rest + tid < s.vocab)
-                    store_elem<ZF>(out, rest + tid, 0.0f);
-            }
-            continue;
-        }
-        u32x4 v[kHold];
-        TopSum mine{kNegInf, 0.0f};
-        constexpr uint32_t kNone = ZF == kF32 ? 0xFF800000u : ZF == kBF16 ? 0xFF80FF80u : 0xFC00FC00u;
-        float last = kNegInf;                                  // the lane's one value past the vectors
-        if (rest + tid < s.vocab)
-            last = load_elem<ZF>(row, rest + tid);
-        for (int64_t i0 = tid; i0 < vecs; i0 += static_cast<int64_t>(kHold) * BLOCK) {
-#pragma unroll
-            for (int n = 0; n < kHold; ++n) {
-                v[n] = u32x4{kNone, kNone, kNone, kNone};
-                if (i0 + n * BLOCK < vecs)
-                    v[n] = in[i0 + n * BLOCK];
-            }
-            float top = kNegInf;
-#pragma unroll
-            for (int n = 0; n < kHold; ++n) {
-                float x[kVec];
-                widen_vec<ZF>(v[n], x);
-#pragma unroll
-                for (int i = 0; i < kVec; ++i)
-                    top = fmaxf(top, x[i]);
-            }
-            const float ref = finite_top(top);
-            float sum = 0.0f;
-#pragma unroll
-            for (int n = 0; n < kHold; ++n) {
-                float x[kVec];
-                widen_vec<ZF>(v[n], x);
-#pragma unroll
-                for (int i = 0; i < kVec; ++i)
-                    sum = sum + __builtin_amdgcn_exp2f((x[i] - ref) * c);
-            }
-            mine = NV == kNoVectors ? join(mine, TopSum{top, sum}, c) : TopSum{top, sum};
-        }
-        if (rest + tid < s.vocab)
-            mine = join(mine, TopSum{last, __builtin_amdgcn_exp2f((last - finite_top(last)) * c)}, c);
-        // the teacher's entries: an absent one is -infinity, one past the vocabulary NaN
-        float entry[kTeacher], of_logit[kTeacher], old[kTeacher];
-        int64_t place[kTeacher];
-        TopSum theirs{kNegInf, 0.0f};
-#pragma unroll
-        for (int n = 0; n < kTeacher; ++n) {
-            const int j = tid + n * BLOCK;
-            entry[n] = kNegInf;
-            of_logit[n] = old[n] = 0.0f;
-            place[n] = -1;
-            if (j < s.k) {
-                place[n] = distill_index(s, t, j);
-                if (place[n] >= 0)
-                    entry[n] = load_gate(s.teacher, s.tfmt, t * s.ts + j);
-                if (place[n] >= s.vocab) {
-                    place[n] = -1;
-                    entry[n] = __builtin_nanf("");
+        const int64_t next = t + gridDim.x;
+        const int next_vecs = next < s.tokens ? vecs : 0;
+        // the same for the whole block
+        const bool on = __builtin_amdgcn_readfirstlane(FEW ? few[t & (kFewRows - 1)] : s.flag[t]) != 0;
+        DistillRow row{0.0f, 0.0f, c, 0.0f};
+        float loss = 0.0f, fine = 1.0f;
+        int here = -1;                                         // the first entry's place, and the rest that is the lane's
+        float logit_here = 0.0f, old_here = 0.0f, share_here = 0.0f;
+        bool first = true, alone = true;                       // of its place: the first entry, the only one
+        int32_t* at = places[turn];
+        float* share = shares[turn];
+        if (on) {
+            TopSum theirs{kNegInf, 0.0f};
+            auto add_entry = [&](int64_t& p, float& x) {       // an absent one is -infinity, one past the vocabulary NaN
+                if (p < 0)
+                    x = kNegInf;
+                if (p >= s.vocab) {
+                    p = -1;
+                    x = __builtin_nanf("");
                 }
-                if (place[n] >= 0) {
-                    of_logit[n] = load_elem<ZF>(row, place[n]);
+                if (!(x == kNegInf))
+                    theirs = join(theirs, TopSum{x, __builtin_amdgcn_exp2f((x - x) * c)}, c);
+            };
+            if (tid < s.k) {
+                add_entry(place, theirs_here);
+                here = static_cast<int>(place);
+                at[tid] = here;
+                if (here >= 0) {                               // used after the row's sums: no wait for it here
+                    logit_here = load_elem<ZF>(in, here);
                     if constexpr (GRAD && ACC)
-                        old[n] = load_elem<ZF>(out, place[n]);
+                        old_here = load_elem<ZF>(out, here);
                 }
-                if (!(entry[n] == kNegInf))
-                    theirs = join(theirs, TopSum{entry[n], __builtin_amdgcn_exp2f((entry[n] - entry[n]) * c)}, c);
-                at[j] = static_cast<int32_t>(place[n]);
             }
-        }
-        mine = wave_join(mine, c);
-        theirs = wave_join(theirs, c);
-        if (lane == 0) {
-            of_row[wave] = mine;
-            of_teacher[wave] = theirs;
-        }
-        __syncthreads();
-        mine = of_row[0];
-        theirs = of_teacher[0];
-        for (int w = 1; w < kWaves; ++w) {
-            mine = join(mine, of_row[w], c);
-            theirs = join(theirs, of_teacher[w], c);
-        }
-        const float log_sum = __builtin_amdgcn_logf(mine.sum), log_theirs = __builtin_amdgcn_logf(theirs.sum);
-        // 1, or NaN where the teacher's entries hold a NaN or +infinity
-        const float fine = theirs.sum / theirs.sum;
-        float loss = 0.0f;
+            if (tid < rest_lanes)
+                last = load_elem<ZF>(in, rest + tid);
+            for (int j = tid + BLOCK; j < s.k; j += BLOCK) {
+                int64_t p = distill_index(s, t, j);
+                float x = load_gate(s.teacher, s.tfmt, t * s.ts + j);
+                add_entry(p, x);
+                at[j] = static_cast<int32_t>(p);
+                share[j] = x;
+                of_logit[j] = p >= 0 ? load_elem<ZF>(in, p) : 0.0f;
+                if constexpr (GRAD && ACC)
+                    old[j] = p >= 0 ? load_elem<ZF>(out, p) : 0.0f;
+            }
+            TopSum mine{kNegInf, 0.0f};
+            if constexpr (NV == kTwice) {
+                for (int i0 = tid; i0 < vecs; i0 += kHold * BLOCK) {
 #pragma unroll
-        for (int n = 0; n < kTeacher; ++n) {
-            const int j = tid + n * BLOCK;
-            if (j < s.k) {
-                const float q = entry[n] == kNegInf
-                                    ? 0.0f
-                                    : __builtin_amdgcn_exp2f((entry[n] - theirs.top) * c - log_theirs);
-                share[j] = q;
+                    for (int n = 0; n < kHold; ++n) {
+                        v[n] = u32x4{kNone, kNone, kNone, kNone};
+                        if (i0 + n * BLOCK < vecs)
+                            v[n] = vector_at(in, i0 + n * BLOCK);
+                    }
+                    mine = join(mine, distill_vectors<ZF>(v, c), c);
+                }
+            } else {
+                mine = distill_vectors<ZF>(v, c);
+            }
+            if (tid < rest_lanes)
+                mine = join(mine, TopSum{last, __builtin_amdgcn_exp2f((last - finite_top(last)) * c)}, c);
+            mine = wave_join(mine, c);
+            if (wave * 64 < s.k)
+                theirs = wave_join(theirs, c);
+            if (lane == 0) {
+                of_row[wave] = mine;
+                of_teacher[wave] = theirs;
+            }
+            __syncthreads();
+            mine = of_row[0];
+            theirs = of_teacher[0];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w)
+                mine = join(mine, of_row[w], c);
+            for (int w = 1; w < kWaves && w * 64 < s.k; ++w)
+                theirs = join(theirs, of_teacher[w], c);
+            const float log_theirs = __builtin_amdgcn_logf(theirs.sum);
+            // 1, or NaN where the teacher's entries hold a NaN or +infinity
+            fine = theirs.sum * __builtin_amdgcn_rcpf(theirs.sum) > 0.0f ? 1.0f : __builtin_nanf("");
+            row.top = mine.top;
+            row.log_sum = __builtin_amdgcn_logf(mine.sum);
+            row.by = factor * fine;
+            auto take_share = [&](float x, int p, float z) {
+                const float q = x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((x - theirs.top) * c - log_theirs);
                 // in natural logarithms: a difference near the type's range does not fit times log2(e)
-                if (q != 0.0f && place[n] >= 0)
-                    loss = loss + q * (((entry[n] - theirs.top) * s.per_tau - log_theirs * kLn2) -
-                                       ((of_logit[n] - mine.top) * s.per_tau - log_sum * kLn2));
-            }
-        }
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            loss += __shfl_xor(loss, off);
-        if (lane == 0)
-            part[wave] = loss;
-        if constexpr (GRAD) {
-            const float by = factor * fine;
-            for (int64_t i0 = tid; i0 < vecs; i0 += static_cast<int64_t>(kHold) * BLOCK) {
-#pragma unroll
-                for (int n = 0; n < kHold; ++n) {
-                    const int64_t i = i0 + n * BLOCK;
-                    if (i < vecs) {
-                        if constexpr (NV == kNoVectors)
-                            v[n] = in[i];
-                        float x[kVec], o[kVec] = {};
-                        widen_vec<ZF>(v[n], x);
-                        if constexpr (ACC)
-                            widen_vec<ZF>(reinterpret_cast<const u32x4_any*>(out)[i], o);
-#pragma unroll
-                        for (int m = 0; m < kVec; ++m)
-                            x[m] = o[m] + by * __builtin_amdgcn_exp2f((x[m] - mine.top) * c - log_sum);
-                        reinterpret_cast<u32x4_any*>(out)[i] = narrow_vec<ZF>(x);
+                if (q != 0.0f && p >= 0)
+                    loss = loss + q * (((x - theirs.top) * s.per_tau - log_theirs * kLn2) -
+                                       ((z - row.top) * s.per_tau - row.log_sum * kLn2));
+                return q;
+            };
+            if (wave * 64 < s.k) {
+                if (tid < s.k) {
+                    share_here = take_share(theirs_here, here, logit_here);
+                    share[tid] = share_here;
+                    if (GRAD && here >= 0) {
+                        for (int i = 0; i < s.k; ++i) {
+                            const bool same = at[i] == here && i != tid;
+                            first = first && !(same && i < tid);
+                            alone = alone && !same;
+                        }
                     }
                 }
+                for (int j = tid + BLOCK; j < s.k; j += BLOCK)
+                    share[j] = take_share(share[j], at[j], of_logit[j]);
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1)
+                    loss += __shfl_xor(loss, off);
             }
-            if (rest + tid < s.vocab) {
-                const float was = ACC ? load_elem<ZF>(out, rest + tid) : 0.0f;
-                store_elem<ZF>(out, rest + tid,
-                               was + by * __builtin_amdgcn_exp2f((last - mine.top) * c - log_sum));
+            if (lane == 0)
+                part[wave] = loss;
+        }
+        load_entry(next);
+        if constexpr (NV == kTwice) {
+            if (GRAD && (on || !ACC))
+#pragma unroll 4
+                for (int i = tid; i < vecs; i += BLOCK)
+                    distill_write<ZF, ACC>(out, i, vector_at(in, i), row, on);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                if (GRAD && (on || !ACC) && n * BLOCK + tid < vecs)
+                    distill_write<ZF, ACC>(out + n * BLOCK * 16, tid, v[n], row, on);
+                load_one(next, n, next_vecs);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        __syncthreads();
+        if (GRAD && (on || !ACC) && tid < rest_lanes) {
+            const float was = ACC ? load_elem<ZF>(out, rest + tid) : 0.0f;
+            store_elem<ZF>(out, rest + tid, on ? __builtin_fmaf(row.by, distill_p(last, row), was) : 0.0f);
+        }
+        if (on)
+            __syncthreads();
         if (tid == 0) {
-            for (int w = 1; w < kWaves; ++w)
+            for (int w = 1; w < kWaves && on; ++w)
                 loss += part[w];
             s.token_loss[t] = s.tau * s.tau * loss * fine;
         }
-        if constexpr (GRAD) {
+        if (GRAD && on && tid < s.k) {
             // where the teacher has entries: written again with their shares, by the first entry of each place
-            const float by = factor * fine;
-#pragma unroll
-            for (int n = 0; n < kTeacher; ++n) {
-                const int j = tid + n * BLOCK;
-                if (j < s.k && place[n] >= 0) {
-                    float q = 0.0f;
-                    bool first = true;
-                    for (int i = 0; i < s.k; ++i)
-                        if (at[i] == static_cast<int32_t>(place[n])) {
-                            first = first && i >= j;
-                            q = q + share[i];
-                        }
-                    if (first) {
-                        const float p = __builtin_amdgcn_exp2f((of_logit[n] - mine.top) * c - log_sum);
-                        store_elem<ZF>(out, place[n], old[n] + by * (p - q));
-                    }
-                }
+            auto rewrite = [&](int p, float q, float z, float was) {
+                store_elem<ZF>(out, p, __builtin_fmaf(row.by, distill_p(z, row) - q, was));
+            };
+            auto total = [&](int p) {
+                float q = 0.0f;
+                for (int i = 0; i < s.k; ++i)
+                    q = at[i] == p ? q + share[i] : q;
+                return q;
+            };
+            if (here >= 0 && first)
+                rewrite(here, alone ? share_here : total(here), logit_here, old_here);
+            for (int j = tid + BLOCK; j < s.k; j += BLOCK) {
+                const int p = at[j];
+                bool lead = p >= 0;
+                for (int i = 0; i < j && lead; ++i)
+                    lead = at[i] != p;
+                if (lead)
+                    rewrite(p, total(p), of_logit[j], ACC ? old[j] : 0.0f);
             }
         }
-        __syncthreads();                                       // the next row's entries
+    }
+    if constexpr (FEW) {
+        __shared__ uint32_t ticket;
+        uint32_t* done = reinterpret_cast<uint32_t*>(s.count) + 1;
+        if (gridDim.x > 1) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0)
+                ticket = atomicAdd(done, 1u);
+            __syncthreads();
+            if (ticket != gridDim.x - 1)
+                return;
+            __threadfence();
+        } else {
+            __syncthreads();
+        }
+        const float mean = rows_mean<BLOCK>(s.token_loss, s.tokens, used, s.coef);
+        if (tid == 0) {
+            *s.loss = mean;
+            *s.used = used;
+            *done = 0;
+        }
     }
 }
 
@@ -330,25 +495,34 @@ uint64_t distill_ws_bytes(int64_t tokens) { return 8 + static_cast<uint64_t>(tok
 
 bool distill_tokens_ok(int64_t tokens) { return tokens >= 0 && tokens <= kBalMaxTokens; }
 
+// Blocks that the GPU holds at once (256 CUs), each with as many rows as the
+// others.
 template <int ZF, int BLOCK, int NV>
-void launch_distill2(unsigned b, hipStream_t st, const Distill& s, bool accumulate)
+void launch_distill2(int per_cu, hipStream_t st, const Distill& s, bool accumulate)
 {
-    if (s.grad == nullptr) distill_kernel<ZF, BLOCK, NV, false, false><<<b, BLOCK, 0, st>>>(s);
-    else if (accumulate)   distill_kernel<ZF, BLOCK, NV, true, true><<<b, BLOCK, 0, st>>>(s);
-    else                   distill_kernel<ZF, BLOCK, NV, true, false><<<b, BLOCK, 0, st>>>(s);
+    const int64_t most = 256 * static_cast<int64_t>(per_cu), turns = (s.tokens + most - 1) / most;
+    const unsigned b = grid_blocks((s.tokens + turns - 1) / turns, BLOCK);
+    if (s.tokens <= kFewRows) {
+        if (s.grad == nullptr) distill_kernel<ZF, BLOCK, NV, false, false, true><<<b, BLOCK, 0, st>>>(s);
+        else if (accumulate)   distill_kernel<ZF, BLOCK, NV, true, true, true><<<b, BLOCK, 0, st>>>(s);
+        else                   distill_kernel<ZF, BLOCK, NV, true, false, true><<<b, BLOCK, 0, st>>>(s);
+    } else {
+        if (s.grad == nullptr) distill_kernel<ZF, BLOCK, NV, false, false, false><<<b, BLOCK, 0, st>>>(s);
+        else if (accumulate)   distill_kernel<ZF, BLOCK, NV, true, true, false><<<b, BLOCK, 0, st>>>(s);
+        else                   distill_kernel<ZF, BLOCK, NV, true, false, false><<<b, BLOCK, 0, st>>>(s);
+    }
 }
 
 template <int ZF>
 void launch_distill(hipStream_t st, const Distill& s, bool accumulate)
 {
     const int64_t vecs = s.vocab / (ZF == kF32 ? 4 : 8);
-    const unsigned b = grid_blocks(s.tokens, 1024);
-    if (vecs <= 256)        launch_distill2<ZF, 256, 1>(b, st, s, accumulate);
-    else if (vecs <= 1024)  launch_distill2<ZF, 256, 4>(b, st, s, accumulate);
-    else if (vecs <= 4096)  launch_distill2<ZF, 512, 8>(b, st, s, accumulate);
-    else if (vecs <= 8192)  launch_distill2<ZF, 1024, 8>(b, st, s, accumulate);
-    else if (vecs <= 16384) launch_distill2<ZF, 1024, 16>(b, st, s, accumulate);
-    else                    launch_distill2<ZF, 1024, kNoVectors>(b, st, s, accumulate);
+    if (vecs <= 256)        launch_distill2<ZF, 64, 4>(12, st, s, accumulate);
+    else if (vecs <= 1024)  launch_distill2<ZF, 256, 4>(6, st, s, accumulate);
+    else if (vecs <= 4096)  launch_distill2<ZF, 512, 8>(3, st, s, accumulate);
+    else if (vecs <= 8192)  launch_distill2<ZF, 1024, 8>(1, st, s, accumulate);
+    else if (vecs <= 16384) launch_distill2<ZF, 1024, 16>(1, st, s, accumulate);
+    else                    launch_distill2<ZF, 1024, kTwice>(1, st, s, accumulate);
 }
 
 ds_status distill_loss(const ds_scaler* st, const void* logits, ds_dtype dt, int64_t tokens, int64_t vocab, int64_t stride,
@@ -391,19 +565,23 @@ ds_status distill_loss(const ds_scaler* st, const void* logits, ds_dtype dt, int
     const Distill s{static_cast<const unsigned char*>(logits), tokens, vocab, stride, teacher, index, ts, is, k, fmt_of(tdt),
                     index_bytes == 8, mask, static_cast<float>(1.44269504088896340736 / static_cast<double>(temperature)),
                     temperature, 1.0f / temperature, coef, token_loss, static_cast<unsigned char*>(grad), gs, static_cast<int32_t*>(ws),
-                    static_cast<uint8_t*>(ws) + 8, st};
-    if (tokens > 0) {
-        const unsigned b = grid_blocks((tokens + kUsedBlock / 64 - 1) / (kUsedBlock / 64), kUsedBlock);
+                    static_cast<uint8_t*>(ws) + 8, st, loss, used};
+    if (tokens > kFewRows) {
+        const unsigned b = grid_blocks((tokens + kUsedBlock - 1) / kUsedBlock, kUsedBlock);
         if (dt == DS_FP16)      distill_used_kernel<kF16><<<b, kUsedBlock, 0, stream>>>(s);
         else if (dt == DS_BF16) distill_used_kernel<kBF16><<<b, kUsedBlock, 0, stream>>>(s);
         else                    distill_used_kernel<kF32><<<b, kUsedBlock, 0, stream>>>(s);
         if (launched() != DS_OK)
             return DS_ERR_HIP;
+    }
+    if (tokens > 0) {
         if (dt == DS_FP16)      launch_distill<kF16>(stream, s, accumulate);
         else if (dt == DS_BF16) launch_distill<kBF16>(stream, s, accumulate);
         else                    launch_distill<kF32>(stream, s, accumulate);
         if (launched() != DS_OK)
             return DS_ERR_HIP;
+        if (tokens <= kFewRows)
+            return DS_OK;
     }
     rows_mean_kernel<<<1, kMeanBlock, 0, stream>>>(token_loss, tokens, s.count, coef, loss, used, 1);
     return launched();
