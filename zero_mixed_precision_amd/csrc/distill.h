@@ -153,43 +153,39 @@ __device__ __forceinline__ TopSum wave_join(TopSum a, float c)
     return a;
 }
 
-// Sum of exp2((x - top) c) over the vectors and their maximum.  The registers
-// hold the logits as they came; what is widened from them is formed again where
-// it is used, or it would need twice the registers; the scheduler is held to one
-// vector at a time for the same reason.
-template <int ZF, int N>
-__device__ __forceinline__ TopSum distill_vectors(u32x4 (&v)[N], float c)
+template <int ZF>
+__device__ __forceinline__ float top_of(u32x4 v)
 {
-    constexpr int kVec = ZF == kF32 ? 4 : 8;
-    float top = kNegInf;
+    float x[ZF == kF32 ? 4 : 8], top = kNegInf;
+    widen_vec<ZF>(v, x);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        float x[kVec];
-        widen_vec<ZF>(v[n], x);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            top = fmaxf(top, x[i]);
-        asm("" : "+v"(v[n]));
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    const float ref = finite_top(top);
-    float sum = 0.0f;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        float x[kVec];
-        widen_vec<ZF>(v[n], x);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            sum = sum + __builtin_amdgcn_exp2f((x[i] - ref) * c);
-        asm("" : "+v"(v[n]));
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    return {top, sum};
+    for (int i = 0; i < (ZF == kF32 ? 4 : 8); ++i)
+        top = fmaxf(top, x[i]);
+    return top;
 }
 
-// A row's softmax as the gradient needs it.
+__device__ __forceinline__ float wave_max(float x)
+{
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        x = fmaxf(x, __shfl_xor(x, off));
+    return x;
+}
+
+__device__ __forceinline__ float wave_sum(float x)
+{
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        x += __shfl_xor(x, off);
+    return x;
+}
+
+// A row's softmax as the gradient needs it: p = 2^(c x - ref) / sum, or, where
+// `exact`, 2^((x - top) c - log2 sum).  `by` is the gradient's factor, NaN where
+// the teacher's entries hold a NaN, `by_sum` that over the sum.
 struct DistillRow {
-    float top, log_sum, c, by;             // by: factor of the gradient, NaN where the teacher's entries hold one
+    float top, c, ref, log_sum, by, by_sum;
+    bool exact;
 };
 
 __device__ __forceinline__ float distill_p(float x, const DistillRow& r)
@@ -215,9 +211,17 @@ __device__ __forceinline__ void distill_write(unsigned char* out, uint32_t i, u3
     widen_vec<ZF>(v, x);
     if constexpr (ACC)
         widen_vec<ZF>(vector_at(out, i), o);
+    if (r.exact) {
 #pragma unroll
-    for (int m = 0; m < kVec; ++m)
-        x[m] = ACC ? __builtin_fmaf(r.by, distill_p(x[m], r), o[m]) : r.by * distill_p(x[m], r);
+        for (int m = 0; m < kVec; ++m)
+            x[m] = __builtin_fmaf(r.by, distill_p(x[m], r), o[m]);
+    } else {
+#pragma unroll
+        for (int m = 0; m < kVec; ++m) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[m], r.c, -r.ref));
+            x[m] = ACC ? __builtin_fmaf(r.by_sum, e, o[m]) : r.by_sum * e;
+        }
+    }
     reinterpret_cast<u32x4_any*>(out)[i] = narrow_vec<ZF>(x);
 }
 
@@ -228,9 +232,19 @@ constexpr int kTwiceHold = 4;
 // rows itself, and the last block to end forms the mean.
 constexpr int kFewRows = 256;
 
-// NV vectors a lane hold a row.  A block goes from row to row; while it writes a
-// row's gradient it loads the next row into the registers that this frees, so
-// loads and stores are on their way together.
+// NV vectors a lane hold a row, as they came: what is widened from them is formed
+// again where it is used, or it would need twice the registers, and the scheduler
+// is held to one vector at a time for the same reason.  A block goes from row to
+// row; while it writes a row's gradient it loads the next row into the registers
+// that this frees, so loads and stores are on their way together.
+//
+// The sum needs no maximum, only a reference that no logit exceeds by far: a
+// wave takes the largest of its first vectors.  With ref = c top rounded, 2^(c x
+// - ref) is one fused operation and an exponential, and as exact as from the
+// difference.  Where the sum says that the reference was none (nothing but
+// -infinity in the first vectors, a logit 2^64 times as likely as the reference,
+// values near the type's range, NaN), the row is summed again from its maximum,
+// differences first.
 template <int ZF, int BLOCK, int NV, bool GRAD, bool ACC, bool FEW>
 __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
 {
@@ -307,7 +321,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
         const int next_vecs = next < s.tokens ? vecs : 0;
         // the same for the whole block
         const bool on = __builtin_amdgcn_readfirstlane(FEW ? few[t & (kFewRows - 1)] : s.flag[t]) != 0;
-        DistillRow row{0.0f, 0.0f, c, 0.0f};
+        DistillRow row{0.0f, c, 0.0f, 0.0f, 0.0f, 0.0f, false};
         float loss = 0.0f, fine = 1.0f;
         int here = -1;                                         // the first entry's place, and the rest that is the lane's
         float logit_here = 0.0f, old_here = 0.0f, share_here = 0.0f;
@@ -348,43 +362,103 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
                 if constexpr (GRAD && ACC)
                     old[j] = p >= 0 ? load_elem<ZF>(out, p) : 0.0f;
             }
-            TopSum mine{kNegInf, 0.0f};
-            if constexpr (NV == kTwice) {
-                for (int i0 = tid; i0 < vecs; i0 += kHold * BLOCK) {
+            // f(vector) for every vector of the lane
+            auto each = [&](auto f) {
+                if constexpr (NV == kTwice) {
+                    for (int i0 = tid; i0 < vecs; i0 += kHold * BLOCK) {
 #pragma unroll
-                    for (int n = 0; n < kHold; ++n) {
-                        v[n] = u32x4{kNone, kNone, kNone, kNone};
-                        if (i0 + n * BLOCK < vecs)
-                            v[n] = vector_at(in, i0 + n * BLOCK);
+                        for (int n = 0; n < kHold; ++n) {
+                            v[n] = u32x4{kNone, kNone, kNone, kNone};
+                            if (i0 + n * BLOCK < vecs)
+                                v[n] = vector_at(in, i0 + n * BLOCK);
+                        }
+#pragma unroll
+                        for (int n = 0; n < kHold; ++n)
+                            f(v[n]);
                     }
-                    mine = join(mine, distill_vectors<ZF>(v, c), c);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) {
+                        f(v[n]);
+                        asm("" : "+v"(v[n]));
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
-            } else {
-                mine = distill_vectors<ZF>(v, c);
+            };
+            const float mine = tid < rest_lanes ? last : kNegInf;
+            u32x4 head = v[0];
+            if constexpr (NV == kTwice) {
+                head = u32x4{kNone, kNone, kNone, kNone};
+                if (tid < vecs)
+                    head = vector_at(in, tid);
             }
-            if (tid < rest_lanes)
-                mine = join(mine, TopSum{last, __builtin_amdgcn_exp2f((last - finite_top(last)) * c)}, c);
-            mine = wave_join(mine, c);
+            const float top = wave_max(fmaxf(top_of<ZF>(head), mine)), ref = top * c;
+            float sum = __builtin_amdgcn_exp2f(__builtin_fmaf(mine, c, -ref));
+            each([&](u32x4 vec) {
+                float x[kVec];
+                widen_vec<ZF>(vec, x);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    sum = sum + __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -ref));
+            });
+            sum = wave_sum(sum);
             if (wave * 64 < s.k)
                 theirs = wave_join(theirs, c);
             if (lane == 0) {
-                of_row[wave] = mine;
+                const bool some = wave * 64 < vecs || wave * 64 < rest_lanes;
+                of_row[wave] = some ? TopSum{top, sum} : TopSum{kNegInf, 0.0f};
                 of_teacher[wave] = theirs;
             }
             __syncthreads();
-            mine = of_row[0];
-            theirs = of_teacher[0];
+            row.top = of_row[0].top;
 #pragma unroll
             for (int w = 1; w < kWaves; ++w)
-                mine = join(mine, of_row[w], c);
+                row.top = fmaxf(row.top, of_row[w].top);
+            row.ref = row.top * c;
+            float total_sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                total_sum += of_row[w].top == kNegInf ? of_row[w].sum
+                                                      : of_row[w].sum * __builtin_amdgcn_exp2f(of_row[w].top * c - row.ref);
+            row.exact = !(total_sum >= 0.5f && total_sum <= 0x1p64f && fabsf(row.ref) <= 0x1p126f);
+            theirs = of_teacher[0];
             for (int w = 1; w < kWaves && w * 64 < s.k; ++w)
                 theirs = join(theirs, of_teacher[w], c);
+            if (row.exact) {
+                float most = mine;
+                each([&](u32x4 vec) { most = fmaxf(most, top_of<ZF>(vec)); });
+                most = wave_max(most);
+                __syncthreads();                               // the sums above have been read
+                if (lane == 0)
+                    of_row[wave].top = most;
+                __syncthreads();
+                for (int w = 0; w < kWaves; ++w)
+                    most = fmaxf(most, of_row[w].top);
+                sum = __builtin_amdgcn_exp2f((mine - most) * c);
+                each([&](u32x4 vec) {
+                    float x[kVec];
+                    widen_vec<ZF>(vec, x);
+                    for (int i = 0; i < kVec; ++i)
+                        sum = sum + __builtin_amdgcn_exp2f((x[i] - most) * c);
+                });
+                sum = wave_sum(sum);
+                if (lane == 0)
+                    of_row[wave].sum = sum;
+                __syncthreads();
+                total_sum = 0.0f;
+                for (int w = 0; w < kWaves; ++w)
+                    total_sum += of_row[w].sum;
+                row.top = most;
+            }
+            row.log_sum = __builtin_amdgcn_logf(total_sum);
             const float log_theirs = __builtin_amdgcn_logf(theirs.sum);
             // 1, or NaN where the teacher's entries hold a NaN or +infinity
             fine = theirs.sum * __builtin_amdgcn_rcpf(theirs.sum) > 0.0f ? 1.0f : __builtin_nanf("");
-            row.top = mine.top;
-            row.log_sum = __builtin_amdgcn_logf(mine.sum);
             row.by = factor * fine;
+            row.by_sum = row.by / total_sum;
+            // what the reference's rounding has added to the sum's logarithm
+            if (!row.exact)
+                row.log_sum -= __builtin_fmaf(row.top, c, -row.ref);
             auto take_share = [&](float x, int p, float z) {
                 const float q = x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((x - theirs.top) * c - log_theirs);
                 // in natural logarithms: a difference near the type's range does not fit times log2(e)
@@ -519,7 +593,7 @@ void launch_distill(hipStream_t st, const Distill& s, bool accumulate)
     const int64_t vecs = s.vocab / (ZF == kF32 ? 4 : 8);
     if (vecs <= 256)        launch_distill2<ZF, 64, 4>(12, st, s, accumulate);
     else if (vecs <= 1024)  launch_distill2<ZF, 256, 4>(6, st, s, accumulate);
-    else if (vecs <= 4096)  launch_distill2<ZF, 512, 8>(3, st, s, accumulate);
+    else if (vecs <= 4096)  launch_distill2<ZF, 512, 8>(2, st, s, accumulate);
     else if (vecs <= 8192)  launch_distill2<ZF, 1024, 8>(1, st, s, accumulate);
     else if (vecs <= 16384) launch_distill2<ZF, 1024, 16>(1, st, s, accumulate);
     else                    launch_distill2<ZF, 1024, kTwice>(1, st, s, accumulate);
