@@ -203,10 +203,6 @@ template <int ZF, bool ACC>
 __device__ __forceinline__ void distill_write(unsigned char* out, uint32_t i, u32x4 v, const DistillRow& r, bool on)
 {
     constexpr int kVec = ZF == kF32 ? 4 : 8;
-    if (!on) {                                                 // a row that is not used
-        reinterpret_cast<u32x4_any*>(out)[i] = u32x4{0, 0, 0, 0};
-        return;
-    }
     float x[kVec], o[kVec] = {};
     widen_vec<ZF>(v, x);
     if constexpr (ACC)
@@ -222,7 +218,11 @@ __device__ __forceinline__ void distill_write(unsigned char* out, uint32_t i, u3
             x[m] = ACC ? __builtin_fmaf(r.by_sum, e, o[m]) : r.by_sum * e;
         }
     }
-    reinterpret_cast<u32x4_any*>(out)[i] = narrow_vec<ZF>(x);
+    v = narrow_vec<ZF>(x);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+        v[m] = on ? v[m] : 0u;                                 // a row that is not used
+    reinterpret_cast<u32x4_any*>(out)[i] = v;
 }
 
 constexpr int kTwice = 0;                  // NV of the form that reads its row twice
@@ -236,7 +236,10 @@ constexpr int kFewRows = 256;
 // again where it is used, or it would need twice the registers, and the scheduler
 // is held to one vector at a time for the same reason.  A block goes from row to
 // row; while it writes a row's gradient it loads the next row into the registers
-// that this frees, so loads and stores are on their way together.
+// that this frees, so loads and stores are on their way together, and sums the
+// first vectors while the last are still coming.  For that, the wait for a vector
+// must be able to count the loads behind it: none of them is conditional, lanes
+// past the row's end read and write its last vector with the others.
 //
 // The sum needs no maximum, only a reference that no logit exceeds by far: a
 // wave takes the largest of its first vectors.  With ref = c top rounded, 2^(c x
@@ -250,8 +253,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
 {
     constexpr int ES = ZF == kF32 ? 4 : 2, kVec = 16 / ES, kWaves = BLOCK / 64;
     constexpr int kHold = NV == kTwice ? kTwiceHold : NV;
-    constexpr uint32_t kNone = ZF == kF32 ? 0xFF800000u : ZF == kBF16 ? 0xFF80FF80u : 0xFC00FC00u;
-    __shared__ TopSum of_row[kWaves], of_teacher[kWaves];
+        __shared__ TopSum of_row[kWaves], of_teacher[kWaves];
     __shared__ float part[kWaves];
     // the entries' places (-1: absent) and their shares, of two rows in turn; a
     // lane's own: the student's logit there, and what the gradient held there
@@ -268,29 +270,35 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
     const int rest_lanes = static_cast<int>(s.vocab - rest);
     const float c = s.c;
     u32x4 v[kHold];
-    float last = kNegInf;                                      // the lane's one value past the vectors
-    // vector n of row t; `limit`: vecs, or 0 behind the last row
-    auto load_one = [&](int64_t t, int n, int limit) {
-        v[n] = u32x4{kNone, kNone, kNone, kNone};
-        if (n * BLOCK + tid < limit)
-            v[n] = vector_at(s.logits + t * s.stride * ES + n * BLOCK * 16, tid);
+    // where the lane's vector n starts, from a row's first byte: the wave's part and the lane's vectors behind it
+    auto part_of = [&](int n) { return min(n * BLOCK, vecs - 1); };
+    auto lane_of = [&](int n) {
+        int own = tid;
+        asm volatile("" : "+v"(own));                          // formed where it is used: NV of them take too many registers
+        return min(own, vecs - 1 - part_of(n));
     };
-    // the lane's first entry of row t: its place (past the vocabulary: as it is) and the teacher's logit
+    auto load_one = [&](int64_t t, int n) { v[n] = vector_at(s.logits + t * s.stride * ES + part_of(n) * 16, lane_of(n)); };
+    // what comes before a row's vectors: the lane's first entry (its place, past the vocabulary as it is, and the
+    // teacher's logit), its one value past the vectors, whether the row is used
     int64_t place = -1;
-    float theirs_here = kNegInf;
+    float theirs_here = kNegInf, last = kNegInf;
+    uint32_t flag = 0;
     auto load_entry = [&](int64_t t) {
         place = -1;
-        if (tid < s.k && t < s.tokens) {
+        if (tid < s.k) {
             place = distill_index(s, t, tid);
             theirs_here = load_gate(s.teacher, s.tfmt, t * s.ts + tid);
         }
+        if (tid < rest_lanes)
+            last = load_elem<ZF>(s.logits, t * s.stride + rest + tid);
+        if constexpr (!FEW)
+            flag = s.flag[t];
     };
-    load_entry(blockIdx.x);
+    load_entry(min(static_cast<int64_t>(blockIdx.x), s.tokens - 1));
     if constexpr (NV != kTwice) {
-        const int limit = blockIdx.x < s.tokens ? vecs : 0;
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            load_one(blockIdx.x, n, limit);
+            load_one(min(static_cast<int64_t>(blockIdx.x), s.tokens - 1), n);
     }
     int32_t used = 0;
     if constexpr (FEW) {
@@ -317,10 +325,10 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
     for (int64_t t = blockIdx.x; t < s.tokens; t += gridDim.x, turn ^= 1) {
         const unsigned char* in = s.logits + t * s.stride * ES;
         unsigned char* out = GRAD ? s.grad + t * s.gs * ES : nullptr;
-        const int64_t next = t + gridDim.x;
-        const int next_vecs = next < s.tokens ? vecs : 0;
+        const int64_t next = min(t + gridDim.x, s.tokens - 1);
         // the same for the whole block
-        const bool on = __builtin_amdgcn_readfirstlane(FEW ? few[t & (kFewRows - 1)] : s.flag[t]) != 0;
+        const bool on = __builtin_amdgcn_readfirstlane(FEW ? few[t & (kFewRows - 1)] : flag) != 0;
+        const float mine = last;
         DistillRow row{0.0f, c, 0.0f, 0.0f, 0.0f, 0.0f, false};
         float loss = 0.0f, fine = 1.0f;
         int here = -1;                                         // the first entry's place, and the rest that is the lane's
@@ -350,8 +358,6 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
                         old_here = load_elem<ZF>(out, here);
                 }
             }
-            if (tid < rest_lanes)
-                last = load_elem<ZF>(in, rest + tid);
             for (int j = tid + BLOCK; j < s.k; j += BLOCK) {
                 int64_t p = distill_index(s, t, j);
                 float x = load_gate(s.teacher, s.tfmt, t * s.ts + j);
@@ -362,44 +368,45 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
                 if constexpr (GRAD && ACC)
                     old[j] = p >= 0 ? load_elem<ZF>(out, p) : 0.0f;
             }
-            // f(vector) for every vector of the lane
+            // f(vector, whether the lane has it) for every vector
             auto each = [&](auto f) {
                 if constexpr (NV == kTwice) {
                     for (int i0 = tid; i0 < vecs; i0 += kHold * BLOCK) {
 #pragma unroll
-                        for (int n = 0; n < kHold; ++n) {
-                            v[n] = u32x4{kNone, kNone, kNone, kNone};
-                            if (i0 + n * BLOCK < vecs)
-                                v[n] = vector_at(in, i0 + n * BLOCK);
-                        }
+                        for (int n = 0; n < kHold; ++n)
+                            v[n] = vector_at(in, min(i0 + n * BLOCK, vecs - 1));
 #pragma unroll
                         for (int n = 0; n < kHold; ++n)
-                            f(v[n]);
+                            f(v[n], i0 + n * BLOCK < vecs);
                     }
                 } else {
 #pragma unroll
                     for (int n = 0; n < NV; ++n) {
-                        f(v[n]);
+                        int own = tid;
+                        asm volatile("" : "+v"(own));
+                        f(v[n], own < vecs - n * BLOCK);
                         asm("" : "+v"(v[n]));
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             };
-            const float mine = tid < rest_lanes ? last : kNegInf;
-            u32x4 head = v[0];
+            float top = mine;
             if constexpr (NV == kTwice) {
-                head = u32x4{kNone, kNone, kNone, kNone};
                 if (tid < vecs)
-                    head = vector_at(in, tid);
+                    top = fmaxf(top, top_of<ZF>(vector_at(in, tid)));
+            } else {
+                top = fmaxf(top, tid < vecs ? top_of<ZF>(v[0]) : kNegInf);
             }
-            const float top = wave_max(fmaxf(top_of<ZF>(head), mine)), ref = top * c;
+            top = wave_max(top);
+            const float ref = top * c;
             float sum = __builtin_amdgcn_exp2f(__builtin_fmaf(mine, c, -ref));
-            each([&](u32x4 vec) {
-                float x[kVec];
+            each([&](u32x4 vec, bool has) {
+                float x[kVec], of_vec = 0.0f;
                 widen_vec<ZF>(vec, x);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
-                    sum = sum + __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -ref));
+                    of_vec = of_vec + __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -ref));
+                sum = sum + (has ? of_vec : 0.0f);
             });
             sum = wave_sum(sum);
             if (wave * 64 < s.k)
@@ -426,7 +433,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
                 theirs = join(theirs, of_teacher[w], c);
             if (row.exact) {
                 float most = mine;
-                each([&](u32x4 vec) { most = fmaxf(most, top_of<ZF>(vec)); });
+                each([&](u32x4 vec, bool) { most = fmaxf(most, top_of<ZF>(vec)); });
                 most = wave_max(most);
                 __syncthreads();                               // the sums above have been read
                 if (lane == 0)
@@ -435,11 +442,11 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
                 for (int w = 0; w < kWaves; ++w)
                     most = fmaxf(most, of_row[w].top);
                 sum = __builtin_amdgcn_exp2f((mine - most) * c);
-                each([&](u32x4 vec) {
+                each([&](u32x4 vec, bool has) {
                     float x[kVec];
                     widen_vec<ZF>(vec, x);
                     for (int i = 0; i < kVec; ++i)
-                        sum = sum + __builtin_amdgcn_exp2f((x[i] - most) * c);
+                        sum = sum + (has ? __builtin_amdgcn_exp2f((x[i] - most) * c) : 0.0f);
                 });
                 sum = wave_sum(sum);
                 if (lane == 0)
@@ -497,15 +504,19 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
         } else {
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
-                if (GRAD && (on || !ACC) && n * BLOCK + tid < vecs)
-                    distill_write<ZF, ACC>(out + n * BLOCK * 16, tid, v[n], row, on);
-                load_one(next, n, next_vecs);
+                if constexpr (GRAD && ACC) {                   // added to: by one lane only
+                    if (on && n * BLOCK + tid < vecs)
+                        distill_write<ZF, ACC>(out + n * BLOCK * 16, tid, v[n], row, on);
+                } else if constexpr (GRAD) {
+                    distill_write<ZF, ACC>(out + part_of(n) * 16, lane_of(n), v[n], row, on);
+                }
+                load_one(next, n);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (GRAD && (on || !ACC) && tid < rest_lanes) {
             const float was = ACC ? load_elem<ZF>(out, rest + tid) : 0.0f;
-            store_elem<ZF>(out, rest + tid, on ? __builtin_fmaf(row.by, distill_p(last, row), was) : 0.0f);
+            store_elem<ZF>(out, rest + tid, on ? __builtin_fmaf(row.by, distill_p(mine, row), was) : 0.0f);
         }
         if (on)
             __syncthreads();
@@ -591,7 +602,8 @@ template <int ZF>
 void launch_distill(hipStream_t st, const Distill& s, bool accumulate)
 {
     const int64_t vecs = s.vocab / (ZF == kF32 ? 4 : 8);
-    if (vecs <= 256)        launch_distill2<ZF, 64, 4>(12, st, s, accumulate);
+    if (vecs < 1)           launch_distill2<ZF, 64, kTwice>(8, st, s, accumulate);
+    else if (vecs <= 256)   launch_distill2<ZF, 64, 4>(12, st, s, accumulate);
     else if (vecs <= 1024)  launch_distill2<ZF, 256, 4>(6, st, s, accumulate);
     else if (vecs <= 4096)  launch_distill2<ZF, 512, 8>(2, st, s, accumulate);
     else if (vecs <= 8192)  launch_distill2<ZF, 1024, 8>(1, st, s, accumulate);
