@@ -115,7 +115,9 @@ def inputs(T, V, D, kind, seed=0, index=torch.int64):
 
 SIZES = [(1, 1, 1), (1, 2, 64), (2, 16, 8), (16, 1000, 64), (5, 129, 63), (64, 128, 128), (65, 257, 65), (127, 255, 192),
          (128, 256, 256), (129, 300, 250), (200, 5000, 100), (1, 32000, 512), (33, 10007, 333), (300, 513, 1000),
-         (513, 777, 520), (1000, 2000, 40), (2, 70001, 24), (700, 1024, 2048)]
+         (513, 777, 520), (1000, 2000, 40), (2, 70001, 24), (700, 1024, 2048),
+         # sums split into parts: over the vocabulary, over the tokens, over both and over pieces
+         (3, 20000, 40), (3000, 20, 10), (2500, 9000, 33), (130, 65537, 64), (2049, 300, 16), (4100, 129, 200)]
 
 
 @pytest.mark.parametrize("kind", ["fp16", "bf16"])
@@ -150,8 +152,8 @@ def test_rows_that_are_left_out(T, V, D, kind):
 
 @pytest.mark.parametrize("kind,dtype", [("fp16", torch.float32), ("bf16", torch.float32), ("bf16", torch.bfloat16),
                                         ("fp16", torch.float16)])
-def test_weight_gradients_add_up(kind, dtype):
-    T, V, D = 130, 700, 200
+@pytest.mark.parametrize("T,V,D", [(130, 700, 200), (3000, 20, 10)])
+def test_weight_gradients_add_up(T, V, D, kind, dtype):
     op = VocabCrossEntropy(V, D, T, TYPES[kind])
     x, w, y = inputs(T, V, D, kind)
     check(op, x, w, y, dtype=dtype)
@@ -265,10 +267,10 @@ def test_gradient_against_differences():
         assert abs((moved[0] - moved[1]) / (2 * h) - float(d[at])) <= bound
 
 
-def test_sizes_in_turn_and_no_tokens():
-    V, D = 300, 72
-    op = VocabCrossEntropy(V, D, 260, torch.float16)
-    for T in (260, 1, 0, 17, 259):
+@pytest.mark.parametrize("V,D,sizes", [(300, 72, (260, 1, 0, 17, 259)), (40000, 24, (9000, 2, 300, 2100))])
+def test_sizes_in_turn_and_no_tokens(V, D, sizes):
+    op = VocabCrossEntropy(V, D, max(sizes), torch.float16)
+    for T in sizes:
         x, w, y = inputs(max(T, 1), V, D, "fp16", seed=T)
         check(op, x[:T], w, y[:T])
 

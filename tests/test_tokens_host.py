@@ -152,6 +152,9 @@ def test_workspace_bytes():
     f = _lib.ds_vocab_ce_workspace_bytes
     assert f(-1, 8, 8) == 0 and f(8, 0, 8) == 0 and f(8, 8, 0) == 0 and f(8, 8, 65537) == 0 and f(1 << 25, 8, 8) == 0
     assert 0 < f(0, 1, 1) <= f(256, 1, 1) < f(257, 1, 1)
+    for V, D in ((1, 1), (500, 64), (32000, 100), (131072, 4096), (1 << 24, 8)):    # what serves many tokens serves fewer
+        sizes = [f(t, V, D) for t in (1, 100, 256, 1000, 4096, 5000, 8192, 16000, 40000, 65536, 131072, 131073, 1 << 20)]
+        assert sizes == sorted(sizes)
     # a piece's dz, not the vocabulary's, and no more of the weight than that
     assert f(8192, 131072, 4096) < 2 * 8192 * 131072
 

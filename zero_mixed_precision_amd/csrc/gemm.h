@@ -68,8 +68,9 @@ struct TileOf {
     static constexpr int kRowBytes = COLS ? BR * 2 : kBK * 2;
     static constexpr int kPieces = kRowBytes / 16;             // per row in LDS
 
-    // The permutation of a row's pieces.
-    static __device__ __forceinline__ int mix(int row) { return COLS ? (row & 3) << 1 : row & 7; }
+    // The permutation of a row's pieces: 16 lanes that read one after another
+    // meet all 64 banks (no conflict counted in either form).
+    static __device__ __forceinline__ int mix(int row) { return COLS ? (row & 3) << 2 : (row >> 1) & 7; }
 
     uint32_t voff[kLoads];
 
@@ -171,30 +172,45 @@ struct Product {
             pa += AC ? kBK * a.stride : kBK;
             pb += BC ? kBK * b.stride : kBK;
         };
-        if (ktiles > 0)
-            load(0, 0);
-        uint32_t now = 0;
-        for (int kt = 0; kt < ktiles; ++kt) {
-            loads_done();
-            __syncthreads();
-            if (kt + 1 < ktiles)
-                load(kt + 1, now ^ kStage);
-            const unsigned char* la = lds + now;
+        if (ktiles <= 0)
+            return;
+        load(0, 0);
+        loads_done();
+        __syncthreads();
+        if (ktiles > 1)
+            load(1, kStage);
+        u32x4 fa[2][MI], fb[2][NI];
+        auto read = [&](uint32_t stage, int kk, int to) {
+            const unsigned char* la = lds + stage;
             const unsigned char* lb = la + TA::kBytes;
 #pragma unroll
+            for (int i = 0; i < MI; ++i)
+                fa[to][i] = TA::frag(la, wm, i, kk, lane);
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                fb[to][j] = TB::frag(lb, wn, j, kk, lane);
+        };
+        read(0, 0, 0);
+        uint32_t now = 0;
+        for (int kt = 0; kt < ktiles; ++kt) {
+#pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk) {
-                u32x4 fa[MI], fb[NI];
-#pragma unroll
-                for (int i = 0; i < MI; ++i)
-                    fa[i] = TA::frag(la, wm, i, kk, lane);
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-                    fb[j] = TB::frag(lb, wn, j, kk, lane);
+                // the next fragments, while the matrix cores have the last ones; behind a tile's last, all waves
+                // have read it, and its place takes the tile after the next
+                if (kk + 1 < kBK / 16) {
+                    read(now, kk + 1, (kk + 1) & 1);
+                } else if (kt + 1 < ktiles) {
+                    loads_done();
+                    __syncthreads();
+                    if (kt + 2 < ktiles)
+                        load(kt + 2, now);
+                    read(now ^ kStage, 0, 0);
+                }
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
 #pragma unroll
                     for (int j = 0; j < NI; ++j)
-                        acc[i][j] = mfma32<FMT>(fa[i], fb[j], acc[i][j]);
+                        acc[i][j] = mfma32<FMT>(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
             }
             now ^= kStage;
         }

@@ -24,22 +24,31 @@ constexpr int64_t kVocabMaxVocab = int64_t(1) << 24;
 constexpr int64_t kVocabMaxWidth = 65536;
 constexpr int64_t kVocabMaxStride = int64_t(1) << 22;   // of W read in place: offsets in a tile have 32 bits
 constexpr uint64_t kVocabPiece = uint64_t(1) << 29;     // bytes of a piece's dz
+constexpr int64_t kVocabMinPiece = 2048, kVocabMaxPiece = 32768;
+// Tiles of the two gradients that are to be there at once: where there are fewer,
+// a tile's sum is split over k and joined afterwards.
+constexpr int64_t kVocabBlocks = 512;
+constexpr uint64_t kVocabParts = static_cast<uint64_t>(kVocabBlocks) * 128 * 128 * 4;   // bytes of the parts
 
 struct VocabSizes {
     int64_t tokens, vocab, width;
     int64_t tp, dp, vc;                    // padded tokens and width, vocabulary of a piece
+    int64_t vmax;                          // the largest piece of any number of tokens
     int64_t tiles;                         // partial sums per row
+    int32_t xs, ws;                        // parts of the sums for dX and dW
 };
 
 struct VocabWork {
     int32_t *used, *slot, *list, *target;  // [1], [tokens], [tp], [tp]
+    uint32_t* ticket;                      // blocks of the join that are done
     float* of_target;                      // [tp] the target's logit
     TopSum* part;                          // [tiles][tp]
     TopSum* row;                           // [tp] maximum, log2 of the sum
     uint16_t* x;                           // [tp][dp]
     uint16_t* w;                           // [vc][dp], where W cannot be read in place
     uint16_t* dz;                          // [tp][vc]
-    float* dx;                             // [tp][dp], where there are several pieces
+    float* dx;                             // [xs][tokens][dp], where there are several pieces or parts
+    float* dw;                             // [ws][vc][dp], where there are several parts
 };
 
 // Compact numbers of the used rows (t ascending), by one block.
@@ -77,8 +86,10 @@ __global__ __launch_bounds__(kVocabListBlock) void vocab_list_kernel(const I* __
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         *w.used = before;
+        *w.ticket = 0;
+    }
 }
 
 // A row of `width` 16-bit values, padded with zeros to dp, by one wave.
@@ -101,29 +112,85 @@ __device__ __forceinline__ void pack_row(const uint16_t* from, int64_t width, ui
 }
 
 constexpr int kPackBlock = 256;
-// Wave t < tokens: row t of X to its place, or zeros to its gradient; the waves
-// behind: zero rows up to the next 64.
+
+// The row of wave-number t: row t of X to its place, or zeros to its gradient;
+// behind the last: zero rows up to the next 64.
+__device__ __forceinline__ void pack_token(const uint16_t* hidden, int64_t hs, uint16_t* dhidden, int64_t dhs,
+                                           const VocabSizes& s, const VocabWork& w, int64_t t, int slot, int used, int lane)
+{
+    if (t >= s.tokens) {
+        const int64_t row = used + (t - s.tokens);
+        if (row < (used + kBK - 1) / kBK * kBK)
+            pack_row(nullptr, 0, w.x + row * s.dp, s.dp, lane);
+    } else if (slot >= 0) {
+        pack_row(hidden + t * hs, s.width, w.x + slot * s.dp, s.dp, lane);
+    } else if (dhidden != nullptr) {
+        for (int64_t i = lane; i < s.width; i += 64)
+            dhidden[t * dhs + i] = 0;
+    }
+}
+
 __global__ __launch_bounds__(kPackBlock) void vocab_pack_kernel(const uint16_t* __restrict__ hidden, int64_t hs,
                                                                 uint16_t* __restrict__ dhidden, int64_t dhs,
                                                                 VocabSizes s, VocabWork w)
 {
-    const int lane = static_cast<int>(__lane_id());
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kPackBlock / 64);
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kPackBlock / 64) + threadIdx.x / 64; t < s.tokens + kBK;
-         t += step) {
-        if (t >= s.tokens) {
-            const int64_t row = *w.used + (t - s.tokens);
-            if (row < (*w.used + kBK - 1) / kBK * kBK)
-                pack_row(nullptr, 0, w.x + row * s.dp, s.dp, lane);
-            continue;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kPackBlock / 64) + threadIdx.x / 64; t < s.tokens + kBK; t += step)
+        pack_token(hidden, hs, dhidden, dhs, s, w, t, t < s.tokens ? w.slot[t] : -1, *w.used,
+                   static_cast<int>(__lane_id()));
+}
+
+// Both in one kernel for few tokens: every block numbers all rows itself.
+constexpr int kFewTokens = 2048;
+template <typename I>
+__global__ __launch_bounds__(kPackBlock) void vocab_list_pack_kernel(const I* __restrict__ targets,
+                                                                     const uint8_t* __restrict__ mask,
+                                                                     const uint16_t* __restrict__ hidden, int64_t hs,
+                                                                     uint16_t* __restrict__ dhidden, int64_t dhs, VocabSizes s,
+                                                                     VocabWork w, float* __restrict__ token_loss)
+{
+    constexpr int kWaves = kPackBlock / 64;
+    __shared__ uint64_t on[kFewTokens / 64];                   // a bit for each row
+    const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
+    const int tokens = static_cast<int>(s.tokens), words = (tokens + 63) / 64;
+    for (int v = wave; v < words; v += kWaves) {
+        const int t = v * 64 + lane;
+        int64_t y = -1;
+        if (t < tokens && (mask == nullptr || mask[t] != 0))
+            y = targets[t];
+        const uint64_t bits = __ballot(y >= 0);
+        if (lane == 0)
+            on[v] = bits;
+    }
+    __syncthreads();
+    auto before = [&](int t) {                                 // used rows below t
+        int n = 0;
+        for (int v = lane; v * 64 < t; v += 64)
+            n += __popcll(v * 64 + 64 <= t ? on[v] : on[v] & ((1ull << (t - v * 64)) - 1));
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            n += __shfl_xor(n, off);
+        return n;
+    };
+    const int used = before(tokens);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *w.used = used;
+        *w.ticket = 0;
+    }
+    const int step = static_cast<int>(gridDim.x) * kWaves;
+    for (int t = static_cast<int>(blockIdx.x) * kWaves + wave; t < tokens + kBK; t += step) {
+        int slot = -1;
+        if (t < tokens && (on[t / 64] >> (t % 64) & 1)) {
+            slot = before(t);
+            if (lane == 0) {
+                const int64_t y = targets[t];
+                w.list[slot] = t;
+                w.target[slot] = y < s.vocab ? static_cast<int32_t>(y) : -1;
+            }
+        } else if (t < tokens && lane == 0) {
+            token_loss[t] = 0.0f;
         }
-        const int slot = w.slot[t];
-        if (slot >= 0) {
-            pack_row(hidden + t * hs, s.width, w.x + slot * s.dp, s.dp, lane);
-        } else if (dhidden != nullptr) {
-            for (int64_t i = lane; i < s.width; i += 64)
-                dhidden[t * dhs + i] = 0;
-        }
+        pack_token(hidden, hs, dhidden, dhs, s, w, t, slot, used, lane);
     }
 }
 
@@ -224,10 +291,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kerne
 }
 
 // Joins each row's partial sums: 64 rows a block, its waves share the tiles.
+// MEAN: the last block to end forms the mean.
 constexpr int kJoinBlock = 256;
-__global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, VocabWork w, float* __restrict__ token_loss)
+constexpr int64_t kJoinMean = 16384;       // up to so many tokens; past that the sum wants more lanes
+template <bool MEAN>
+__global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, VocabWork w, float coef,
+                                                                float* token_loss, float* loss, int32_t* used_out)
 {
     __shared__ TopSum part[kJoinBlock / 64][64];
+    __shared__ uint32_t ticket;
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
     const int used = *w.used;
     for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * 64; n0 < used; n0 += static_cast<int64_t>(gridDim.x) * 64) {
@@ -249,6 +321,23 @@ __global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, Vo
         }
         __syncthreads();
     }
+    if constexpr (MEAN) {
+        if (gridDim.x > 1) {
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0)
+                ticket = atomicAdd(w.ticket, 1u);
+            __syncthreads();
+            if (ticket != gridDim.x - 1)
+                return;
+            __threadfence();
+        }
+        const float mean = rows_mean<kJoinBlock>(token_loss, s.tokens, used, coef);
+        if (threadIdx.x == 0) {
+            *loss = mean;
+            *used_out = used;
+        }
+    }
 }
 
 struct VocabGrad {
@@ -258,6 +347,7 @@ struct VocabGrad {
     int64_t dhs;
     void* dweight;
     int64_t dws;
+    int32_t dw32, accumulate;              // dW in fp32; added to
     int32_t first, last;                   // of the pieces
 };
 
@@ -299,112 +389,175 @@ __device__ __forceinline__ f32x4 load4(const void* row, int64_t d, int64_t width
     return x;
 }
 
-// dX of a piece: m: width, n: tokens, k: the piece's vocabulary.
-template <int FMT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_dx_kernel(VocabPiece p, VocabSizes s, VocabWork w,
-                                                                            VocabGrad g)
+template <int FMT>
+__device__ __forceinline__ void store_dw(const VocabGrad& g, int64_t v, int64_t d, int64_t width, f32x4 x)
 {
-    using P = Product<FMT, true, false, BM, BN, WM, WN>;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[P::kLds];
+    unsigned char* row = static_cast<unsigned char*>(g.dweight) + v * g.dws * (g.dw32 ? 4 : 2);
+    if (g.dw32)
+        store4<kF32>(row, d, width, g.accumulate ? x + load4<kF32>(row, d, width) : x);
+    else
+        store4<FMT>(row, d, width, g.accumulate ? x + load4<FMT>(row, d, width) : x);
+}
+
+// The k tiles of part `of` of `parts`.
+__device__ __forceinline__ void part_of_k(int ktiles, int of, int parts, int& first, int& count)
+{
+    const int each = (ktiles + parts - 1) / parts;
+    first = min(of * each, ktiles);
+    count = min(each, ktiles - first);
+}
+
+// dX of a piece (m: width, n: tokens, k: the piece's vocabulary) by the first
+// `tx` blocks, dW of its rows (m: width, n: the piece's vocabulary, k: tokens) by
+// the others.
+template <int FMT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_grads_kernel(VocabPiece p, VocabSizes s, VocabWork w,
+                                                                               VocabGrad g, int32_t tx)
+{
+    using PX = Product<FMT, true, false, BM, BN, WM, WN>;
+    using PW = Product<FMT, true, true, BM, BN, WM, WN>;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[PX::kLds];
     const int used = *w.used;
-    int tm, tn;
-    tile_of(static_cast<int>(blockIdx.x), static_cast<int>((s.dp + BM - 1) / BM), static_cast<int>((s.tokens + BN - 1) / BN),
-            tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
-    if (n0 >= used)
-        return;
-    P c;
-    c.run(lds, Operand{p.w + m0, p.stride, static_cast<int32_t>(s.dp) - m0, static_cast<int32_t>(p.rows)},
-          Operand{w.dz + n0 * s.vc, s.vc, static_cast<int32_t>(s.tp) - n0, 0}, static_cast<int>((p.rows + kBK - 1) / kBK));
     const float factor = vocab_factor<FMT>(g, used);
+    const int tiles_m = static_cast<int>((s.dp + BM - 1) / BM);
+    int tm, tn, first, count;
+    if (static_cast<int>(blockIdx.x) < tx) {
+        const int tiles = tx / s.xs, of = static_cast<int>(blockIdx.x) / tiles;
+        tile_of(static_cast<int>(blockIdx.x) % tiles, tiles_m, tiles / tiles_m, tm, tn);
+        const int m0 = tm * BM, n0 = tn * BN;
+        if (n0 >= used)
+            return;
+        part_of_k(static_cast<int>((p.rows + kBK - 1) / kBK), of, s.xs, first, count);
+        const int64_t k0 = static_cast<int64_t>(first) * kBK;
+        PX c;
+        c.run(lds, Operand{p.w + k0 * p.stride + m0, p.stride, static_cast<int32_t>(s.dp) - m0, static_cast<int32_t>(p.rows - k0)},
+              Operand{w.dz + n0 * s.vc + k0, s.vc, static_cast<int32_t>(s.tp) - n0, 0}, count);
+        const bool out = g.last && s.xs == 1;
 #pragma unroll
-    for (int j = 0; j < P::NI; ++j) {
-        const int n = n0 + c.col(j);
-        if (n >= used)
-            continue;
-        const int64_t t = g.last ? w.list[n] : 0;
+        for (int j = 0; j < PX::NI; ++j) {
+            const int n = n0 + c.col(j);
+            if (n >= used)
+                continue;
+            const int64_t t = out ? w.list[n] : 0;
 #pragma unroll
-        for (int i = 0; i < P::MI; ++i)
+            for (int i = 0; i < PX::MI; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int d = m0 + c.row(i, 4 * q);
-                if (d >= s.dp)
-                    continue;
-                f32x4 x = {c.acc[i][j][4 * q], c.acc[i][j][4 * q + 1], c.acc[i][j][4 * q + 2], c.acc[i][j][4 * q + 3]};
-                f32x4* sum = reinterpret_cast<f32x4*>(w.dx + static_cast<int64_t>(n) * s.dp + d);
-                if (!g.first)
-                    x = x + *sum;
-                if (g.last)
-                    store4<FMT>(g.dhidden + t * g.dhs, d, s.width, x * factor);
-                else
-                    *sum = x;
-            }
+                for (int q = 0; q < 4; ++q) {
+                    const int d = m0 + c.row(i, 4 * q);
+                    if (d >= s.dp)
+                        continue;
+                    f32x4 x = {c.acc[i][j][4 * q], c.acc[i][j][4 * q + 1], c.acc[i][j][4 * q + 2], c.acc[i][j][4 * q + 3]};
+                    f32x4* sum = reinterpret_cast<f32x4*>(w.dx + (of * s.tokens + n) * s.dp + d);
+                    if (!g.first)
+                        x = x + *sum;
+                    if (out)
+                        store4<FMT>(g.dhidden + t * g.dhs, d, s.width, x * factor);
+                    else
+                        *sum = x;
+                }
+        }
+    } else {
+        const int block = static_cast<int>(blockIdx.x) - tx, tiles = (static_cast<int>(gridDim.x) - tx) / s.ws;
+        const int of = block / tiles;
+        tile_of(block % tiles, tiles_m, tiles / tiles_m, tm, tn);
+        const int m0 = tm * BM, n0 = tn * BN;
+        part_of_k((used + kBK - 1) / kBK, of, s.ws, first, count);
+        const int64_t k0 = static_cast<int64_t>(first) * kBK;
+        const int k_rows = static_cast<int>(s.tp - k0);
+        PW c;
+        c.run(lds, Operand{w.x + k0 * s.dp + m0, s.dp, static_cast<int32_t>(s.dp) - m0, k_rows},
+              Operand{w.dz + k0 * s.vc + n0, s.vc, static_cast<int32_t>(s.vc) - n0, k_rows}, count);
+#pragma unroll
+        for (int j = 0; j < PW::NI; ++j) {
+            const int n = n0 + c.col(j);
+            if (n >= p.rows)
+                continue;
+#pragma unroll
+            for (int i = 0; i < PW::MI; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int d = m0 + c.row(i, 4 * q);
+                    if (d >= s.dp)
+                        continue;
+                    const f32x4 x = {c.acc[i][j][4 * q], c.acc[i][j][4 * q + 1], c.acc[i][j][4 * q + 2],
+                                     c.acc[i][j][4 * q + 3]};
+                    if (s.ws > 1)
+                        *reinterpret_cast<f32x4*>(w.dw + (of * p.rows + n) * s.dp + d) = x;
+                    else if (d < s.width)
+                        store_dw<FMT>(g, p.v0 + n, d, s.width, x * factor);
+                }
+        }
     }
 }
 
-// dW of a piece: m: width, n: the piece's vocabulary, k: tokens.
-template <int FMT, int OF, bool ACC, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_dw_kernel(VocabPiece p, VocabSizes s, VocabWork w,
-                                                                            VocabGrad g)
+// Adds the parts: rows of dX (behind the last piece) by the first rows, rows of
+// dW by the others; a wave has a row.
+template <int FMT>
+__global__ __launch_bounds__(kPackBlock) void vocab_parts_kernel(VocabPiece p, VocabSizes s, VocabWork w, VocabGrad g,
+                                                                 int64_t xrows, int64_t wrows)
 {
-    using P = Product<FMT, true, true, BM, BN, WM, WN>;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[P::kLds];
+    const int lane = static_cast<int>(__lane_id());
     const int used = *w.used;
-    int tm, tn;
-    tile_of(static_cast<int>(blockIdx.x), static_cast<int>((s.dp + BM - 1) / BM), static_cast<int>((p.rows + BN - 1) / BN), tm,
-            tn);
-    const int m0 = tm * BM, n0 = tn * BN;
-    P c;
-    const int k_rows = static_cast<int>(s.tp);
-    c.run(lds, Operand{w.x + m0, s.dp, static_cast<int32_t>(s.dp) - m0, k_rows},
-          Operand{w.dz + n0, s.vc, static_cast<int32_t>(s.vc) - n0, k_rows}, (used + kBK - 1) / kBK);
     const float factor = vocab_factor<FMT>(g, used);
-    constexpr int es = OF == kF32 ? 4 : 2;
-#pragma unroll
-    for (int j = 0; j < P::NI; ++j) {
-        const int n = n0 + c.col(j);
-        if (n >= p.rows)
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kPackBlock / 64);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kPackBlock / 64) + threadIdx.x / 64; r < xrows + wrows; r += step) {
+        const bool x_side = r < xrows;
+        if (x_side && r >= used)
             continue;
-        unsigned char* row = static_cast<unsigned char*>(g.dweight) + (p.v0 + n) * g.dws * es;
-#pragma unroll
-        for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int d = m0 + c.row(i, 4 * q);
-                if (d >= s.width)
-                    continue;
-                f32x4 x = {c.acc[i][j][4 * q], c.acc[i][j][4 * q + 1], c.acc[i][j][4 * q + 2], c.acc[i][j][4 * q + 3]};
-                x = x * factor;
-                if constexpr (ACC)
-                    x = x + load4<OF>(row, d, s.width);
-                store4<OF>(row, d, s.width, x);
-            }
+        const int64_t row = x_side ? r : r - xrows, all = x_side ? s.tokens : p.rows;
+        const float* part = x_side ? w.dx : w.dw;
+        const int parts = x_side ? s.xs : s.ws;
+        for (int64_t d = 4 * lane; d < s.width; d += 256) {
+            f32x4 sum = *reinterpret_cast<const f32x4*>(part + row * s.dp + d);
+            for (int i = 1; i < parts; ++i)
+                sum = sum + *reinterpret_cast<const f32x4*>(part + (i * all + row) * s.dp + d);
+            sum = sum * factor;
+            if (x_side)
+                store4<FMT>(g.dhidden + w.list[row] * g.dhs, d, s.width, sum);
+            else
+                store_dw<FMT>(g, p.v0 + row, d, s.width, sum);
+        }
     }
 }
 
 // ---- host side ----
 
+int64_t up_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+// Parts that a product over `ktiles` tiles of k is split into, for `tiles` tiles
+// of 128 x 128: as many as fill the GPU, with four tiles of k each at least.
+int32_t vocab_split(int64_t tiles, int64_t ktiles)
+{
+    int64_t n = kVocabBlocks / tiles;
+    n = n < ktiles / 4 ? n : ktiles / 4;
+    return static_cast<int32_t>(n < 1 ? 1 : n);
+}
+
 bool vocab_sizes(int64_t tokens, int64_t vocab, int64_t width, VocabSizes* s)
 {
     if (tokens < 0 || tokens > kVocabMaxTokens || vocab < 1 || vocab > kVocabMaxVocab || width < 1 || width > kVocabMaxWidth)
         return false;
-    auto up = [](int64_t x, int64_t a) { return (x + a - 1) / a * a; };
     s->tokens = tokens;
     s->vocab = vocab;
     s->width = width;
-    s->tp = up(tokens > 0 ? tokens : 1, kVocabTile);
-    s->dp = up(width, kBK);
-    const int64_t whole = up(vocab, kVocabTile);
+    s->tp = up_to(tokens > 0 ? tokens : 1, kVocabTile);
+    s->dp = up_to(width, kBK);
+    const int64_t whole = up_to(vocab, kVocabTile);
+    s->vmax = whole < kVocabMaxPiece ? whole : kVocabMaxPiece;
     int64_t vc = static_cast<int64_t>(kVocabPiece / (2 * static_cast<uint64_t>(s->tp))) / kVocabTile * kVocabTile;
-    vc = vc < 2048 ? 2048 : vc > 65536 ? 65536 : vc;
-    s->vc = vc < whole ? vc : whole;
+    vc = vc < kVocabMinPiece ? kVocabMinPiece : vc;
+    s->vc = vc < s->vmax ? vc : s->vmax;
     s->tiles = 0;
+    const int64_t dt = (s->dp + 127) / 128;
+    s->xs = vocab_split(dt * ((s->tp + 127) / 128), s->vc / kBK);
+    s->ws = vocab_split(dt * ((s->vc + 127) / 128), s->tp / kBK);
     return true;
 }
 
 constexpr int kVocabMinTile = 128;         // of the vocabulary, for the partial sums' space
 
-// The workspace's arrays from `base` on, each 256-byte aligned; returns the bytes.
+// The workspace's arrays from `base` on, each 256-byte aligned; returns the
+// bytes, which are no fewer than those for fewer tokens (with larger pieces).
 uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
 {
     uint64_t at = 0;
@@ -413,9 +566,11 @@ uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    const uint64_t tp = static_cast<uint64_t>(s.tp), dp = static_cast<uint64_t>(s.dp), vc = static_cast<uint64_t>(s.vc);
+    const uint64_t tp = static_cast<uint64_t>(s.tp), dp = static_cast<uint64_t>(s.dp), vmax = static_cast<uint64_t>(s.vmax);
     const uint64_t tiles = (static_cast<uint64_t>(s.vocab) + kVocabMinTile - 1) / kVocabMinTile;
+    const uint64_t piece = 2 * tp * static_cast<uint64_t>(s.vc), most = std::min(2 * tp * vmax, kVocabPiece);
     w->used = reinterpret_cast<int32_t*>(take(4));
+    w->ticket = reinterpret_cast<uint32_t*>(take(4));
     w->slot = reinterpret_cast<int32_t*>(take(4 * tp));
     w->list = reinterpret_cast<int32_t*>(take(4 * tp));
     w->target = reinterpret_cast<int32_t*>(take(4 * tp));
@@ -423,9 +578,10 @@ uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
     w->part = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * tp * tiles));
     w->row = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * tp));
     w->x = reinterpret_cast<uint16_t*>(take(2 * tp * dp));
-    w->w = reinterpret_cast<uint16_t*>(take(2 * vc * dp));
-    w->dz = reinterpret_cast<uint16_t*>(take(2 * tp * vc));
-    w->dx = reinterpret_cast<float*>(take(s.vc < s.vocab ? 4 * tp * dp : 0));
+    w->w = reinterpret_cast<uint16_t*>(take(2 * vmax * dp));
+    w->dz = reinterpret_cast<uint16_t*>(take(std::max(piece, most)));
+    w->dx = reinterpret_cast<float*>(take(std::max(kVocabParts, s.vc < s.vocab ? 4 * tp * dp : 0)));
+    w->dw = reinterpret_cast<float*>(take(kVocabParts));
     return at;
 }
 
@@ -433,8 +589,6 @@ struct VocabCall {
     const uint16_t* weight;
     int64_t ws;
     bool in_place;                         // W is read where it lies
-    ds_dtype dwt;
-    bool accumulate;
 };
 
 VocabPiece vocab_piece(const VocabSizes& s, const VocabWork& w, const VocabCall& c, int64_t v0, hipStream_t st)
@@ -447,27 +601,43 @@ VocabPiece vocab_piece(const VocabSizes& s, const VocabWork& w, const VocabCall&
     return {w.w, s.dp, v0, rows};
 }
 
-unsigned vocab_tiles(int64_t m, int bm, int64_t n, int bn)
+int64_t vocab_tiles(int64_t m, int64_t n, int tile) { return ((m + tile - 1) / tile) * ((n + tile - 1) / tile); }
+
+// Whether tiles of 256 x 256 (one block a CU) are faster than such of 128 x 128
+// (two): the time of each in rounds of the GPU, a small tile costing 1 / 0.85 of a
+// quarter of a large one.
+bool vocab_large(int64_t large, int64_t small)
 {
-    return static_cast<unsigned>(((m + bm - 1) / bm) * ((n + bn - 1) / bn));
+    return 4.0 * static_cast<double>((large + 255) / 256) <= 2.0 / 0.85 * static_cast<double>((small + 511) / 512);
 }
 
-template <int FMT, int BM, int BN, int WM, int WN>
+template <int FMT, bool DZ>
+int64_t vocab_logits(const VocabPiece& p, const VocabSizes& s, const VocabWork& w, bool large, hipStream_t st)
+{
+    const unsigned b = static_cast<unsigned>(vocab_tiles(p.rows, s.tokens, large ? 256 : 128));
+    if (large) vocab_logits_kernel<FMT, DZ, 256, 256, 64, 128><<<b, 512, 0, st>>>(p, s, w);
+    else       vocab_logits_kernel<FMT, DZ, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w);
+    return large ? 256 : 128;
+}
+
+template <int FMT>
 ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const VocabGrad& g, float* token_loss, float* loss,
                     int32_t* used, hipStream_t st)
 {
-    constexpr int threads = (BM / WM) * (BN / WN) * 64;
-    static_assert(BM >= kVocabMinTile, "space of the partial sums");
-    s.tiles = (s.vocab + BM - 1) / BM;
     if (s.tokens > 0) {
-        for (int64_t v0 = 0; v0 < s.vocab; v0 += s.vc) {
-            const VocabPiece p = vocab_piece(s, w, c, v0, st);
-            vocab_logits_kernel<FMT, false, BM, BN, WM, WN>
-                <<<vocab_tiles(p.rows, BM, s.tokens, BN), threads, 0, st>>>(p, s, w);
-        }
-        vocab_join_kernel<<<grid_blocks((s.tokens + 63) / 64, kJoinBlock), kJoinBlock, 0, st>>>(s, w, token_loss);
+        const int64_t piece = s.vc < s.vocab ? s.vc : s.vocab;
+        const bool large = vocab_large(vocab_tiles(piece, s.tokens, 256), vocab_tiles(piece, s.tokens, 128));
+        s.tiles = (s.vocab + (large ? 255 : 127)) / (large ? 256 : 128);
+        for (int64_t v0 = 0; v0 < s.vocab; v0 += s.vc)
+            vocab_logits<FMT, false>(vocab_piece(s, w, c, v0, st), s, w, large, st);
+        const unsigned b = grid_blocks((s.tokens + 63) / 64, kJoinBlock);
+        if (s.tokens <= kJoinMean)
+            vocab_join_kernel<true><<<b, kJoinBlock, 0, st>>>(s, w, g.coef, token_loss, loss, used);
+        else
+            vocab_join_kernel<false><<<b, kJoinBlock, 0, st>>>(s, w, g.coef, token_loss, loss, used);
     }
-    rows_mean_kernel<<<1, kMeanBlock, 0, st>>>(token_loss, s.tokens, w.used, g.coef, loss, used, 0);
+    if (s.tokens == 0 || s.tokens > kJoinMean)
+        rows_mean_kernel<<<1, kMeanBlock, 0, st>>>(token_loss, s.tokens, w.used, g.coef, loss, used, 0);
     if (launched() != DS_OK)
         return DS_ERR_HIP;
     if (g.dhidden == nullptr && g.dweight == nullptr)
@@ -477,22 +647,30 @@ ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const 
         VocabGrad h = g;
         h.first = v0 == 0;
         h.last = v0 + p.rows == s.vocab;
-        if (s.tokens > 0) {
-            vocab_logits_kernel<FMT, true, BM, BN, WM, WN>
-                <<<vocab_tiles(p.rows, BM, s.tokens, BN), threads, 0, st>>>(p, s, w);
-            if (g.dhidden != nullptr)
-                vocab_dx_kernel<FMT, BM, BN, WM, WN><<<vocab_tiles(s.dp, BM, s.tokens, BN), threads, 0, st>>>(p, s, w, h);
-        }
-        if (g.dweight != nullptr) {
-            const unsigned b = vocab_tiles(s.dp, BM, p.rows, BN);
-            if (c.dwt == DS_FP32) {
-                if (c.accumulate) vocab_dw_kernel<FMT, kF32, true, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
-                else              vocab_dw_kernel<FMT, kF32, false, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
-            } else {
-                if (c.accumulate) vocab_dw_kernel<FMT, FMT, true, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
-                else              vocab_dw_kernel<FMT, FMT, false, BM, BN, WM, WN><<<b, threads, 0, st>>>(p, s, w, h);
-            }
-        }
+        if (s.tokens > 0)
+            vocab_logits<FMT, true>(p, s, w, vocab_large(vocab_tiles(p.rows, s.tokens, 256), vocab_tiles(p.rows, s.tokens, 128)),
+                                    st);
+        // both gradients in one launch: the second fills what the first leaves free
+        const bool dx = g.dhidden != nullptr && s.tokens > 0, dw = g.dweight != nullptr;
+        auto tiles = [&](int tile, int64_t& x, int64_t& all) {
+            x = dx ? vocab_tiles(s.dp, s.tokens, tile) * s.xs : 0;
+            all = x + (dw ? vocab_tiles(s.dp, p.rows, tile) * s.ws : 0);
+        };
+        int64_t x, all, x_large, all_large;
+        tiles(128, x, all);
+        tiles(256, x_large, all_large);
+        if (all == 0)
+            continue;
+        if (vocab_large(all_large, all))
+            vocab_grads_kernel<FMT, 256, 256, 64, 128><<<static_cast<unsigned>(all_large), 512, 0, st>>>(
+                p, s, w, h, static_cast<int32_t>(x_large));
+        else
+            vocab_grads_kernel<FMT, 128, 128, 64, 64><<<static_cast<unsigned>(all), 256, 0, st>>>(p, s, w, h,
+                                                                                                static_cast<int32_t>(x));
+        const int64_t xrows = dx && h.last && s.xs > 1 ? s.tokens : 0, wrows = dw && s.ws > 1 ? p.rows : 0;
+        if (xrows + wrows > 0)
+            vocab_parts_kernel<FMT><<<grid_blocks((xrows + wrows + 3) / 4, kPackBlock), kPackBlock, 0, st>>>(p, s, w, h, xrows,
+                                                                                                         wrows);
         if (launched() != DS_OK)
             return DS_ERR_HIP;
     }
@@ -533,17 +711,26 @@ ds_status vocab_ce(const ds_scaler* scaler, const void* hidden, int64_t hs, cons
     if (bal_alias(p, span, 11, 5))
         return DS_ERR_ALIAS;
     const VocabCall c{static_cast<const uint16_t*>(weight), ws,
-                      aligned(weight, 16) && ws % 8 == 0 && width % kBK == 0 && ws <= kVocabMaxStride, dwt, accumulate};
-    const VocabGrad g{scaler, coef, static_cast<uint16_t*>(dhidden), dhs, dweight, dws, 0, 0};
-    if (index_bytes == 4)
-        vocab_list_kernel<int32_t><<<1, kVocabListBlock, 0, st>>>(static_cast<const int32_t*>(targets), mask, s, w, token_loss);
-    else
-        vocab_list_kernel<int64_t><<<1, kVocabListBlock, 0, st>>>(static_cast<const int64_t*>(targets), mask, s, w, token_loss);
-    vocab_pack_kernel<<<grid_blocks((tokens + kBK + 3) / 4, kPackBlock), kPackBlock, 0, st>>>(
-        static_cast<const uint16_t*>(hidden), hs, g.dhidden, dhs, s, w);
+                      aligned(weight, 16) && ws % 8 == 0 && width % kBK == 0 && ws <= kVocabMaxStride};
+    const VocabGrad g{scaler, coef, static_cast<uint16_t*>(dhidden), dhs, dweight, dws, dwt == DS_FP32, accumulate, 0, 0};
+    const uint16_t* x = static_cast<const uint16_t*>(hidden);
+    const unsigned pack = grid_blocks((tokens + kBK + 3) / 4, kPackBlock);
+    if (tokens <= kFewTokens) {
+        if (index_bytes == 4)
+            vocab_list_pack_kernel<int32_t><<<pack, kPackBlock, 0, st>>>(static_cast<const int32_t*>(targets), mask, x, hs,
+                                                                        g.dhidden, dhs, s, w, token_loss);
+        else
+            vocab_list_pack_kernel<int64_t><<<pack, kPackBlock, 0, st>>>(static_cast<const int64_t*>(targets), mask, x, hs,
+                                                                        g.dhidden, dhs, s, w, token_loss);
+    } else {
+        if (index_bytes == 4)
+            vocab_list_kernel<int32_t><<<1, kVocabListBlock, 0, st>>>(static_cast<const int32_t*>(targets), mask, s, w, token_loss);
+        else
+            vocab_list_kernel<int64_t><<<1, kVocabListBlock, 0, st>>>(static_cast<const int64_t*>(targets), mask, s, w, token_loss);
+        vocab_pack_kernel<<<pack, kPackBlock, 0, st>>>(x, hs, g.dhidden, dhs, s, w);
+    }
     if (launched() != DS_OK)
         return DS_ERR_HIP;
-    if (dt == DS_FP16)
-        return vocab_run<kF16, 128, 128, 64, 64>(s, w, c, g, token_loss, loss, used, st);
-    return vocab_run<kBF16, 128, 128, 64, 64>(s, w, c, g, token_loss, loss, used, st);
+    return dt == DS_FP16 ? vocab_run<kF16>(s, w, c, g, token_loss, loss, used, st)
+                         : vocab_run<kBF16>(s, w, c, g, token_loss, loss, used, st);
 }
