@@ -16,6 +16,7 @@
 constexpr int kDispBlock = 256, kDispWaves = kDispBlock / 64;
 constexpr int64_t kDispChunk = 1024;       // pairs per block, at least
 constexpr int64_t kDispMaxBlocks = 256;    // blocks of the sort: each reads the counts of all
+constexpr int kDispSpan = 4;               // vectors of a row that a lane has at once
 constexpr int64_t kDispMaxPairs = (int64_t(1) << 31) - 1;
 constexpr int64_t kDispMaxWidth = int64_t(1) << 24;
 static_assert(DS_MAX_EXPERTS <= 2 * kDispBlock, "the scan has two experts a lane");
@@ -241,26 +242,65 @@ __device__ __forceinline__ int disp_slot(const DispMove& s, int64_t t, int j)
     return static_cast<uint32_t>(slot) < static_cast<uint64_t>(s.rows) ? slot : -1;
 }
 
-template <int ES, int G>
+// A group goes over a row in spans of U vectors a lane, and takes a span of one
+// row whole before the next row's, so that what it reads and writes of a row lies
+// together.  Lanes past a row's last vector repeat it, and rows of dropped choices
+// are read as the first row's: no load is conditional, so that a wait for one
+// row's span can leave the next one's on its way.
+template <int G, int U>
+struct DispSpan {
+    int at[U];                             // the lane's vectors
+    bool has[U];
+
+    __device__ __forceinline__ DispSpan(int base, int vecs, int lane)
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = base + u * G + lane;
+            has[u] = c < vecs;
+            at[u] = min(c, vecs - 1);
+        }
+    }
+
+    __device__ __forceinline__ void load(u32x4 (&v)[U], const unsigned char* row) const
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = reinterpret_cast<const u32x4_any*>(row)[static_cast<uint32_t>(at[u])];
+    }
+
+    __device__ __forceinline__ void store(unsigned char* row, int u, u32x4 v) const
+    {
+        if (has[u])
+            reinterpret_cast<u32x4_any*>(row)[static_cast<uint32_t>(at[u])] = v;
+    }
+};
+
+template <int ES, int G, int U>
 __global__ __launch_bounds__(kDispBlock) void dispatch_gather_kernel(DispMove s, const unsigned char* __restrict__ x,
                                                                      int64_t xs, unsigned char* __restrict__ out,
                                                                      int64_t os)
 {
     constexpr int kVec = 16 / ES;
     const int lane = static_cast<int>(threadIdx.x) % G;
-    const int64_t vecs = s.width / kVec;
+    const int vecs = static_cast<int>(s.width / kVec);
     int64_t groups;
     for (int64_t t = disp_first<G>(groups); t < s.tokens; t += groups) {
         const unsigned char* from = x + t * xs * ES;
-        for (int64_t c = lane; c < vecs; c += G) {
-            const u32x4 v = reinterpret_cast<const u32x4_any*>(from)[c];
+        for (int base = 0; base < vecs; base += U * G) {
+            const DispSpan<G, U> span(base, vecs, lane);
+            u32x4 v[U];
+            span.load(v, from);
             for (int j = 0; j < s.k; ++j) {
                 const int slot = disp_slot<G>(s, t, j);
-                if (slot >= 0)
-                    reinterpret_cast<u32x4_any*>(out + slot * os * ES)[c] = v;
+                if (slot >= 0) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        span.store(out + slot * os * ES, u, v[u]);
+                }
             }
         }
-        for (int64_t i = vecs * kVec + lane; i < s.width; i += G)
+        for (int64_t i = static_cast<int64_t>(vecs) * kVec + lane; i < s.width; i += G)
             for (int j = 0; j < s.k; ++j) {
                 const int slot = disp_slot<G>(s, t, j);
                 if (slot >= 0) {
@@ -275,7 +315,7 @@ __global__ __launch_bounds__(kDispBlock) void dispatch_gather_kernel(DispMove s,
 
 // out[t] = sum_j gate_tj rows[place_tj] (without gates: of the rows), in fp32,
 // j ascending, rounded once.
-template <int FMT, int G, int KM>
+template <int FMT, int G, int KM, int U>
 __global__ __launch_bounds__(kDispBlock) void dispatch_combine_kernel(DispMove s, const unsigned char* __restrict__ rows,
                                                                       int64_t rs, const void* __restrict__ gates,
                                                                       int gfmt, int64_t gs,
@@ -283,7 +323,7 @@ __global__ __launch_bounds__(kDispBlock) void dispatch_combine_kernel(DispMove s
 {
     constexpr int ES = FMT == kF32 ? 4 : 2, kVec = 16 / ES;
     const int lane = static_cast<int>(threadIdx.x) % G;
-    const int64_t vecs = s.width / kVec;
+    const int vecs = static_cast<int>(s.width / kVec);
     int64_t groups;
     for (int64_t t = disp_first<G>(groups); t < s.tokens; t += groups) {
         int slot[KM];
@@ -295,25 +335,33 @@ __global__ __launch_bounds__(kDispBlock) void dispatch_combine_kernel(DispMove s
             if (slot[j] >= 0 && gates != nullptr)
                 gate[j] = load_gate(gates, gfmt, t * gs + j);
         }
-        for (int64_t c = lane; c < vecs; c += G) {
-            u32x4 v[KM];
+        for (int base = 0; base < vecs; base += U * G) {
+            const DispSpan<G, U> span(base, vecs, lane);
+            float sum[U][kVec] = {};
+            if (s.rows > 0) {
+                u32x4 v[2][U];
+                span.load(v[0], rows + max(slot[0], 0) * rs * ES);
 #pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (slot[j] >= 0)
-                    v[j] = reinterpret_cast<const u32x4_any*>(rows + slot[j] * rs * ES)[c];
-            float sum[kVec] = {};
+                for (int j = 0; j < KM; ++j) {
+                    if (j + 1 < KM)
+                        span.load(v[(j + 1) % 2], rows + max(slot[j + 1], 0) * rs * ES);
+                    if (slot[j] >= 0) {
 #pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (slot[j] >= 0) {
-                    float r[kVec];
-                    widen_vec<FMT>(v[j], r);
+                        for (int u = 0; u < U; ++u) {
+                            float r[kVec];
+                            widen_vec<FMT>(v[j % 2][u], r);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i)
-                        sum[i] = __builtin_fmaf(gate[j], r[i], sum[i]);
+                            for (int i = 0; i < kVec; ++i)
+                                sum[u][i] = __builtin_fmaf(gate[j], r[i], sum[u][i]);
+                        }
+                    }
                 }
-            reinterpret_cast<u32x4_any*>(out + t * os * ES)[c] = narrow_vec<FMT>(sum);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                span.store(out + t * os * ES, u, narrow_vec<FMT>(sum[u]));
         }
-        for (int64_t i = vecs * kVec + lane; i < s.width; i += G) {
+        for (int64_t i = static_cast<int64_t>(vecs) * kVec + lane; i < s.width; i += G) {
             float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < KM; ++j)
@@ -326,7 +374,7 @@ __global__ __launch_bounds__(kDispBlock) void dispatch_combine_kernel(DispMove s
 
 // drows[place_tj] = gate_tj dy[t], dgate_tj = sum_d dy[t] rows[place_tj] in
 // fp32 (a choice that was dropped: 0).  One wave (or block) has a whole row.
-template <int FMT, int G, int KM>
+template <int FMT, int G, int KM, int U>
 __global__ __launch_bounds__(kDispBlock) void dispatch_combine_grad_kernel(
     DispMove s, const unsigned char* __restrict__ dy, int64_t ds, const unsigned char* __restrict__ rows, int64_t rs,
     const void* __restrict__ gates, int gfmt, int64_t gs, unsigned char* __restrict__ drows, int64_t drs,
@@ -336,7 +384,7 @@ __global__ __launch_bounds__(kDispBlock) void dispatch_combine_grad_kernel(
     static_assert(G <= 64 || G == kDispBlock, "a wave or a block has a token");
     __shared__ float part[G > 64 ? kDispWaves : 1][KM];
     const int lane = static_cast<int>(threadIdx.x) % G;
-    const int64_t vecs = s.width / kVec;
+    const int vecs = static_cast<int>(s.width / kVec);
     int64_t groups;
     for (int64_t t = disp_first<G>(groups); t < s.tokens; t += groups) {
         int slot[KM];
@@ -347,29 +395,33 @@ __global__ __launch_bounds__(kDispBlock) void dispatch_combine_grad_kernel(
             dot[j] = 0.0f;
             gate[j] = slot[j] >= 0 ? load_gate(gates, gfmt, t * gs + j) : 0.0f;
         }
-        for (int64_t c = lane; c < vecs; c += G) {
-            const u32x4 own = reinterpret_cast<const u32x4_any*>(dy + t * ds * ES)[c];
-            u32x4 v[KM];
+        for (int base = 0; s.rows > 0 && base < vecs; base += U * G) {
+            const DispSpan<G, U> span(base, vecs, lane);
+            u32x4 own[U], v[2][U];
+            span.load(own, dy + t * ds * ES);
+            span.load(v[0], rows + max(slot[0], 0) * rs * ES);
 #pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (slot[j] >= 0)
-                    v[j] = reinterpret_cast<const u32x4_any*>(rows + slot[j] * rs * ES)[c];
-            float d[kVec];
-            widen_vec<FMT>(own, d);
-#pragma unroll
-            for (int j = 0; j < KM; ++j)
+            for (int j = 0; j < KM; ++j) {
+                if (j + 1 < KM)
+                    span.load(v[(j + 1) % 2], rows + max(slot[j + 1], 0) * rs * ES);
                 if (slot[j] >= 0) {
-                    float r[kVec];
-                    widen_vec<FMT>(v[j], r);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) {
-                        dot[j] = __builtin_fmaf(d[i], r[i], dot[j]);
-                        r[i] = gate[j] * d[i];
+                    for (int u = 0; u < U; ++u) {
+                        float d[kVec], r[kVec], sum = 0.0f;
+                        widen_vec<FMT>(own[u], d);
+                        widen_vec<FMT>(v[j % 2][u], r);
+#pragma unroll
+                        for (int i = 0; i < kVec; ++i) {
+                            sum = __builtin_fmaf(d[i], r[i], sum);
+                            r[i] = gate[j] * d[i];
+                        }
+                        dot[j] = dot[j] + (span.has[u] ? sum : 0.0f);
+                        span.store(drows + slot[j] * drs * ES, u, narrow_vec<FMT>(r));
                     }
-                    reinterpret_cast<u32x4_any*>(drows + slot[j] * drs * ES)[c] = narrow_vec<FMT>(r);
                 }
+            }
         }
-        for (int64_t i = vecs * kVec + lane; i < s.width; i += G) {
+        for (int64_t i = static_cast<int64_t>(vecs) * kVec + lane; i < s.width; i += G) {
             const float d = load_elem<FMT>(dy, t * ds + i);
 #pragma unroll
             for (int j = 0; j < KM; ++j)
@@ -538,13 +590,13 @@ ds_status dispatch_gather(const DispMove& s, ds_dtype dt, const void* x, int64_t
     const unsigned char* from = static_cast<const unsigned char*>(x);
     unsigned char* to = static_cast<unsigned char*>(out);
     if (dt == DS_FP32) {
-        if (lanes == 16)      dispatch_gather_kernel<4, 16><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
-        else if (lanes == 64) dispatch_gather_kernel<4, 64><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
-        else                  dispatch_gather_kernel<4, 256><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
+        if (lanes == 16)      dispatch_gather_kernel<4, 16, 1><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
+        else if (lanes == 64) dispatch_gather_kernel<4, 64, kDispSpan><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
+        else                  dispatch_gather_kernel<4, 256, kDispSpan><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
     } else {
-        if (lanes == 16)      dispatch_gather_kernel<2, 16><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
-        else if (lanes == 64) dispatch_gather_kernel<2, 64><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
-        else                  dispatch_gather_kernel<2, 256><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
+        if (lanes == 16)      dispatch_gather_kernel<2, 16, 1><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
+        else if (lanes == 64) dispatch_gather_kernel<2, 64, kDispSpan><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
+        else                  dispatch_gather_kernel<2, 256, kDispSpan><<<b, kDispBlock, 0, st>>>(s, from, xs, to, os);
     }
     return launched();
 }
@@ -562,10 +614,10 @@ struct DispCombine {
 template <int FMT, int G>
 void launch_combine2(unsigned b, hipStream_t st, const DispMove& s, const DispCombine& a)
 {
-    if (s.k <= 2)      dispatch_combine_kernel<FMT, G, 2><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
-    else if (s.k <= 4) dispatch_combine_kernel<FMT, G, 4><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
-    else if (s.k <= 8) dispatch_combine_kernel<FMT, G, 8><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
-    else               dispatch_combine_kernel<FMT, G, 16><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
+    if (s.k <= 2)      dispatch_combine_kernel<FMT, G, 2, (G == 16 ? 1 : kDispSpan)><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
+    else if (s.k <= 4) dispatch_combine_kernel<FMT, G, 4, (G == 16 ? 1 : kDispSpan)><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
+    else if (s.k <= 8) dispatch_combine_kernel<FMT, G, 8, (G == 16 ? 1 : kDispSpan)><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
+    else               dispatch_combine_kernel<FMT, G, 16, (G == 16 ? 1 : kDispSpan)><<<b, kDispBlock, 0, st>>>(s, a.rows, a.rs, a.gates, a.gfmt, a.gs, a.out, a.os);
 }
 
 template <int FMT>
@@ -626,7 +678,7 @@ struct DispCombineGrad {
 template <int FMT, int G, int KM>
 void launch_combine_grad3(unsigned b, hipStream_t st, const DispMove& s, const DispCombineGrad& a)
 {
-    dispatch_combine_grad_kernel<FMT, G, KM><<<b, kDispBlock, 0, st>>>(s, a.dy, a.ds, a.rows, a.rs, a.gates, a.gfmt, a.gs,
+    dispatch_combine_grad_kernel<FMT, G, KM, (G == 16 ? 1 : kDispSpan)><<<b, kDispBlock, 0, st>>>(s, a.dy, a.ds, a.rows, a.rs, a.gates, a.gfmt, a.gs,
                                                                       a.drows, a.drs, a.dgates, a.dgs);
 }
 
