@@ -146,7 +146,7 @@ def test_sort_of_every_kind_of_choice():
                                         ("fp32", "bf16")])
 @pytest.mark.parametrize("T,k,E,width", [(1, 1, 1, 1), (1, 2, 8, 512), (7, 3, 5, 7), (33, 4, 16, 8), (100, 8, 64, 130),
                                          (64, 16, 32, 1001), (257, 2, 3, 520), (30, 5, 12, 4099), (2500, 8, 64, 600),
-                                         (3000, 1, 4, 65)])
+                                         (3000, 1, 4, 65), (5000, 8, 64, 1001)])
 def test_moves(T, k, E, width, kind, gkind):
     op = ExpertDispatch(E, k, T)
     check_moves(op, choices(T, k, E, dropped=0.2), width, kind, gkind)
