@@ -160,22 +160,21 @@ def test_workspace_bytes():
 
 
 def over_stand_ins(monkeypatch, kind, stream=None, current=0, index=0):
-    torch_, library = Torch(current), None
-    torch_.int32, torch_.int64 = torch.int32, torch.int64
+    torch_ = Torch(current)
     library = Library(torch_)
     monkeypatch.setattr(_lib, "lib", library)
     monkeypatch.setattr(_lib, "_raw_stream", lambda i: 0x100 * i)
     op = kind.__new__(kind)
     op.torch, op.stream, op._device, op._many, op.device = torch_, stream, index, True, torch.device("cuda", index)
-    op.max_tokens, op._ws, op._ws_bytes, op._at, op.value = 100, Tensor(64, index=index), 64, (1, 2, 3), "value"
-    op.coef = 1.0
+    op.max_tokens, op._scratch, op._at, op.value, op.coef = 100, (9, 64), (1, 2, 3), "value", 1.0
+    op._index_types = (torch.int32, torch.int64)
     return op, torch_, library
 
 
 def dispatch(monkeypatch, **kw):
     op, torch_, library = over_stand_ins(monkeypatch, ExpertDispatch, **kw)
     op.E, op.k, op.tokens = 64, 8, 0
-    op.offsets, op.place, op.source = (Tensor(100, dtype=torch.int32, index=op._device) for _ in range(3))
+    op.offsets, op._place, op._at = Tensor(100, dtype=torch.int32, index=op._device), 2, (1, 2, 3, 9, 64)
     return op, torch_, library
 
 

@@ -209,18 +209,72 @@ struct VocabPiece {
     int64_t stride, v0, rows;
 };
 
+// A row's maximum and sum over the whole vocabulary from its partial ones, a
+// share of them (`first`, `step`).  Rows are always joined from kJoinWaves
+// shares, so that a loss has the same bits with and without the gradient.
+constexpr int kJoinWaves = 4;
+__device__ __forceinline__ TopSum vocab_join(const VocabSizes& s, const VocabWork& w, int64_t n, int first, int step)
+{
+    TopSum sum{kNegInf, 0.0f};
+    for (int64_t i = first; i < s.tiles; i += step)
+        sum = join(sum, w.part[i * s.tp + n], kLog2e);
+    return sum;
+}
+
+// What a row's joined sums say: maximum and log2 of the sum, NaN for a target
+// past the vocabulary, and the row's loss.
+__device__ __forceinline__ TopSum vocab_row(const VocabWork& w, int64_t n, TopSum sum, float& loss)
+{
+    const bool known = w.target[n] >= 0;
+    const float log_sum = __builtin_amdgcn_logf(sum.sum);
+    loss = known ? (sum.top - w.of_target[n]) + log_sum * kLn2 : __builtin_nanf("");
+    return {known ? sum.top : __builtin_nanf(""), log_sum};
+}
+
+struct VocabLoss {
+    float coef;
+    float *token_loss, *loss;
+    int32_t* used;
+};
+
 // Logits of a piece and, at the end, (DZ) dz or else each row's maximum and sum
-// over the tile.  m: vocabulary, n: tokens.
-template <int FMT, bool DZ, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kernel(VocabPiece p, VocabSizes s, VocabWork w)
+// over the tile.  m: vocabulary, n: tokens.  JOIN (with DZ, for few tokens and a
+// small vocabulary): every block joins its rows' partial sums itself, the first
+// one has all rows and ends the loss, which saves a launch.
+template <int FMT, bool DZ, bool JOIN, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kernel(VocabPiece p, VocabSizes s, VocabWork w,
+                                                                                VocabLoss l)
 {
     using P = Product<FMT, false, false, BM, BN, WM, WN>;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[P::kLds];
+    __shared__ TopSum joined[JOIN ? BN : 1];
     const int used = *w.used;
     int tm, tn;
     tile_of(static_cast<int>(blockIdx.x), static_cast<int>((p.rows + BM - 1) / BM), static_cast<int>((s.tokens + BN - 1) / BN),
             tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
+    if constexpr (JOIN) {
+        static_assert(DZ && P::kThreads >= BN, "a lane for each row");
+        const int n = static_cast<int>(threadIdx.x);
+        if (n < used && n < BN) {
+            float loss;
+            TopSum sum = vocab_join(s, w, n, 0, kJoinWaves);
+#pragma unroll
+            for (int i = 1; i < kJoinWaves; ++i)
+                sum = join(sum, vocab_join(s, w, n, i, kJoinWaves), kLog2e);
+            joined[n] = vocab_row(w, n, sum, loss);
+            if (blockIdx.x == 0)
+                l.token_loss[w.list[n]] = loss;
+        }
+        __syncthreads();
+        if (blockIdx.x == 0) {
+            const float mean = rows_mean<P::kThreads>(l.token_loss, s.tokens, used, l.coef);
+            if (threadIdx.x == 0) {
+                *l.loss = mean;
+                *l.used = used;
+            }
+        }
+    }
     if (n0 >= used)
         return;
     P c;
@@ -234,7 +288,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kerne
         const int y = on ? w.target[n] : -1;
         const int hit = y < 0 ? -1 : static_cast<int>(y - p.v0) - m0;
         if constexpr (DZ) {
-            const TopSum row = on ? w.row[n] : TopSum{0.0f, 0.0f};
+            const TopSum row = !on ? TopSum{0.0f, 0.0f} : JOIN ? joined[JOIN ? c.col(j) : 0] : w.row[n];
             constexpr float unit = FMT == kF16 ? 32768.0f : 1.0f;
 #pragma unroll
             for (int i = 0; i < P::MI; ++i)
@@ -292,13 +346,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kerne
 
 // Joins each row's partial sums: 64 rows a block, its waves share the tiles.
 // MEAN: the last block to end forms the mean.
-constexpr int kJoinBlock = 256;
+constexpr int kJoinBlock = 64 * kJoinWaves;
 constexpr int64_t kJoinMean = 16384;       // up to so many tokens; past that the sum wants more lanes
 template <bool MEAN>
-__global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, VocabWork w, float coef,
-                                                                float* token_loss, float* loss, int32_t* used_out)
+__global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, VocabWork w, VocabLoss l)
 {
-    __shared__ TopSum part[kJoinBlock / 64][64];
+    __shared__ TopSum part[kJoinWaves][64];
     __shared__ uint32_t ticket;
     const int lane = static_cast<int>(__lane_id()), wave = threadIdx.x / 64;
     const int used = *w.used;
@@ -306,18 +359,15 @@ __global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, Vo
         const int64_t n = n0 + lane;
         TopSum sum{kNegInf, 0.0f};
         if (n < used)
-            for (int64_t i = wave; i < s.tiles; i += kJoinBlock / 64)
-                sum = join(sum, w.part[i * s.tp + n], kLog2e);
+            sum = vocab_join(s, w, n, wave, kJoinWaves);
         part[wave][lane] = sum;
         __syncthreads();
         if (wave == 0 && n < used) {
-            for (int i = 1; i < kJoinBlock / 64; ++i)
+            for (int i = 1; i < kJoinWaves; ++i)
                 sum = join(sum, part[i][lane], kLog2e);
-            const bool known = w.target[n] >= 0;
-            const float log_sum = __builtin_amdgcn_logf(sum.sum);
-            // a target past the vocabulary: NaN for the row
-            w.row[n] = TopSum{known ? sum.top : __builtin_nanf(""), log_sum};
-            token_loss[w.list[n]] = known ? (sum.top - w.of_target[n]) + log_sum * kLn2 : __builtin_nanf("");
+            float loss_here;
+            w.row[n] = vocab_row(w, n, sum, loss_here);
+            l.token_loss[w.list[n]] = loss_here;
         }
         __syncthreads();
     }
@@ -332,10 +382,10 @@ __global__ __launch_bounds__(kJoinBlock) void vocab_join_kernel(VocabSizes s, Vo
                 return;
             __threadfence();
         }
-        const float mean = rows_mean<kJoinBlock>(token_loss, s.tokens, used, coef);
+        const float mean = rows_mean<kJoinBlock>(l.token_loss, s.tokens, used, l.coef);
         if (threadIdx.x == 0) {
-            *loss = mean;
-            *used_out = used;
+            *l.loss = mean;
+            *l.used = used;
         }
     }
 }
@@ -611,36 +661,43 @@ bool vocab_large(int64_t large, int64_t small)
     return 4.0 * static_cast<double>((large + 255) / 256) <= 2.0 / 0.85 * static_cast<double>((small + 511) / 512);
 }
 
+// JOIN of the logits kernel: rows of one tile, and partial sums that a lane goes
+// through in the time of a launch.
+constexpr int64_t kVocabJoinTokens = 128, kVocabJoinTiles = 32;
+
 template <int FMT, bool DZ>
-int64_t vocab_logits(const VocabPiece& p, const VocabSizes& s, const VocabWork& w, bool large, hipStream_t st)
+void vocab_logits(const VocabPiece& p, const VocabSizes& s, const VocabWork& w, const VocabLoss& l, bool large, bool join,
+                  hipStream_t st)
 {
     const unsigned b = static_cast<unsigned>(vocab_tiles(p.rows, s.tokens, large ? 256 : 128));
-    if (large) vocab_logits_kernel<FMT, DZ, 256, 256, 64, 128><<<b, 512, 0, st>>>(p, s, w);
-    else       vocab_logits_kernel<FMT, DZ, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w);
-    return large ? 256 : 128;
+    if (DZ && join) vocab_logits_kernel<FMT, true, true, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w, l);
+    else if (large) vocab_logits_kernel<FMT, DZ, false, 256, 256, 64, 128><<<b, 512, 0, st>>>(p, s, w, l);
+    else            vocab_logits_kernel<FMT, DZ, false, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w, l);
 }
 
 template <int FMT>
-ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const VocabGrad& g, float* token_loss, float* loss,
-                    int32_t* used, hipStream_t st)
+ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const VocabGrad& g, const VocabLoss& l, hipStream_t st)
 {
+    const bool with_grad = g.dhidden != nullptr || g.dweight != nullptr;
+    bool join = false;
     if (s.tokens > 0) {
         const int64_t piece = s.vc < s.vocab ? s.vc : s.vocab;
         const bool large = vocab_large(vocab_tiles(piece, s.tokens, 256), vocab_tiles(piece, s.tokens, 128));
         s.tiles = (s.vocab + (large ? 255 : 127)) / (large ? 256 : 128);
+        join = with_grad && s.tokens <= kVocabJoinTokens && s.tiles <= kVocabJoinTiles && s.vc >= s.vocab;
         for (int64_t v0 = 0; v0 < s.vocab; v0 += s.vc)
-            vocab_logits<FMT, false>(vocab_piece(s, w, c, v0, st), s, w, large, st);
+            vocab_logits<FMT, false>(vocab_piece(s, w, c, v0, st), s, w, l, large, false, st);
         const unsigned b = grid_blocks((s.tokens + 63) / 64, kJoinBlock);
-        if (s.tokens <= kJoinMean)
-            vocab_join_kernel<true><<<b, kJoinBlock, 0, st>>>(s, w, g.coef, token_loss, loss, used);
-        else
-            vocab_join_kernel<false><<<b, kJoinBlock, 0, st>>>(s, w, g.coef, token_loss, loss, used);
+        if (!join && s.tokens <= kJoinMean)
+            vocab_join_kernel<true><<<b, kJoinBlock, 0, st>>>(s, w, l);
+        else if (!join)
+            vocab_join_kernel<false><<<b, kJoinBlock, 0, st>>>(s, w, l);
     }
     if (s.tokens == 0 || s.tokens > kJoinMean)
-        rows_mean_kernel<<<1, kMeanBlock, 0, st>>>(token_loss, s.tokens, w.used, g.coef, loss, used, 0);
+        rows_mean_kernel<<<1, kMeanBlock, 0, st>>>(l.token_loss, s.tokens, w.used, l.coef, l.loss, l.used, 0);
     if (launched() != DS_OK)
         return DS_ERR_HIP;
-    if (g.dhidden == nullptr && g.dweight == nullptr)
+    if (!with_grad)
         return DS_OK;
     for (int64_t v0 = 0; v0 < s.vocab; v0 += s.vc) {
         const VocabPiece p = vocab_piece(s, w, c, v0, st);
@@ -648,8 +705,8 @@ ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const 
         h.first = v0 == 0;
         h.last = v0 + p.rows == s.vocab;
         if (s.tokens > 0)
-            vocab_logits<FMT, true>(p, s, w, vocab_large(vocab_tiles(p.rows, s.tokens, 256), vocab_tiles(p.rows, s.tokens, 128)),
-                                    st);
+            vocab_logits<FMT, true>(p, s, w, l,
+                                    vocab_large(vocab_tiles(p.rows, s.tokens, 256), vocab_tiles(p.rows, s.tokens, 128)), join, st);
         // both gradients in one launch: the second fills what the first leaves free
         const bool dx = g.dhidden != nullptr && s.tokens > 0, dw = g.dweight != nullptr;
         auto tiles = [&](int tile, int64_t& x, int64_t& all) {
@@ -731,6 +788,6 @@ ds_status vocab_ce(const ds_scaler* scaler, const void* hidden, int64_t hs, cons
     }
     if (launched() != DS_OK)
         return DS_ERR_HIP;
-    return dt == DS_FP16 ? vocab_run<kF16>(s, w, c, g, token_loss, loss, used, st)
-                         : vocab_run<kBF16>(s, w, c, g, token_loss, loss, used, st);
+    const VocabLoss l{coef, token_loss, loss, used};
+    return dt == DS_FP16 ? vocab_run<kF16>(s, w, c, g, l, st) : vocab_run<kBF16>(s, w, c, g, l, st);
 }

@@ -43,6 +43,8 @@ class ExpertDispatch(TokenOperator):
             need = _lib.ds_dispatch_workspace_bytes(self.max_tokens, self.E, self.k)
             self._ws = torch.empty((need + 3) // 4, dtype=torch.int32, device=self.device)
         self.tokens = 0                     # of the last sort()
+        self._place = self.place.data_ptr()
+        self._at = (self.offsets.data_ptr(), self._place, self.source.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4)
 
     def _sorted(self, tokens, what):
         if tokens != self.tokens:
@@ -56,12 +58,12 @@ class ExpertDispatch(TokenOperator):
         size, at, stride = self._indices(chosen, (T, self.k), "chosen")
         if T > self.max_tokens:
             raise ValueError(f"chosen: {T} tokens, at most {self.max_tokens} were asked for")
-        rc = _lib.lib.ds_dispatch_sort(at, size, T, self.E, self.k, stride, self.offsets.data_ptr(), self.place.data_ptr(),
-                                       self.source.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4, self._stream())
+        rc = _lib.lib.ds_dispatch_sort(at, size, T, self.E, self.k, stride, *self._at, self._stream())
         if rc:
             _lib._ok(rc, "ds_dispatch_sort")
         self.tokens = T
-        self._keep(chosen)
+        if self.stream is not None:
+            self._keep(chosen)
         return self.offsets
 
     def _pair(self, tokens_side, sorted_side, names):
@@ -82,22 +84,24 @@ class ExpertDispatch(TokenOperator):
         """out[place[t, j]] = x[t].  ``x``: [tokens, width] in fp16, bf16 or fp32; ``out``: its type, at least tokens * k
         rows; rows behind the last one are left as they are."""
         dt, width, a, astride, b, bstride, n = self._pair(x, out, ("x", "out"))
-        rc = _lib.lib.ds_dispatch_gather(a, dt, self.tokens, self.k, width, astride, self.place.data_ptr(), b, bstride, n,
+        rc = _lib.lib.ds_dispatch_gather(a, dt, self.tokens, self.k, width, astride, self._place, b, bstride, n,
                                          self._stream())
         if rc:
             _lib._ok(rc, "ds_dispatch_gather")
-        self._keep(x, out)
+        if self.stream is not None:
+            self._keep(x, out)
         return out
 
     @on_its_device
     def gather_gradient(self, dout, dx):
         """dx[t] = sum_j dout[place[t, j]], the gradient of gather() by ``x``."""
         dt, width, a, astride, b, bstride, n = self._pair(dx, dout, ("dx", "dout"))
-        rc = _lib.lib.ds_dispatch_gather_grad(b, dt, self.tokens, self.k, width, bstride, n, self.place.data_ptr(), a,
+        rc = _lib.lib.ds_dispatch_gather_grad(b, dt, self.tokens, self.k, width, bstride, n, self._place, a,
                                               astride, self._stream())
         if rc:
             _lib._ok(rc, "ds_dispatch_gather_grad")
-        self._keep(dout, dx)
+        if self.stream is not None:
+            self._keep(dout, dx)
         return dx
 
     @on_its_device
@@ -106,11 +110,12 @@ class ExpertDispatch(TokenOperator):
         ``rows``: at least tokens * k rows; ``gates``: [tokens, k] in fp16, bf16 or fp32, not read for dropped choices."""
         dt, width, a, astride, b, bstride, n = self._pair(out, rows, ("out", "rows"))
         gt, g, _, gstride = self._rows(gates, self.k, "gates", rows=self.tokens)
-        rc = _lib.lib.ds_dispatch_combine(b, dt, self.tokens, self.k, width, bstride, n, self.place.data_ptr(), g, gt,
+        rc = _lib.lib.ds_dispatch_combine(b, dt, self.tokens, self.k, width, bstride, n, self._place, g, gt,
                                           gstride, a, astride, self._stream())
         if rc:
             _lib._ok(rc, "ds_dispatch_combine")
-        self._keep(rows, gates, out)
+        if self.stream is not None:
+            self._keep(rows, gates, out)
         return out
 
     @on_its_device
@@ -126,9 +131,10 @@ class ExpertDispatch(TokenOperator):
         if dg != gt:
             raise ValueError(f"dgates: expected {gates.dtype}, got {dgates.dtype}")
         rc = _lib.lib.ds_dispatch_combine_grad(a, dt, self.tokens, self.k, width, astride, b, bstride, min(n, dn),
-                                               self.place.data_ptr(), g, gt, gstride, d, dstride, e, estride,
+                                               self._place, g, gt, gstride, d, dstride, e, estride,
                                                self._stream())
         if rc:
             _lib._ok(rc, "ds_dispatch_combine_grad")
-        self._keep(dout, rows, gates, drows, dgates)
+        if self.stream is not None:
+            self._keep(dout, rows, gates, drows, dgates)
         return drows, dgates

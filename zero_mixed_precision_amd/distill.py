@@ -45,6 +45,7 @@ class TopLogitDistillation(TokenOperator):
             # its count of used rows starts at zero
             need = _lib.ds_distill_workspace_bytes(self.max_tokens)
             self._ws = torch.zeros((need + 7) // 8, dtype=torch.float64, device=self.device)
+        self._scratch = (self._ws.data_ptr(), self._ws.numel() * 8)
         self._at = (self.token_loss.data_ptr(), self.value.data_ptr(), self.used.data_ptr())
 
     def _call(self, logits, teacher, index, out, mask, scaler, accumulate):
@@ -60,10 +61,11 @@ class TopLogitDistillation(TokenOperator):
                 raise ValueError(f"out: expected {logits.dtype}, got {out.dtype}")
         rc = _lib.lib.ds_distill_loss(self._scaler(scaler), z, dt, T, self.vocab, stride, t, tt, tstride, i, size, istride,
                                       self.k, self._mask(mask, T), self.temperature, self.coef, *self._at, d, gstride,
-                                      bool(accumulate) and T > 0, self._ws.data_ptr(), self._ws.numel() * 8, self._stream())
+                                      bool(accumulate) and T > 0, *self._scratch, self._stream())
         if rc:
             _lib._ok(rc, "ds_distill_loss")
-        self._keep(logits, teacher, index, out, mask, scaler)
+        if self.stream is not None:
+            self._keep(logits, teacher, index, out, mask, scaler)
         return self.value
 
     @on_its_device

@@ -17,6 +17,7 @@ class TokenOperator:
             device = torch.device("cuda", torch.cuda.current_device())
         check_stream(stream, device)
         self.device, self._device, self._many = device, device.index, torch.cuda.device_count() > 1
+        self._index_types = (torch.int32, torch.int64)
 
     def _own(self):
         """The stream that the operator's arrays are made on."""
@@ -32,11 +33,12 @@ class TokenOperator:
         time is the host's: each property of a tensor is asked for once."""
         dt = _dtype_of(x, self.torch, what)
         shape = x.shape
+        if not x.is_cuda or x.get_device() != self._device:
+            self._here(x, what)
         if len(shape) != 2 or shape[1] != columns or (rows is not None and shape[0] != rows) or \
                 (least is not None and shape[0] < least):
             some = rows if rows is not None else "rows" if least is None else f"at least {least}"
             raise ValueError(f"{what}: expected [{some}, {columns}], got {tuple(shape)}")
-        self._here(x, what)
         n = shape[0]
         if n == 0:
             return dt, None, 0, columns
@@ -51,8 +53,8 @@ class TokenOperator:
 
     def _indices(self, x, shape, what):
         """(bytes of an index, address, row stride) of int32 or int64 indices."""
-        size = {self.torch.int32: 4, self.torch.int64: 8}.get(x.dtype)
-        if size is None or tuple(x.shape) != shape:
+        size = x.dtype.itemsize
+        if x.dtype not in self._index_types or tuple(x.shape) != shape:
             raise ValueError(f"{what}: expected {shape} int32 or int64 values, got {tuple(x.shape)} of {x.dtype}")
         self._here(x, what)
         columns = shape[1] if len(shape) == 2 else 1
@@ -91,8 +93,6 @@ class TokenOperator:
 
     def _keep(self, *tensors):
         """On a stream of its own: torch does not hand the tensors' memory out again before that stream has used it."""
-        if self.stream is None:
-            return
         from .checkpoint import torch_stream
         there = torch_stream(self.stream, self.torch)
         for x in tensors:

@@ -42,6 +42,7 @@ class VocabCrossEntropy(TokenOperator):
             self.used = torch.zeros((), dtype=torch.int32, device=self.device)
             self._ws_bytes = _lib.ds_vocab_ce_workspace_bytes(self.max_tokens, self.vocab, self.width)
             self._ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+        self._scratch = (self._ws.data_ptr(), self._ws_bytes)
         self._at = (self.token_loss.data_ptr(), self.value.data_ptr(), self.used.data_ptr())
 
     def _matrix(self, x, what, rows=None):
@@ -65,10 +66,11 @@ class VocabCrossEntropy(TokenOperator):
                 raise ValueError(f"dweight: expected {self.dtype} or float32, got {dweight.dtype}")
         rc = _lib.lib.ds_vocab_ce(self._scaler(scaler), h, hstride, w, wstride, dt, y, size, T, self.vocab, self.width,
                                   self._mask(mask, T), self.coef, *self._at, dh, dhstride, dw, dwt, dwstride,
-                                  bool(accumulate), self._ws.data_ptr(), self._ws_bytes, self._stream())
+                                  bool(accumulate), *self._scratch, self._stream())
         if rc:
             _lib._ok(rc, "ds_vocab_ce")
-        self._keep(hidden, weight, targets, dhidden, dweight, mask, scaler)
+        if self.stream is not None:
+            self._keep(hidden, weight, targets, dhidden, dweight, mask, scaler)
         return self.value
 
     @on_its_device
