@@ -70,7 +70,11 @@ struct TileOf {
 
     // The permutation of a row's pieces: 16 lanes that read one after another
     // meet all 64 banks (no conflict counted in either form).
-    static __device__ __forceinline__ int mix(int row) { return COLS ? (row & 3) << 2 : (row >> 1) & 7; }
+    static __device__ __forceinline__ int mix(int row)
+    {
+        static_assert(kPieces >= 8, "what the permutations move");
+        return !COLS ? (row >> 1) & 7 : kPieces >= 16 ? (row & 3) << 2 : (row & 3) << 1;
+    }
 
     uint32_t voff[kLoads];
 

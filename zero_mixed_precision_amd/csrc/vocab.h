@@ -25,6 +25,7 @@ constexpr int64_t kVocabMaxWidth = 65536;
 constexpr int64_t kVocabMaxStride = int64_t(1) << 22;   // of W read in place: offsets in a tile have 32 bits
 constexpr uint64_t kVocabPiece = uint64_t(1) << 29;     // bytes of a piece's dz
 constexpr int64_t kVocabMinPiece = 2048, kVocabMaxPiece = 32768;
+constexpr int64_t kVocabSmallTokens = 8192;             // up to so many, tiles of 64 x 64
 // Tiles of the two gradients that are to be there at once: where there are fewer,
 // a tile's sum is split over k and joined afterwards.
 constexpr int64_t kVocabBlocks = 512;
@@ -213,11 +214,23 @@ struct VocabPiece {
 // share of them (`first`, `step`).  Rows are always joined from kJoinWaves
 // shares, so that a loss has the same bits with and without the gradient.
 constexpr int kJoinWaves = 4;
+// JOIN of the logits kernel: its rows, and partial sums that a lane goes through
+// in the time of a launch.
+constexpr int kVocabJoinTokens = 128, kVocabJoinTiles = 32;
 __device__ __forceinline__ TopSum vocab_join(const VocabSizes& s, const VocabWork& w, int64_t n, int first, int step)
 {
     TopSum sum{kNegInf, 0.0f};
-    for (int64_t i = first; i < s.tiles; i += step)
-        sum = join(sum, w.part[i * s.tp + n], kLog2e);
+    for (int64_t i = first; i < s.tiles; i += 8 * step) {      // eight loads on their way
+        TopSum v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t at = i + u * step;
+            v[u] = at < s.tiles ? w.part[at * s.tp + n] : TopSum{kNegInf, 0.0f};
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            sum = join(sum, v[u], kLog2e);
+    }
     return sum;
 }
 
@@ -239,35 +252,35 @@ struct VocabLoss {
 
 // Logits of a piece and, at the end, (DZ) dz or else each row's maximum and sum
 // over the tile.  m: vocabulary, n: tokens.  JOIN (with DZ, for few tokens and a
-// small vocabulary): every block joins its rows' partial sums itself, the first
-// one has all rows and ends the loss, which saves a launch.
+// small vocabulary): every block joins all rows' partial sums itself, the last
+// one ends the loss, which saves a launch.
 template <int FMT, bool DZ, bool JOIN, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kernel(VocabPiece p, VocabSizes s, VocabWork w,
                                                                                 VocabLoss l)
 {
     using P = Product<FMT, false, false, BM, BN, WM, WN>;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[P::kLds];
-    __shared__ TopSum joined[JOIN ? BN : 1];
+    __shared__ TopSum joined[JOIN ? kVocabJoinTokens : 1];
     const int used = *w.used;
     int tm, tn;
     tile_of(static_cast<int>(blockIdx.x), static_cast<int>((p.rows + BM - 1) / BM), static_cast<int>((s.tokens + BN - 1) / BN),
             tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     if constexpr (JOIN) {
-        static_assert(DZ && P::kThreads >= BN, "a lane for each row");
+        static_assert(DZ && P::kThreads >= kVocabJoinTokens, "a lane for each row");
         const int n = static_cast<int>(threadIdx.x);
-        if (n < used && n < BN) {
+        if (n < used && n < kVocabJoinTokens) {
             float loss;
             TopSum sum = vocab_join(s, w, n, 0, kJoinWaves);
 #pragma unroll
             for (int i = 1; i < kJoinWaves; ++i)
                 sum = join(sum, vocab_join(s, w, n, i, kJoinWaves), kLog2e);
             joined[n] = vocab_row(w, n, sum, loss);
-            if (blockIdx.x == 0)
+            if (blockIdx.x + 1 == gridDim.x)
                 l.token_loss[w.list[n]] = loss;
         }
         __syncthreads();
-        if (blockIdx.x == 0) {
+        if (blockIdx.x + 1 == gridDim.x) {                     // the last one: a short tile, or none
             const float mean = rows_mean<P::kThreads>(l.token_loss, s.tokens, used, l.coef);
             if (threadIdx.x == 0) {
                 *l.loss = mean;
@@ -288,7 +301,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void vocab_logits_kerne
         const int y = on ? w.target[n] : -1;
         const int hit = y < 0 ? -1 : static_cast<int>(y - p.v0) - m0;
         if constexpr (DZ) {
-            const TopSum row = !on ? TopSum{0.0f, 0.0f} : JOIN ? joined[JOIN ? c.col(j) : 0] : w.row[n];
+            const TopSum row = !on ? TopSum{0.0f, 0.0f} : JOIN ? joined[JOIN ? n : 0] : w.row[n];
             constexpr float unit = FMT == kF16 ? 32768.0f : 1.0f;
 #pragma unroll
             for (int i = 0; i < P::MI; ++i)
@@ -604,8 +617,6 @@ bool vocab_sizes(int64_t tokens, int64_t vocab, int64_t width, VocabSizes* s)
     return true;
 }
 
-constexpr int kVocabMinTile = 128;         // of the vocabulary, for the partial sums' space
-
 // The workspace's arrays from `base` on, each 256-byte aligned; returns the
 // bytes, which are no fewer than those for fewer tokens (with larger pieces).
 uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
@@ -617,7 +628,8 @@ uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
         return p;
     };
     const uint64_t tp = static_cast<uint64_t>(s.tp), dp = static_cast<uint64_t>(s.dp), vmax = static_cast<uint64_t>(s.vmax);
-    const uint64_t tiles = (static_cast<uint64_t>(s.vocab) + kVocabMinTile - 1) / kVocabMinTile;
+    const uint64_t v64 = (static_cast<uint64_t>(s.vocab) + 63) / 64;   // tiles of 64 up to kVocabSmallTokens, else of 128
+    const uint64_t parts = std::max((v64 + 1) / 2 * tp, v64 * std::min(tp, static_cast<uint64_t>(kVocabSmallTokens)));
     const uint64_t piece = 2 * tp * static_cast<uint64_t>(s.vc), most = std::min(2 * tp * vmax, kVocabPiece);
     w->used = reinterpret_cast<int32_t*>(take(4));
     w->ticket = reinterpret_cast<uint32_t*>(take(4));
@@ -625,7 +637,7 @@ uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
     w->list = reinterpret_cast<int32_t*>(take(4 * tp));
     w->target = reinterpret_cast<int32_t*>(take(4 * tp));
     w->of_target = reinterpret_cast<float*>(take(4 * tp));
-    w->part = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * tp * tiles));
+    w->part = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * parts));
     w->row = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * tp));
     w->x = reinterpret_cast<uint16_t*>(take(2 * tp * dp));
     w->w = reinterpret_cast<uint16_t*>(take(2 * vmax * dp));
@@ -653,26 +665,32 @@ VocabPiece vocab_piece(const VocabSizes& s, const VocabWork& w, const VocabCall&
 
 int64_t vocab_tiles(int64_t m, int64_t n, int tile) { return ((m + tile - 1) / tile) * ((n + tile - 1) / tile); }
 
-// Whether tiles of 256 x 256 (one block a CU) are faster than such of 128 x 128
-// (two): the time of each in rounds of the GPU, a small tile costing 1 / 0.85 of a
-// quarter of a large one.
-bool vocab_large(int64_t large, int64_t small)
+// The side of a product's tiles, from how many there would be.  Up to 256 tiles
+// of 128 x 128 (a CU each) take tiles of 64 x 64: the blocks go through their k in
+// the same number of turns, each shorter, and have a quarter of the code to fetch
+// at the end.  Else 256 x 256 (one block a CU) or 128 x 128 (two), by the rounds
+// of the GPU, a tile of 128 costing 1 / 0.85 of a quarter of one of 256.
+int vocab_side(const VocabSizes& s, int64_t n128, int64_t n256)
 {
-    return 4.0 * static_cast<double>((large + 255) / 256) <= 2.0 / 0.85 * static_cast<double>((small + 511) / 512);
+    if (n128 <= 256 && s.tokens <= kVocabSmallTokens)
+        return 64;
+    return 4.0 * static_cast<double>((n256 + 255) / 256) <= 2.0 / 0.85 * static_cast<double>((n128 + 511) / 512) ? 256 : 128;
 }
 
-// JOIN of the logits kernel: rows of one tile, and partial sums that a lane goes
-// through in the time of a launch.
-constexpr int64_t kVocabJoinTokens = 128, kVocabJoinTiles = 32;
+int vocab_logits_side(const VocabSizes& s, int64_t rows)
+{
+    return vocab_side(s, vocab_tiles(rows, s.tokens, 128), vocab_tiles(rows, s.tokens, 256));
+}
 
 template <int FMT, bool DZ>
-void vocab_logits(const VocabPiece& p, const VocabSizes& s, const VocabWork& w, const VocabLoss& l, bool large, bool join,
+void vocab_logits(const VocabPiece& p, const VocabSizes& s, const VocabWork& w, const VocabLoss& l, int side, bool join,
                   hipStream_t st)
 {
-    const unsigned b = static_cast<unsigned>(vocab_tiles(p.rows, s.tokens, large ? 256 : 128));
-    if (DZ && join) vocab_logits_kernel<FMT, true, true, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w, l);
-    else if (large) vocab_logits_kernel<FMT, DZ, false, 256, 256, 64, 128><<<b, 512, 0, st>>>(p, s, w, l);
-    else            vocab_logits_kernel<FMT, DZ, false, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w, l);
+    const unsigned b = static_cast<unsigned>(vocab_tiles(p.rows, s.tokens, side));
+    if (DZ && join)       vocab_logits_kernel<FMT, true, true, 64, 64, 32, 32><<<b, 256, 0, st>>>(p, s, w, l);
+    else if (side == 64)  vocab_logits_kernel<FMT, DZ, false, 64, 64, 32, 32><<<b, 256, 0, st>>>(p, s, w, l);
+    else if (side == 128) vocab_logits_kernel<FMT, DZ, false, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w, l);
+    else                  vocab_logits_kernel<FMT, DZ, false, 256, 256, 64, 128><<<b, 512, 0, st>>>(p, s, w, l);
 }
 
 template <int FMT>
@@ -682,11 +700,11 @@ ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const 
     bool join = false;
     if (s.tokens > 0) {
         const int64_t piece = s.vc < s.vocab ? s.vc : s.vocab;
-        const bool large = vocab_large(vocab_tiles(piece, s.tokens, 256), vocab_tiles(piece, s.tokens, 128));
-        s.tiles = (s.vocab + (large ? 255 : 127)) / (large ? 256 : 128);
-        join = with_grad && s.tokens <= kVocabJoinTokens && s.tiles <= kVocabJoinTiles && s.vc >= s.vocab;
+        const int side = vocab_logits_side(s, piece);
+        s.tiles = (s.vocab + side - 1) / side;
+        join = with_grad && s.tokens <= kVocabJoinTokens && s.tiles <= kVocabJoinTiles && side == 64;
         for (int64_t v0 = 0; v0 < s.vocab; v0 += s.vc)
-            vocab_logits<FMT, false>(vocab_piece(s, w, c, v0, st), s, w, l, large, false, st);
+            vocab_logits<FMT, false>(vocab_piece(s, w, c, v0, st), s, w, l, side, false, st);
         const unsigned b = grid_blocks((s.tokens + 63) / 64, kJoinBlock);
         if (!join && s.tokens <= kJoinMean)
             vocab_join_kernel<true><<<b, kJoinBlock, 0, st>>>(s, w, l);
@@ -705,25 +723,26 @@ ds_status vocab_run(VocabSizes s, const VocabWork& w, const VocabCall& c, const 
         h.first = v0 == 0;
         h.last = v0 + p.rows == s.vocab;
         if (s.tokens > 0)
-            vocab_logits<FMT, true>(p, s, w, l,
-                                    vocab_large(vocab_tiles(p.rows, s.tokens, 256), vocab_tiles(p.rows, s.tokens, 128)), join, st);
+            vocab_logits<FMT, true>(p, s, w, l, vocab_logits_side(s, p.rows), join, st);
         // both gradients in one launch: the second fills what the first leaves free
         const bool dx = g.dhidden != nullptr && s.tokens > 0, dw = g.dweight != nullptr;
         auto tiles = [&](int tile, int64_t& x, int64_t& all) {
             x = dx ? vocab_tiles(s.dp, s.tokens, tile) * s.xs : 0;
             all = x + (dw ? vocab_tiles(s.dp, p.rows, tile) * s.ws : 0);
         };
-        int64_t x, all, x_large, all_large;
-        tiles(128, x, all);
-        tiles(256, x_large, all_large);
-        if (all == 0)
+        int64_t x, n128, n256;
+        tiles(256, x, n256);
+        tiles(128, x, n128);
+        if (n128 == 0)
             continue;
-        if (vocab_large(all_large, all))
-            vocab_grads_kernel<FMT, 256, 256, 64, 128><<<static_cast<unsigned>(all_large), 512, 0, st>>>(
-                p, s, w, h, static_cast<int32_t>(x_large));
-        else
-            vocab_grads_kernel<FMT, 128, 128, 64, 64><<<static_cast<unsigned>(all), 256, 0, st>>>(p, s, w, h,
-                                                                                                static_cast<int32_t>(x));
+        const int side = vocab_side(s, n128, n256);
+        int64_t all;
+        tiles(side, x, all);
+        const unsigned b = static_cast<unsigned>(all);
+        const int32_t tx = static_cast<int32_t>(x);
+        if (side == 64)       vocab_grads_kernel<FMT, 64, 64, 32, 32><<<b, 256, 0, st>>>(p, s, w, h, tx);
+        else if (side == 128) vocab_grads_kernel<FMT, 128, 128, 64, 64><<<b, 256, 0, st>>>(p, s, w, h, tx);
+        else                  vocab_grads_kernel<FMT, 256, 256, 64, 128><<<b, 512, 0, st>>>(p, s, w, h, tx);
         const int64_t xrows = dx && h.last && s.xs > 1 ? s.tokens : 0, wrows = dw && s.ws > 1 ? p.rows : 0;
         if (xrows + wrows > 0)
             vocab_parts_kernel<FMT><<<grid_blocks((xrows + wrows + 3) / 4, kPackBlock), kPackBlock, 0, st>>>(p, s, w, h, xrows,
