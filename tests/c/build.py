@@ -68,7 +68,23 @@ def build_list_checks() -> str:
     return LIST_OUT
 
 
+TOKENS_SRC = os.path.join(HERE, "tokens_checks.c")
+TOKENS_OUT = os.path.join(HERE, "tokens_checks")
+
+
+def build_tokens_checks() -> str:
+    """The host paths of the dispatch, distillation and cross-entropy entry points, linked against the sanitized library
+    that build_host_checks() made."""
+    clang = os.path.join(ROCM, "llvm", "bin", "clang")
+    cmd = [clang, "-std=c11", "-O1", "-g", "-Wall", "-Wextra", "-Werror", "-fsanitize=address,undefined",
+           "-fno-omit-frame-pointer", "-I", os.path.join(ROOT, "include"), TOKENS_SRC, "-o", TOKENS_OUT,
+           "-L", HERE, "-l:libdszero_asan.so", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    return TOKENS_OUT
+
+
 if __name__ == "__main__":
     print(build_driver())
     print(build_host_checks())
     print(build_list_checks())
+    print(build_tokens_checks())

@@ -180,12 +180,10 @@ __device__ __forceinline__ float wave_sum(float x)
     return x;
 }
 
-// A row's softmax as the gradient needs it: p = 2^(c x - ref) / sum, or, where
-// `exact`, 2^((x - top) c - log2 sum).  `by` is the gradient's factor, NaN where
-// the teacher's entries hold a NaN, `by_sum` that over the sum.
+// A row's softmax as the gradient needs it: p = 2^((x - top) c - log2 sum).
+// `by` is the gradient's factor, NaN where the teacher's entries hold one.
 struct DistillRow {
-    float top, c, ref, log_sum, by, by_sum;
-    bool exact;
+    float top, c, log_sum, by;
 };
 
 __device__ __forceinline__ float distill_p(float x, const DistillRow& r)
@@ -207,17 +205,9 @@ __device__ __forceinline__ void distill_write(unsigned char* out, uint32_t i, u3
     widen_vec<ZF>(v, x);
     if constexpr (ACC)
         widen_vec<ZF>(vector_at(out, i), o);
-    if (r.exact) {
 #pragma unroll
-        for (int m = 0; m < kVec; ++m)
-            x[m] = __builtin_fmaf(r.by, distill_p(x[m], r), o[m]);
-    } else {
-#pragma unroll
-        for (int m = 0; m < kVec; ++m) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[m], r.c, -r.ref));
-            x[m] = ACC ? __builtin_fmaf(r.by_sum, e, o[m]) : r.by_sum * e;
-        }
-    }
+    for (int m = 0; m < kVec; ++m)
+        x[m] = ACC ? __builtin_fmaf(r.by, distill_p(x[m], r), o[m]) : r.by * distill_p(x[m], r);
     v = narrow_vec<ZF>(x);
 #pragma unroll
     for (int m = 0; m < 4; ++m)
@@ -244,11 +234,12 @@ constexpr int kFewRows = 256;
 // The sum needs no maximum, only a reference that no logit exceeds by far: a
 // wave takes the largest of its first vectors.  With ref = c top rounded, 2^(c x
 // - ref) is one fused operation and an exponential, and as exact as from the
-// difference.  Where the sum says that the reference was none (nothing but
+// difference (the gradient takes the difference itself, which cannot overflow).
+// Where the sum says that the reference was none (nothing but
 // -infinity in the first vectors, a logit 2^64 times as likely as the reference,
 // values near the type's range, NaN), the row is summed again from its maximum,
 // differences first.
-template <int ZF, int BLOCK, int NV, bool GRAD, bool ACC, bool FEW>
+template <int ZF, int BLOCK, int NV, bool GRAD, bool ACC>
 __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
 {
     constexpr int ES = ZF == kF32 ? 4 : 2, kVec = 16 / ES, kWaves = BLOCK / 64;
@@ -261,8 +252,9 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
     __shared__ float shares[2][DS_MAX_TEACHER_LOGITS];
     __shared__ float of_logit[DS_MAX_TEACHER_LOGITS];
     __shared__ float old[ACC ? DS_MAX_TEACHER_LOGITS : 1];
-    __shared__ uint8_t few[FEW ? kFewRows : 1];
-    __shared__ int32_t few_used[FEW ? kWaves : 1];
+    __shared__ uint8_t few[kFewRows];
+    __shared__ int32_t few_used[kWaves];
+    const bool is_few = s.tokens <= kFewRows;
     const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(__lane_id());
     const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int vecs = static_cast<int>(s.vocab / kVec);
@@ -291,7 +283,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
         }
         if (tid < rest_lanes)
             last = load_elem<ZF>(s.logits, t * s.stride + rest + tid);
-        if constexpr (!FEW)
+        if (!is_few)
             flag = s.flag[t];
     };
     load_entry(min(static_cast<int64_t>(blockIdx.x), s.tokens - 1));
@@ -301,7 +293,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
             load_one(min(static_cast<int64_t>(blockIdx.x), s.tokens - 1), n);
     }
     int32_t used = 0;
-    if constexpr (FEW) {
+    if (is_few) {
         int32_t mine = 0;
         for (int64_t t0 = 0; t0 < s.tokens; t0 += BLOCK) {
             const bool on = distill_used<ZF>(s, t0 + tid, lane);
@@ -327,9 +319,9 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
         unsigned char* out = GRAD ? s.grad + t * s.gs * ES : nullptr;
         const int64_t next = min(t + gridDim.x, s.tokens - 1);
         // the same for the whole block
-        const bool on = __builtin_amdgcn_readfirstlane(FEW ? few[t & (kFewRows - 1)] : flag) != 0;
+        const bool on = __builtin_amdgcn_readfirstlane(is_few ? few[t & (kFewRows - 1)] : flag) != 0;
         const float mine = last;
-        DistillRow row{0.0f, c, 0.0f, 0.0f, 0.0f, 0.0f, false};
+        DistillRow row{0.0f, c, 0.0f, 0.0f};
         float loss = 0.0f, fine = 1.0f;
         int here = -1;                                         // the first entry's place, and the rest that is the lane's
         float logit_here = 0.0f, old_here = 0.0f, share_here = 0.0f;
@@ -421,19 +413,21 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
 #pragma unroll
             for (int w = 1; w < kWaves; ++w)
                 row.top = fmaxf(row.top, of_row[w].top);
-            row.ref = row.top * c;
+            const float row_ref = row.top * c;
             float total_sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
                 total_sum += of_row[w].top == kNegInf ? of_row[w].sum
-                                                      : of_row[w].sum * __builtin_amdgcn_exp2f(of_row[w].top * c - row.ref);
-            row.exact = !(total_sum >= 0.5f && total_sum <= 0x1p64f && fabsf(row.ref) <= 0x1p126f);
+                                                      : of_row[w].sum * __builtin_amdgcn_exp2f(of_row[w].top * c - row_ref);
+            const bool fits = total_sum >= 0.5f && total_sum <= 0x1p64f && fabsf(row_ref) <= 0x1p126f;
             theirs = of_teacher[0];
             for (int w = 1; w < kWaves && w * 64 < s.k; ++w)
                 theirs = join(theirs, of_teacher[w], c);
-            if (row.exact) {
+            if (!fits) {                                       // seldom: from memory, in short code
                 float most = mine;
-                each([&](u32x4 vec, bool) { most = fmaxf(most, top_of<ZF>(vec)); });
+#pragma unroll 1
+                for (int i = tid; i < vecs; i += BLOCK)
+                    most = fmaxf(most, top_of<ZF>(vector_at(in, i)));
                 most = wave_max(most);
                 __syncthreads();                               // the sums above have been read
                 if (lane == 0)
@@ -442,12 +436,14 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
                 for (int w = 0; w < kWaves; ++w)
                     most = fmaxf(most, of_row[w].top);
                 sum = __builtin_amdgcn_exp2f((mine - most) * c);
-                each([&](u32x4 vec, bool has) {
+#pragma unroll 1
+                for (int i = tid; i < vecs; i += BLOCK) {
                     float x[kVec];
-                    widen_vec<ZF>(vec, x);
-                    for (int i = 0; i < kVec; ++i)
-                        sum = sum + (has ? __builtin_amdgcn_exp2f((x[i] - most) * c) : 0.0f);
-                });
+                    widen_vec<ZF>(vector_at(in, i), x);
+#pragma unroll
+                    for (int m = 0; m < kVec; ++m)
+                        sum = sum + __builtin_amdgcn_exp2f((x[m] - most) * c);
+                }
                 sum = wave_sum(sum);
                 if (lane == 0)
                     of_row[wave].sum = sum;
@@ -462,10 +458,9 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
             // 1, or NaN where the teacher's entries hold a NaN or +infinity
             fine = theirs.sum * __builtin_amdgcn_rcpf(theirs.sum) > 0.0f ? 1.0f : __builtin_nanf("");
             row.by = factor * fine;
-            row.by_sum = row.by / total_sum;
             // what the reference's rounding has added to the sum's logarithm
-            if (!row.exact)
-                row.log_sum -= __builtin_fmaf(row.top, c, -row.ref);
+            if (fits)
+                row.log_sum -= __builtin_fmaf(row.top, c, -row_ref);
             auto take_share = [&](float x, int p, float z) {
                 const float q = x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((x - theirs.top) * c - log_theirs);
                 // in natural logarithms: a difference near the type's range does not fit times log2(e)
@@ -548,7 +543,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
             }
         }
     }
-    if constexpr (FEW) {
+    if (is_few) {
         __shared__ uint32_t ticket;
         uint32_t* done = reinterpret_cast<uint32_t*>(s.count) + 1;
         if (gridDim.x > 1) {
@@ -587,22 +582,16 @@ void launch_distill2(int per_cu, hipStream_t st, const Distill& s, bool accumula
 {
     const int64_t most = 256 * static_cast<int64_t>(per_cu), turns = (s.tokens + most - 1) / most;
     const unsigned b = grid_blocks((s.tokens + turns - 1) / turns, BLOCK);
-    if (s.tokens <= kFewRows) {
-        if (s.grad == nullptr) distill_kernel<ZF, BLOCK, NV, false, false, true><<<b, BLOCK, 0, st>>>(s);
-        else if (accumulate)   distill_kernel<ZF, BLOCK, NV, true, true, true><<<b, BLOCK, 0, st>>>(s);
-        else                   distill_kernel<ZF, BLOCK, NV, true, false, true><<<b, BLOCK, 0, st>>>(s);
-    } else {
-        if (s.grad == nullptr) distill_kernel<ZF, BLOCK, NV, false, false, false><<<b, BLOCK, 0, st>>>(s);
-        else if (accumulate)   distill_kernel<ZF, BLOCK, NV, true, true, false><<<b, BLOCK, 0, st>>>(s);
-        else                   distill_kernel<ZF, BLOCK, NV, true, false, false><<<b, BLOCK, 0, st>>>(s);
-    }
+    if (s.grad == nullptr) distill_kernel<ZF, BLOCK, NV, false, false><<<b, BLOCK, 0, st>>>(s);
+    else if (accumulate)   distill_kernel<ZF, BLOCK, NV, true, true><<<b, BLOCK, 0, st>>>(s);
+    else                   distill_kernel<ZF, BLOCK, NV, true, false><<<b, BLOCK, 0, st>>>(s);
 }
 
 template <int ZF>
 void launch_distill(hipStream_t st, const Distill& s, bool accumulate)
 {
     const int64_t vecs = s.vocab / (ZF == kF32 ? 4 : 8);
-    if (vecs < 1)           launch_distill2<ZF, 64, kTwice>(8, st, s, accumulate);
+    if (vecs < 1)           launch_distill2<ZF, 1024, kTwice>(1, st, s, accumulate);
     else if (vecs <= 256)   launch_distill2<ZF, 64, 4>(12, st, s, accumulate);
     else if (vecs <= 1024)  launch_distill2<ZF, 256, 4>(6, st, s, accumulate);
     else if (vecs <= 4096)  launch_distill2<ZF, 512, 8>(2, st, s, accumulate);

@@ -619,11 +619,11 @@ bool vocab_sizes(int64_t tokens, int64_t vocab, int64_t width, VocabSizes* s)
 
 // The workspace's arrays from `base` on, each 256-byte aligned; returns the
 // bytes, which are no fewer than those for fewer tokens (with larger pieces).
-uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
+uint64_t vocab_work(const VocabSizes& s, void* base, VocabWork* w)
 {
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
-        unsigned char* p = base + at;
+        void* p = reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(base) + at);
         at += (bytes + 255) / 256 * 256;
         return p;
     };
@@ -631,19 +631,19 @@ uint64_t vocab_work(const VocabSizes& s, unsigned char* base, VocabWork* w)
     const uint64_t v64 = (static_cast<uint64_t>(s.vocab) + 63) / 64;   // tiles of 64 up to kVocabSmallTokens, else of 128
     const uint64_t parts = std::max((v64 + 1) / 2 * tp, v64 * std::min(tp, static_cast<uint64_t>(kVocabSmallTokens)));
     const uint64_t piece = 2 * tp * static_cast<uint64_t>(s.vc), most = std::min(2 * tp * vmax, kVocabPiece);
-    w->used = reinterpret_cast<int32_t*>(take(4));
-    w->ticket = reinterpret_cast<uint32_t*>(take(4));
-    w->slot = reinterpret_cast<int32_t*>(take(4 * tp));
-    w->list = reinterpret_cast<int32_t*>(take(4 * tp));
-    w->target = reinterpret_cast<int32_t*>(take(4 * tp));
-    w->of_target = reinterpret_cast<float*>(take(4 * tp));
-    w->part = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * parts));
-    w->row = reinterpret_cast<TopSum*>(take(sizeof(TopSum) * tp));
-    w->x = reinterpret_cast<uint16_t*>(take(2 * tp * dp));
-    w->w = reinterpret_cast<uint16_t*>(take(2 * vmax * dp));
-    w->dz = reinterpret_cast<uint16_t*>(take(std::max(piece, most)));
-    w->dx = reinterpret_cast<float*>(take(std::max(kVocabParts, s.vc < s.vocab ? 4 * tp * dp : 0)));
-    w->dw = reinterpret_cast<float*>(take(kVocabParts));
+    w->used = static_cast<int32_t*>(take(4));
+    w->ticket = static_cast<uint32_t*>(take(4));
+    w->slot = static_cast<int32_t*>(take(4 * tp));
+    w->list = static_cast<int32_t*>(take(4 * tp));
+    w->target = static_cast<int32_t*>(take(4 * tp));
+    w->of_target = static_cast<float*>(take(4 * tp));
+    w->part = static_cast<TopSum*>(take(sizeof(TopSum) * parts));
+    w->row = static_cast<TopSum*>(take(sizeof(TopSum) * tp));
+    w->x = static_cast<uint16_t*>(take(2 * tp * dp));
+    w->w = static_cast<uint16_t*>(take(2 * vmax * dp));
+    w->dz = static_cast<uint16_t*>(take(std::max(piece, most)));
+    w->dx = static_cast<float*>(take(std::max(kVocabParts, s.vc < s.vocab ? 4 * tp * dp : 0)));
+    w->dw = static_cast<float*>(take(kVocabParts));
     return at;
 }
 
@@ -775,7 +775,7 @@ ds_status vocab_ce(const ds_scaler* scaler, const void* hidden, int64_t hs, cons
         !aligned(workspace, 256))
         return DS_ERR_ALIGN;
     VocabWork w;
-    const uint64_t need = vocab_work(s, static_cast<unsigned char*>(workspace), &w);
+    const uint64_t need = vocab_work(s, workspace, &w);
     if (bytes < need)
         return DS_ERR_SIZE;
     const uint64_t ut = static_cast<uint64_t>(tokens);
