@@ -154,3 +154,60 @@ def test_the_example_and_its_layers_gradients():
     assert float((y.detach().double() - want).norm() / want.norm()) <= 8 * 2.0 ** -8
     for p, w in zip((x, *layer.parameters()), grads):
         assert float((p.grad.double() - w).norm() / w.norm()) <= 8 * 2.0 ** -8
+
+
+def test_the_binding_gives_the_classes_results():
+    """The entry points under their C names, with strided tensors, against the classes."""
+    from zero_mixed_precision_amd import _lib
+
+    params, x, targets, mask, teacher, index = data(torch.bfloat16)
+    head, bf, f32 = params[-1], _lib.DS_BF16, _lib.DS_FP32
+    ce = VocabCrossEntropy(V, D, T, torch.bfloat16, coef=0.5)
+    dx, dhead = torch.empty_like(x), torch.empty_like(head)
+    ce.loss_and_gradient(x, head, targets, dx, dhead, mask=mask)
+    token_loss, loss, used = (torch.empty(n, dtype=d, device=DEV) for n, d in ((T, torch.float32), (1, torch.float32),
+                                                                              (1, torch.int32)))
+    ws = torch.empty(_lib.ds_vocab_ce_workspace_bytes(T, V, D), dtype=torch.uint8, device=DEV)
+    wide, dx2, dhead2 = torch.cat([x, x], 1)[:, :D], torch.empty_like(x), torch.empty_like(head)
+    _lib.ds_vocab_ce(None, wide, 2 * D, head, D, bf, targets, 8, T, V, D, mask, 0.5, token_loss, loss, used, dx2, D, dhead2, bf,
+                     D, False, ws)
+    assert torch.equal(dx, dx2) and torch.equal(dhead, dhead2) and torch.equal(loss[0], ce.value)
+
+    logits = x @ head.t()
+    distill = TopLogitDistillation(V, N, T, temperature=TAU)
+    d, d2 = torch.empty_like(logits), torch.empty_like(logits)
+    distill.loss_and_gradient(logits, teacher, index, d, mask=mask)
+    ws = torch.zeros((_lib.ds_distill_workspace_bytes(T) + 7) // 8, dtype=torch.float64, device=DEV)
+    _lib.ds_distill_loss(None, logits, bf, T, V, V, teacher, f32, N, index, 8, N, N, mask, TAU, 1.0, token_loss, loss, used, d2,
+                         V, False, ws)
+    assert torch.equal(d, d2) and torch.equal(loss[0], distill.value)
+
+    chosen = index[:, :K] % E
+    op = ExpertDispatch(E, K, T)
+    offsets = op.sort(chosen)
+    rows, y, gates = torch.zeros(T * K, D, dtype=x.dtype, device=DEV), torch.empty_like(x), torch.rand(T, K, device=DEV)
+    op.gather(x, rows)
+    op.combine(rows, gates, y)
+    drows, dgates = op.combine_gradient(x, rows, gates, torch.zeros_like(rows), torch.empty_like(gates))
+    dx = op.gather_gradient(rows, torch.empty_like(x))
+    ints = lambda n: torch.empty(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    o2, place, source, ws = ints(E + 1), ints(T * K), ints(T * K), ints(_lib.ds_dispatch_workspace_bytes(T, E, K) // 4)
+    r2, y2, dr2, dg2, dx2 = (torch.zeros_like(a) for a in (rows, y, drows, dgates, dx))
+    strided = index[:, :K] % E
+    wide = torch.cat([strided, strided], 1)
+    _lib.ds_dispatch_sort(wide[:, :K], 8, T, E, K, 2 * K, o2, place, source, ws)
+    _lib.ds_dispatch_gather(x, bf, T, K, D, D, place, r2, D, T * K)
+    _lib.ds_dispatch_combine(r2, bf, T, K, D, D, T * K, place, gates, f32, K, y2, D)
+    _lib.ds_dispatch_combine_grad(x, bf, T, K, D, D, r2, D, T * K, place, gates, f32, K, dr2, D, dg2, K)
+    _lib.ds_dispatch_gather_grad(r2, bf, T, K, D, D, T * K, place, dx2, D)
+    for a, b in ((offsets, o2), (op.place.view(-1), place), (op.source, source), (rows, r2), (y, y2), (drows, dr2),
+                 (dgates, dg2), (dx, dx2)):
+        assert torch.equal(a, b)
+    for bad in (lambda: _lib.ds_dispatch_gather(x.cpu(), bf, T, K, D, D, place, r2, D, T * K),
+                lambda: _lib.ds_dispatch_sort(wide[:, :K], 8, T, E, K, K, o2, place, source, ws),
+                lambda: _lib.ds_distill_loss(None, logits, bf, T, V + 1, V + 1, teacher, f32, N, index, 8, N, N, mask, TAU, 1.0,
+                                             token_loss, loss, used, None, 0, False, ws),
+                lambda: _lib.ds_vocab_ce(None, x, D, head, D, bf, targets.int(), 8, T, V, D, mask, 0.5, token_loss, loss, used,
+                                         dx2, D, None, bf, 0, False, ws)):
+        with pytest.raises(ValueError):
+            bad()

@@ -522,20 +522,25 @@ def ds_balance_workspace_bytes(tokens, experts) -> int:
     return lib.ds_balance_workspace_bytes(int(tokens), int(experts))
 
 
-def _rows(x, dtype, tokens, experts, stride, what):
-    """Address of a strided [tokens, experts] matrix: an int, or a GPU tensor with unit stride inside its rows."""
+def _matrix(x, size, rows, columns, stride, what):
+    """Address of a strided [rows, columns] matrix of values of ``size`` bytes: an int, or a GPU tensor with unit stride
+    inside its rows."""
     if x is None or isinstance(x, int):
         return x
     if not getattr(x, "is_cuda", False):
         raise ValueError(f"{what}: expected a tensor in GPU memory, got one on {x.device}")
-    if tokens > 0:
+    if rows > 0:
         shape = tuple(x.shape)
-        if len(shape) != 2 or shape[0] < tokens or shape[1] < experts or x.element_size() != _esize(dtype):
-            raise ValueError(f"{what}: expected [{tokens}, {experts}] values of {_esize(dtype)} bytes, got {shape} of "
+        if len(shape) != 2 or shape[0] < rows or shape[1] < columns or x.element_size() != size:
+            raise ValueError(f"{what}: expected [{rows}, {columns}] values of {size} bytes, got {shape} of "
                              f"{x.element_size()}")
-        if (experts > 1 and x.stride(1) != 1) or (tokens > 1 and x.stride(0) != stride):
+        if (columns > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) != stride):
             raise ValueError(f"{what}: expected strides ({stride}, 1), got {tuple(x.stride())}")
     return x.data_ptr()
+
+
+def _rows(x, dtype, tokens, experts, stride, what):
+    return _matrix(x, _esize(dtype), tokens, experts, stride, what)
 
 
 def ds_balance_loss(logits, dtype, tokens, experts, row_stride, mask, k, coef, counts, mean_prob, loss, used, workspace,
@@ -562,12 +567,90 @@ def ds_dispatch_workspace_bytes(tokens, experts, k) -> int:
     return lib.ds_dispatch_workspace_bytes(int(tokens), int(experts), int(k))
 
 
+def ds_dispatch_sort(chosen, index_bytes, tokens, experts, k, row_stride, offsets, place, source, workspace,
+                     workspace_bytes=None, stream=None) -> None:
+    T, E, k = int(tokens), int(experts), int(k)
+    _ok(lib.ds_dispatch_sort(_matrix(chosen, int(index_bytes), T, k, int(row_stride), "chosen"), int(index_bytes), T, E, k,
+                             int(row_stride), _p(offsets, 4 * (E + 1), "offsets"), _p(place, 4 * T * k, "place"),
+                             _p(source, 4 * T * k, "source"),
+                             _p(workspace, ds_dispatch_workspace_bytes(T, E, k), "workspace"),
+                             _nbytes(workspace, workspace_bytes), _s(stream)), "ds_dispatch_sort")
+
+
+def ds_dispatch_gather(x, dtype, tokens, k, width, x_stride, place, out, out_stride, out_rows, stream=None) -> None:
+    T, k, D, n = int(tokens), int(k), int(width), int(out_rows)
+    _ok(lib.ds_dispatch_gather(_rows(x, dtype, T, D, int(x_stride), "x"), int(dtype), T, k, D, int(x_stride),
+                               _p(place, 4 * T * k, "place"), _rows(out, dtype, n, D, int(out_stride), "out"),
+                               int(out_stride), n, _s(stream)), "ds_dispatch_gather")
+
+
+def ds_dispatch_gather_grad(dout, dtype, tokens, k, width, dout_stride, dout_rows, place, dx, dx_stride,
+                            stream=None) -> None:
+    T, k, D, n = int(tokens), int(k), int(width), int(dout_rows)
+    _ok(lib.ds_dispatch_gather_grad(_rows(dout, dtype, n, D, int(dout_stride), "dout"), int(dtype), T, k, D,
+                                    int(dout_stride), n, _p(place, 4 * T * k, "place"),
+                                    _rows(dx, dtype, T, D, int(dx_stride), "dx"), int(dx_stride), _s(stream)),
+        "ds_dispatch_gather_grad")
+
+
+def ds_dispatch_combine(rows, dtype, tokens, k, width, rows_stride, rows_count, place, gates, gates_dtype, gates_stride, out,
+                        out_stride, stream=None) -> None:
+    T, k, D, n = int(tokens), int(k), int(width), int(rows_count)
+    _ok(lib.ds_dispatch_combine(_rows(rows, dtype, n, D, int(rows_stride), "rows"), int(dtype), T, k, D, int(rows_stride), n,
+                                _p(place, 4 * T * k, "place"),
+                                _rows(gates, gates_dtype, T, k, int(gates_stride), "gates"), int(gates_dtype),
+                                int(gates_stride), _rows(out, dtype, T, D, int(out_stride), "out"), int(out_stride),
+                                _s(stream)), "ds_dispatch_combine")
+
+
+def ds_dispatch_combine_grad(dout, dtype, tokens, k, width, dout_stride, rows, rows_stride, rows_count, place, gates,
+                             gates_dtype, gates_stride, drows, drows_stride, dgates, dgates_stride, stream=None) -> None:
+    T, k, D, n = int(tokens), int(k), int(width), int(rows_count)
+    _ok(lib.ds_dispatch_combine_grad(_rows(dout, dtype, T, D, int(dout_stride), "dout"), int(dtype), T, k, D,
+                                     int(dout_stride), _rows(rows, dtype, n, D, int(rows_stride), "rows"), int(rows_stride),
+                                     n, _p(place, 4 * T * k, "place"),
+                                     _rows(gates, gates_dtype, T, k, int(gates_stride), "gates"), int(gates_dtype),
+                                     int(gates_stride), _rows(drows, dtype, n, D, int(drows_stride), "drows"),
+                                     int(drows_stride), _rows(dgates, gates_dtype, T, k, int(dgates_stride), "dgates"),
+                                     int(dgates_stride), _s(stream)), "ds_dispatch_combine_grad")
+
+
 def ds_distill_workspace_bytes(tokens) -> int:
     return lib.ds_distill_workspace_bytes(int(tokens))
 
 
+def ds_distill_loss(st_or_null, logits, dtype, tokens, vocab, row_stride, teacher, teacher_dtype, teacher_stride, index,
+                    index_bytes, index_stride, k, mask, temperature, coef, token_loss, loss, used, dlogits, grad_stride,
+                    accumulate, workspace, workspace_bytes=None, stream=None) -> None:
+    T, V, k = int(tokens), int(vocab), int(k)
+    _ok(lib.ds_distill_loss(_scaler(st_or_null), _rows(logits, dtype, T, V, int(row_stride), "logits"), int(dtype), T, V,
+                            int(row_stride), _rows(teacher, teacher_dtype, T, k, int(teacher_stride), "teacher"),
+                            int(teacher_dtype), int(teacher_stride),
+                            _matrix(index, int(index_bytes), T, k, int(index_stride), "index"), int(index_bytes),
+                            int(index_stride), k, _p(mask, T, "mask"), temperature, coef, _p(token_loss, 4 * T, "token_loss"),
+                            _p(loss, 4, "loss"), _p(used, 4, "used"),
+                            _rows(dlogits, dtype, T, V, int(grad_stride), "dlogits"), int(grad_stride),
+                            int(bool(accumulate)), _p(workspace, ds_distill_workspace_bytes(T), "workspace"),
+                            _nbytes(workspace, workspace_bytes), _s(stream)), "ds_distill_loss")
+
+
 def ds_vocab_ce_workspace_bytes(tokens, vocab, width) -> int:
     return lib.ds_vocab_ce_workspace_bytes(int(tokens), int(vocab), int(width))
+
+
+def ds_vocab_ce(st_or_null, hidden, hidden_stride, weight, weight_stride, dtype, targets, index_bytes, tokens, vocab, width,
+                mask, coef, token_loss, loss, used, dhidden, dhidden_stride, dweight, dweight_dtype, dweight_stride, accumulate,
+                workspace, workspace_bytes=None, stream=None) -> None:
+    T, V, D = int(tokens), int(vocab), int(width)
+    _ok(lib.ds_vocab_ce(_scaler(st_or_null), _rows(hidden, dtype, T, D, int(hidden_stride), "hidden"), int(hidden_stride),
+                        _rows(weight, dtype, V, D, int(weight_stride), "weight"), int(weight_stride), int(dtype),
+                        _p(targets, int(index_bytes) * T, "targets"), int(index_bytes), T, V, D, _p(mask, T, "mask"), coef,
+                        _p(token_loss, 4 * T, "token_loss"), _p(loss, 4, "loss"), _p(used, 4, "used"),
+                        _rows(dhidden, dtype, T, D, int(dhidden_stride), "dhidden"), int(dhidden_stride),
+                        _rows(dweight, dweight_dtype, V, D, int(dweight_stride), "dweight"), int(dweight_dtype),
+                        int(dweight_stride), int(bool(accumulate)),
+                        _p(workspace, ds_vocab_ce_workspace_bytes(T, V, D), "workspace"),
+                        _nbytes(workspace, workspace_bytes), _s(stream)), "ds_vocab_ce")
 
 
 def ds_layout_greedy(numels, cap, align):

@@ -24,7 +24,8 @@ constexpr int64_t kVocabMaxVocab = int64_t(1) << 24;
 constexpr int64_t kVocabMaxWidth = 65536;
 constexpr int64_t kVocabMaxStride = int64_t(1) << 22;   // of W read in place: offsets in a tile have 32 bits
 constexpr uint64_t kVocabPiece = uint64_t(1) << 29;     // bytes of a piece's dz
-constexpr int64_t kVocabMinPiece = 2048, kVocabMaxPiece = 32768;
+constexpr int64_t kVocabMinPiece = 2048, kVocabWidePiece = 32768;   // a piece of at least so much, or
+constexpr int64_t kVocabWeights = int64_t(1) << 27;     // so many values of W
 constexpr int64_t kVocabSmallTokens = 8192;             // up to so many, tiles of 64 x 64
 // Tiles of the two gradients that are to be there at once: where there are fewer,
 // a tile's sum is split over k and joined afterwards.
@@ -606,10 +607,11 @@ bool vocab_sizes(int64_t tokens, int64_t vocab, int64_t width, VocabSizes* s)
     s->tp = up_to(tokens > 0 ? tokens : 1, kVocabTile);
     s->dp = up_to(width, kBK);
     const int64_t whole = up_to(vocab, kVocabTile);
-    s->vmax = whole < kVocabMaxPiece ? whole : kVocabMaxPiece;
+    s->vmax = std::min(whole, std::max(kVocabWidePiece, kVocabWeights / s->dp / kVocabTile * kVocabTile));
     int64_t vc = static_cast<int64_t>(kVocabPiece / (2 * static_cast<uint64_t>(s->tp))) / kVocabTile * kVocabTile;
-    vc = vc < kVocabMinPiece ? kVocabMinPiece : vc;
-    s->vc = vc < s->vmax ? vc : s->vmax;
+    vc = std::min(std::max(vc, kVocabMinPiece), s->vmax);
+    const int64_t pieces = (vocab + vc - 1) / vc;           // of about the same size
+    s->vc = up_to((vocab + pieces - 1) / pieces, kVocabTile);
     s->tiles = 0;
     const int64_t dt = (s->dp + 127) / 128;
     s->xs = vocab_split(dt * ((s->tp + 127) / 128), s->vc / kBK);

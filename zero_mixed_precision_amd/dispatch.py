@@ -25,6 +25,8 @@ class ExpertDispatch(TokenOperator):
     [max_tokens * k]: the choice t * k + j of each row, -1 behind the last one).  They are overwritten by the next sort(),
     and the moves go by them: a layer whose gradient is still to come keeps its own object.
 
+    Calls of one object go by the same arrays: one after another, on one stream.
+
     ``stream``: a stream of its own (default: torch's current one).  The caller orders it after what writes the inputs,
     and what reads the results after it; the inputs may be freed as soon as a call returns."""
 

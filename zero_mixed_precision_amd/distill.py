@@ -23,6 +23,8 @@ class TopLogitDistillation(TokenOperator):
 
     ``k``: teacher's entries per row (1..1024; rows may have fewer: a negative place is an absent entry).
 
+    Calls of one object share its workspace and results: one after another, on one stream.
+
     ``stream``: a stream of its own (default: torch's current one).  The caller orders it after what writes the inputs,
     and what reads the results after it; the inputs may be freed as soon as a call returns."""
 

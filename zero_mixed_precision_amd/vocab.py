@@ -23,6 +23,8 @@ class VocabCrossEntropy(TokenOperator):
 
     ``dtype``: torch.float16 or torch.bfloat16, of hidden states and weight.  The workspace is allocated here, once.
 
+    Calls of one object share its workspace and results: one after another, on one stream.
+
     ``stream``: a stream of its own (default: torch's current one).  The caller orders it after what writes the inputs,
     and what reads the results after it; the inputs may be freed as soon as a call returns."""
 
