@@ -181,6 +181,83 @@ struct Product {
         load(0, 0);
         loads_done();
         __syncthreads();
+        if constexpr (kWaves == 8)
+            in_turns(lds, load, ktiles);
+        else
+            in_step(lds, load, ktiles);
+        __syncthreads();
+    }
+
+    // A SIMD has two waves, one of either half.  The halves take turns: one reads
+    // its fragments of 32 k (and sends off the next tile's loads), the other
+    // multiplies; all meet behind each turn, the second half one turn behind.  A
+    // tile's place is free once the second half has read its last fragments, in the
+    // turn before the first half sends off the loads that go there; at that turn's
+    // end either half has also waited for its own loads of the next tile, so that
+    // both may read it.  Rows and rows 32768 x 4096 x 4096 / columns and rows 4096 x
+    // 8192 x 16384 / columns 4096 x 16384 x 8192 reach 1110 / 1260 / 1230 TFLOP/s,
+    // 1075 / 1180 / 1190 with all waves in step, 1300 to 1490 with the loads of all
+    // tiles but the first left out; the cross entropy of 8192 x 131072 x 4096 takes
+    // 28.4 ms, 29.5 in step.  Turns of 16 k gain nothing over in step.
+    template <typename Load>
+    __device__ __forceinline__ void in_turns(const unsigned char* lds, Load load, int ktiles)
+    {
+        constexpr int kSteps = 2;                              // of 16 k, in a turn
+        const bool second = wave >= kWaves / 2;
+        auto meet = [] {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (second)
+            meet();
+        uint32_t now = 0;
+        for (int kt = 0; kt < ktiles; ++kt) {
+            const unsigned char* la = lds + now;
+            const unsigned char* lb = la + TA::kBytes;
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; kk += kSteps) {
+                constexpr int kLast = kBK / 16 - kSteps;
+                u32x4 fa[kSteps][MI], fb[kSteps][NI];
+#pragma unroll
+                for (int h = 0; h < kSteps; ++h) {
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+                        fa[h][i] = TA::frag(la, wm, i, kk + h, lane);
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+                        fb[h][j] = TB::frag(lb, wn, j, kk + h, lane);
+                }
+                if (kk == 0 && kt + 1 < ktiles)
+                    load(kt + 1, now ^ kStage);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if (kk == kLast && second)
+                    loads_done();
+                meet();
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int h = 0; h < kSteps; ++h)
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NI; ++j)
+                            acc[i][j] = mfma32<FMT>(fa[h][i], fb[h][j], acc[i][j]);
+                __builtin_amdgcn_s_setprio(0);
+                if (kk == kLast && !second)
+                    loads_done();
+                meet();
+            }
+            now ^= kStage;
+        }
+        if (!second)
+            meet();
+    }
+
+    // One wave of the block on a SIMD, which has nobody to take turns with: it reads
+    // the next fragments while the matrix cores have the last ones.
+    template <typename Load>
+    __device__ __forceinline__ void in_step(const unsigned char* lds, Load load, int ktiles)
+    {
         if (ktiles > 1)
             load(1, kStage);
         u32x4 fa[2][MI], fb[2][NI];
@@ -218,7 +295,6 @@ struct Product {
             }
             now ^= kStage;
         }
-        __syncthreads();
     }
 };
 
