@@ -319,3 +319,12 @@ def test_in_a_graph_and_on_a_stream():
 def test_larger_products(kind, T, V, D):
     x, w, y = inputs(T, V, D, kind)
     check(VocabCrossEntropy(V, D, T, TYPES[kind]), x, w, y, scale=16.0)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [8, 64, 72, 136, 200])
+def test_many_rows_of_few_values(D, kind):
+    """The largest tiles, over one to four steps of 64 values."""
+    T, V = 4096, 8192
+    x, w, y = inputs(T, V, D, kind)
+    check(VocabCrossEntropy(V, D, T, TYPES[kind]), x, w, y)
