@@ -315,3 +315,63 @@ def test_many_rows():
     assert torch.equal(z[0], z[-1]) and torch.equal(z[0], z[T // 2])
     del z
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind,T,V,tau", [("bf16", 2, 32000, 1.0), ("fp16", 200, 32000, 2.0), ("fp32", 256, 50021, 1.5),
+                                          ("bf16", 64, 200003, 1.0), ("fp16", 257, 3001, 1.0)])
+def test_few_rows_in_place_beside_rows_of_nothing(kind, T, V, tau):
+    """In the logits' place, rows of nothing but -infinity (the last among them) are not used, however the blocks run: the
+    bits of a call that writes elsewhere, and those within the bounds; the workspace serves the calls after it."""
+    k = 8
+    z, t, at = inputs(T, V, k, kind)
+    z[::3] = -INF
+    z[-1] = -INF
+    z[1:-1:5, :V - 1] = -INF                              # used for their last logit alone, if not for less
+    at[1:-1:5] = -1
+    at[1:-1:5, 0] = V - 1
+    op = TopLogitDistillation(V, k, 600, tau, coef=0.5)
+    plain, st = torch.empty_like(z), state(64.0)
+    op.loss_and_gradient(z, t, at, plain, scaler=st)
+    want = op.value.clone(), op.used.clone(), op.token_loss[:T].clone()
+    assert int(op.used) == int((z > -INF).any(1).sum())
+    for _ in range(3):
+        own = z.clone()
+        op.loss_and_gradient(own, t, at, own, scaler=st)
+        assert torch.equal(own, plain)
+        for a, b in zip((op.value, op.used, op.token_loss[:T]), want):
+            assert torch.equal(a, b)
+    check(op, z.clone(), t, at, scale=64.0)
+    r = check(op, own.copy_(z), t, at, scale=64.0, out=own)
+    assert not r["used"][::3].any() and not own[::3].any()
+    check(op, *inputs(600, V, k, kind)) if V < 4000 else None
+
+
+def test_few_rows_in_place_in_a_graph_and_with_more_blocks_than_rows(monkeypatch):
+    V, k = 5000, 6
+    for T in (1, 5):
+        z, t, at = inputs(T, V, k, "bf16")
+        if T > 1:
+            z[::2] = -INF
+        op = TopLogitDistillation(V, k, T, 1.0)
+        plain, own = torch.empty_like(z), z.clone()
+        op.loss_and_gradient(z, t, at, plain)
+        want = op.value.clone(), op.used.clone()
+        for blocks in ("1", "7"):
+            monkeypatch.setenv("DSZERO_GRID", blocks)
+            own.copy_(z)
+            op.loss_and_gradient(own, t, at, own)
+            assert torch.equal(own, plain) and torch.equal(op.value, want[0]) and torch.equal(op.used, want[1])
+        monkeypatch.delenv("DSZERO_GRID")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            op.loss_and_gradient(own, t, at, own)
+        for _ in range(3):
+            own.copy_(z)
+            op.value.fill_(-1.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(own, plain) and torch.equal(op.value, want[0]) and torch.equal(op.used, want[1])
+            own.copy_(z)
+            op.loss_and_gradient(own, t, at, own)
+            assert torch.equal(own, plain) and torch.equal(op.value, want[0])
