@@ -375,3 +375,29 @@ def test_few_rows_in_place_in_a_graph_and_with_more_blocks_than_rows(monkeypatch
             own.copy_(z)
             op.loss_and_gradient(own, t, at, own)
             assert torch.equal(own, plain) and torch.equal(op.value, want[0])
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("T,V,k,each", [(5001, 4096, 300, 2), (5001, 4096, 200, 2), (7001, 2100, 700, 3), (3001, 33000, 600, 2)])
+def test_long_lists_between_rows_that_are_left_out(T, V, k, each, kind):
+    """Blocks that go over several rows, some of them left out between two that are used, with entries in many waves: every
+    other place is one of 20, so that most entries share theirs."""
+    z, t, at = inputs(T, V, k, kind)
+    gen = generator(11)
+    at[:, ::2] = torch.randint(0, 20, (T, (k + 1) // 2), generator=gen, device=DEV, dtype=at.dtype)
+    mask = (torch.arange(T, device=DEV) % each != 1) & (torch.rand(T, generator=gen, device=DEV) < 0.8)
+    op = TopLogitDistillation(V, k, T, 2.0)
+    for accumulate in (False, True):
+        check(op, z, t, at, mask=mask, scale=256.0, accumulate=accumulate,
+              out=torch.randn(T, V, generator=gen, device=DEV).mul_(1e-3).to(z.dtype))
+
+
+def test_alternating_rows_of_one_block(monkeypatch):
+    """One block for all rows, the used ones two apart."""
+    monkeypatch.setenv("DSZERO_GRID", "1")
+    for T, V, k in ((61, 4096, 300), (61, 9000, 1000), (40, 32000, 700)):
+        z, t, at = inputs(T, V, k, "bf16")
+        at[:, 1::2] = at[:, :1]
+        mask = torch.arange(T, device=DEV) % 2 == 0
+        check(TopLogitDistillation(V, k, T, 1.0), z, t, at, mask=mask)
+        check(TopLogitDistillation(V, k, T, 1.0), z, t, at, mask=mask, out=torch.ones_like(z), accumulate=True)

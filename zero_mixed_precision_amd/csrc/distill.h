@@ -251,8 +251,10 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
     constexpr int kHold = NV == kTwice ? kTwiceHold : NV;
         __shared__ TopSum of_row[kWaves], of_teacher[kWaves];
     __shared__ float part[kWaves];
-    // the entries' places (-1: absent) and their shares, of two rows in turn; a
-    // lane's own: the student's logit there, and what the gradient held there
+    // the entries' places (-1: absent) and their shares, of two used rows in turn (a
+    // wave may read the last row's while another writes this one's; the row after
+    // writes behind this one's barriers, which a row that is not used does not have);
+    // a lane's own: the student's logit there, and what the gradient held there
     __shared__ __attribute__((aligned(16))) int32_t places[2][DS_MAX_TEACHER_LOGITS];
     __shared__ float shares[2][DS_MAX_TEACHER_LOGITS];
     __shared__ float of_logit[DS_MAX_TEACHER_LOGITS];
@@ -319,7 +321,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
                                                        static_cast<double>(s.tau) / used)
                                   : 0.0f;
     int turn = 0;
-    for (int64_t t = blockIdx.x; t < s.tokens; t += gridDim.x, turn ^= 1) {
+    for (int64_t t = blockIdx.x; t < s.tokens; t += gridDim.x) {
         const unsigned char* in = s.logits + t * s.stride * ES;
         unsigned char* out = GRAD ? s.grad + t * s.gs * ES : nullptr;
         const int64_t next = min(t + gridDim.x, s.tokens - 1);
@@ -334,6 +336,7 @@ __global__ __launch_bounds__(BLOCK) void distill_kernel(Distill s)
         int32_t* at = places[turn];
         float* share = shares[turn];
         if (on) {
+            turn ^= 1;                                         // for the next used row
             TopSum theirs{kNegInf, 0.0f};
             auto add_entry = [&](int64_t& p, float& x) {       // an absent one is -infinity, one past the vocabulary NaN
                 if (p < 0)
