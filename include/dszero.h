@@ -731,7 +731,7 @@ ds_status ds_balance_loss_grad(const ds_scaler* st_or_null, const void* logits, 
  * an unknown dt, gdt or index_bytes -> DS_ERR_DTYPE; else as in the conventions.
  */
 
-/* Device scratch of ds_dispatch_sort (0 for sizes out of range). */
+/* Device scratch of ds_dispatch_sort (0 for sizes out of range); what serves many tokens serves fewer. */
 size_t ds_dispatch_workspace_bytes(int64_t tokens, int32_t experts, int32_t k);
 
 /* offsets: int32[experts + 1], place and source: int32[tokens k], all written.

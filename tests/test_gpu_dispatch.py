@@ -128,6 +128,14 @@ def test_sort(T, k, E, index):
         check_sort(ExpertDispatch(E, k, T), choices(T, k, E, dropped=dropped, index=index))
 
 
+@pytest.mark.parametrize("k,most,fewer", [(1, 262145, 262144), (8, 40000, 32768), (2, 600001, 131072)])
+def test_sort_of_fewer_tokens_than_asked_for(k, most, fewer):
+    """Fewer pairs than the object is made for, in more blocks."""
+    op = ExpertDispatch(256, k, most)
+    for T in (most, fewer, fewer - 1, 5):
+        check_sort(op, choices(T, k, 256, seed=T, dropped=0.1))
+
+
 def test_sort_of_every_kind_of_choice():
     op = ExpertDispatch(4, 3, 500)
     check_sort(op, torch.full((200, 3), -1, device=DEV))                     # nothing left

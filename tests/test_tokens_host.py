@@ -159,6 +159,20 @@ def test_workspace_bytes():
     assert f(8192, 131072, 4096) < 2 * 8192 * 131072
 
 
+def test_a_sort_workspace_for_many_tokens_serves_fewer():
+    """An object's workspace is that of its largest call; a batch of fewer tokens must not be refused by it."""
+    f = _lib.ds_dispatch_workspace_bytes
+    for k in (1, 2, 3, 8, 16):
+        near = [p // k + d for p in (1024, 1 << 17, 1 << 18, 327680, 1 << 19, 1 << 20, 1 << 24, 1 << 30) for d in range(-2, 3)]
+        tokens = sorted({t for t in near + [int(1.07 ** n) for n in range(280)] if t * k < 1 << 31})
+        sizes = [f(t, 256, k) for t in tokens]
+        assert sizes == sorted(sizes)
+        # a row of counts for each block: chunks of 1024 pairs or, past 256 of them, 256 equal ones rounded up to 256
+        for t, size in zip(tokens, sizes):
+            chunk = -(-max(1024, -(-t * k // 256)) // 256) * 256
+            assert size >= 4 * 256 * max(1, -(-t * k // chunk))
+
+
 def over_stand_ins(monkeypatch, kind, stream=None, current=0, index=0):
     torch_ = Torch(current)
     library = Library(torch_)

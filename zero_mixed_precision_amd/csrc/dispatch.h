@@ -499,9 +499,12 @@ int64_t disp_blocks(int64_t pairs)
     return b < 1 ? 1 : b;
 }
 
+// No fewer than for fewer pairs, and never short: past kDispMaxBlocks chunks of
+// kDispChunk a longer chunk's rounding leaves fewer blocks than that.
 uint64_t disp_ws_bytes(int64_t pairs, int32_t experts)
 {
-    return 4 * static_cast<uint64_t>(disp_blocks(pairs)) * static_cast<uint64_t>(experts);
+    const int64_t chunks = (pairs + kDispChunk - 1) / kDispChunk;
+    return 4 * static_cast<uint64_t>(std::clamp(chunks, int64_t(1), kDispMaxBlocks)) * static_cast<uint64_t>(experts);
 }
 
 // Rows of `width` values, `stride` apart: sizes that the byte counts can hold.
