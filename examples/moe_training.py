@@ -25,11 +25,12 @@ class Gather(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, dispatch):
-        ctx.dispatch = dispatch
+        ctx.dispatch, ctx.sorts = dispatch, dispatch.sorts
         return dispatch.gather(x, x.new_zeros(x.shape[0] * dispatch.k, x.shape[1]))
 
     @staticmethod
     def backward(ctx, drows):
+        ctx.dispatch.check_sort(ctx.sorts)
         dx = drows.new_empty(drows.shape[0] // ctx.dispatch.k, drows.shape[1])
         return ctx.dispatch.gather_gradient(drows.contiguous(), dx), None
 
@@ -39,12 +40,13 @@ class Combine(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, rows, gates, dispatch):
-        ctx.dispatch = dispatch
+        ctx.dispatch, ctx.sorts = dispatch, dispatch.sorts
         ctx.save_for_backward(rows, gates)
         return dispatch.combine(rows, gates, rows.new_empty(gates.shape[0], rows.shape[1]))
 
     @staticmethod
     def backward(ctx, dy):
+        ctx.dispatch.check_sort(ctx.sorts)
         rows, gates = ctx.saved_tensors
         return *ctx.dispatch.combine_gradient(dy.contiguous(), rows, gates, torch.zeros_like(rows),
                                               torch.empty_like(gates)), None

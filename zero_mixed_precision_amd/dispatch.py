@@ -23,12 +23,15 @@ class ExpertDispatch(TokenOperator):
     """``sort()`` leaves, on the device: ``offsets`` (int32 [experts + 1]: the rows of expert e start at offsets[e]),
     ``place`` (int32 [max_tokens, k]: the row of each choice, -1 for a dropped one) and ``source`` (int32
     [max_tokens * k]: the choice t * k + j of each row, -1 behind the last one).  They are overwritten by the next sort(),
-    and the moves go by them: a layer whose gradient is still to come keeps its own object.
+    and the moves go by them: a layer whose gradient is still to come keeps its own object.  ``sorts`` counts them; a
+    backward pass hands the count of its forward to ``check_sort()``, which refuses it if another sort() came between.
 
     Calls of one object go by the same arrays: one after another, on one stream.
 
     ``stream``: a stream of its own (default: torch's current one).  The caller orders it after what writes the inputs,
     and what reads the results after it; the inputs may be freed as soon as a call returns."""
+
+    sorts = 0
 
     def __init__(self, num_experts: int, k: int, max_tokens: int, device="cuda", stream=None):
         self.E, self.k = int(num_experts), int(k)
@@ -64,9 +67,16 @@ class ExpertDispatch(TokenOperator):
         if rc:
             _lib._ok(rc, "ds_dispatch_sort")
         self.tokens = T
+        self.sorts += 1
         if self.stream is not None:
             self._keep(chosen)
         return self.offsets
+
+    def check_sort(self, sorts):
+        """Raises if the last sort() is not the one after which ``sorts`` was read."""
+        if sorts != self.sorts:
+            raise RuntimeError(f"sorted {self.sorts - sorts} more times since then: the order of these rows is gone (one "
+                               "ExpertDispatch for each layer and pass whose gradient is still to come)")
 
     def _pair(self, tokens_side, sorted_side, names):
         """Both sides of a move: (type, width, address and stride of the tokens' side, address, stride and rows of the
