@@ -328,3 +328,35 @@ def test_many_rows_of_few_values(D, kind):
     T, V = 4096, 8192
     x, w, y = inputs(T, V, D, kind)
     check(VocabCrossEntropy(V, D, T, TYPES[kind]), x, w, y)
+
+
+@pytest.mark.parametrize("kind,T,V,D", [("bf16", 2041, 7993, 1024), ("fp16", 2041, 7993, 1003), ("bf16", 3000, 7993, 1024),
+                                        ("fp16", 1999, 10007, 2048), ("bf16", 1021, 50021, 1003)])
+def test_the_largest_tiles_with_a_short_last_step(kind, T, V, D):
+    """Tiles of 256 x 256 for both gradients, over a vocabulary and used tokens that end inside a step of 64; W read in
+    place and packed."""
+    x, w, y = inputs(T, V, D, kind)
+    mask = torch.rand(T, generator=generator(2), device=DEV) < 0.97
+    mask[-1] = True
+    y[:5] = V - 1                                         # the last step's own columns
+    while int(mask.sum()) % 64 == 0:
+        mask[int(torch.nonzero(mask)[0])] = False
+    check(VocabCrossEntropy(V, D, T, TYPES[kind]), x, w, y, mask=mask, scale=16.0)
+    x[~mask] = math.nan
+    check(VocabCrossEntropy(V, D, T, TYPES[kind]), x, w, y, mask=mask, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("kind,T,V,D", [("fp16", 16, 1000, 64), ("bf16", 1021, 50021, 1003), ("fp16", 4096, 32000, 512),
+                                        ("bf16", 4096, 8192, 1024)])
+def test_a_call_repeats_its_bits(kind, T, V, D):
+    """Each of the three sides of tiles, with other work on the GPU between the calls."""
+    x, w, y = inputs(T, V, D, kind)
+    op = VocabCrossEntropy(V, D, T, TYPES[kind])
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    first = None
+    for turn in range(4):
+        op.loss_and_gradient(x, w, y, dx, dw)
+        got = [a.clone() for a in (dx, dw, op.token_loss, op.value)]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+        x.float() @ x.float()[:turn + 1].t()
