@@ -22,9 +22,11 @@ from .operands import TokenOperator, token_count
 class ExpertDispatch(TokenOperator):
     """``sort()`` leaves, on the device: ``offsets`` (int32 [experts + 1]: the rows of expert e start at offsets[e]),
     ``place`` (int32 [max_tokens, k]: the row of each choice, -1 for a dropped one) and ``source`` (int32
-    [max_tokens * k]: the choice t * k + j of each row, -1 behind the last one).  They are overwritten by the next sort(),
-    and the moves go by them: a layer whose gradient is still to come keeps its own object.  ``sorts`` counts them; a
-    backward pass hands the count of its forward to ``check_sort()``, which refuses it if another sort() came between.
+    [max_tokens * k]: the choice t * k + j of each row, -1 behind the last one).  The sorted tokens are the first of
+    ``place``, their tokens * k choices the first of ``source``; what lies behind is of earlier calls.  They are
+    overwritten by the next sort(), and the moves go by them: a layer whose gradient is still to come keeps its own object.
+    ``sorts`` counts the calls of sort(); a backward pass hands the count of its forward to ``check_sort()``, which raises
+    if another sort() came between.
 
     Calls of one object go by the same arrays: one after another, on one stream.
 

@@ -18,8 +18,9 @@ from .operands import TokenOperator, token_count
 
 class TopLogitDistillation(TokenOperator):
     """``loss()`` and ``loss_and_gradient()`` leave, on the device: ``value`` (fp32 scalar: coef times the mean over used
-    rows), ``token_loss`` (fp32 [max_tokens], 0 for rows that are not used) and ``used`` (int32 scalar: rows that
-    counted).  They are overwritten by the next call.
+    rows), ``token_loss`` (fp32 [max_tokens], of which the call's tokens are the first: 0 for rows that are not used) and
+    ``used`` (int32 scalar: rows that counted).  They are overwritten by the next call; what ``token_loss`` holds behind its
+    tokens is of earlier ones.
 
     ``k``: teacher's entries per row (1..1024; rows may have fewer: a negative place is an absent entry).
 

@@ -18,8 +18,9 @@ from .operands import TokenOperator, token_count
 
 class VocabCrossEntropy(TokenOperator):
     """``loss()`` and ``loss_and_gradient()`` leave, on the device: ``value`` (fp32 scalar: coef times the mean over used
-    rows), ``token_loss`` (fp32 [max_tokens], 0 for rows that are not used) and ``used`` (int32 scalar: rows that
-    counted).  They are overwritten by the next call.
+    rows), ``token_loss`` (fp32 [max_tokens], of which the call's tokens are the first: 0 for rows that are not used) and
+    ``used`` (int32 scalar: rows that counted).  They are overwritten by the next call; what ``token_loss`` holds behind its
+    tokens is of earlier ones.
 
     ``dtype``: torch.float16 or torch.bfloat16, of hidden states and weight.  The workspace is allocated here, once.
 
